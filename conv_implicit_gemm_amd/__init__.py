@@ -17,7 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libox.so")
 
 OX_OK, OX_ERR_INVALID_ARG, OX_ERR_SHAPE, OX_ERR_UNSUPPORTED, OX_ERR_HIP = 0, 1, 2, 3, 4
-OX_F32, OX_BF16, OX_I8, OX_I32 = 0, 1, 2, 3
+OX_F32, OX_BF16, OX_I8, OX_I32, OX_F8E4M3 = 0, 1, 2, 3, 4
 ACT = {"none": 0, "relu": 1, "relu6": 2, "gelu": 3}
 STATUS_NAMES = {0: "OX_OK", 1: "OX_ERR_INVALID_ARG", 2: "OX_ERR_SHAPE",
                 3: "OX_ERR_UNSUPPORTED", 4: "OX_ERR_HIP"}
@@ -30,7 +30,8 @@ EXPORTS = ("ox_matmul_batched", "ox_gemm_fused", "ox_conv2d_fused", "ox_conv2d_i
            "ox_conv2d_fused_res", "ox_batchnorm_act", "ox_maxpool2d", "ox_global_avgpool",
            "ox_int8_prepare_ex", "ox_dynamic_quantize_workspace_bytes", "ox_dynamic_quantize_linear",
            "ox_matmul_nbits", "ox_gemm_workspace_bytes", "ox_gemm_fused_ws",
-           "ox_static_scratch_bytes", "ox_conv2d_fused_static")
+           "ox_static_scratch_bytes", "ox_conv2d_fused_static", "ox_quantize_fp8", "ox_gemm_fp8",
+           "ox_gemm_grouped", "ox_gemm_grouped_fp8")
 
 
 class OxError(RuntimeError):
@@ -81,6 +82,10 @@ def _load():
         "ox_gemm_workspace_bytes": (C.c_size_t, [I, I64, I64, I64]),
         "ox_gemm_fused_ws": (I, [I, I64, I64, I64, I, I, F, P, P, F, P, I, P, P, C.c_size_t, P]),
         "ox_dynamic_quantize_linear": (I, [I64, P, P, P, P, P, C.c_size_t, P]),
+        "ox_quantize_fp8": (I, [I, I64, I64, P, I64, P, I, P, P, P]),
+        "ox_gemm_fp8": (I, [I, I64, I64, I64, P, P, P, P, P, I, P, P]),
+        "ox_gemm_grouped": (I, [I, I64, I64, I64, I64, I, P, P, P, P, I, P, P]),
+        "ox_gemm_grouped_fp8": (I, [I, I64, I64, I64, I64, P, P, P, P, P, P, I, P, P]),
         "ox_last_error": (C.c_char_p, []),
         "ox_version": (C.c_char_p, []),
     }
@@ -288,6 +293,130 @@ def ox_matmul_nbits(A, B, scales, K, zero_points=None, bias=None, Y=None, stream
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
     _check(lib.ox_matmul_nbits(OX_BF16, M, N, K, 4, 32, _ptr(A), _ptr(B), _ptr(scales),
                                _ptr(zero_points), _ptr(bias), _ptr(Y), _stream(stream)))
+    return Y
+
+
+def _need(ok, fmt, *args):
+    if not ok:
+        raise ValueError(fmt % args)
+
+
+def _operands(*named):
+    """Every tensor dense and on the first one's device; shapes come out of the
+    tensors, so the C call cannot see a mismatch between them."""
+    dev = named[0][0].device
+    for t, name in named:
+        if t is None:
+            continue
+        _dense(t, name)
+        _need(t.device == dev, "%s is on %s, not %s", name, t.device, dev)
+
+
+def _f8_operands(A, a_scales, B, b_scales, K, rows, b_shape):
+    torch = _torch()
+    f8 = (torch.float8_e4m3fn, torch.uint8)
+    if A.dtype not in f8 or B.dtype not in f8:
+        raise TypeError("A and B must be float8_e4m3fn (or uint8 codes), not %s and %s" % (A.dtype, B.dtype))
+    if a_scales.dtype != torch.float32 or b_scales.dtype != torch.float32:
+        raise TypeError("a_scales and b_scales must be float32")
+    kb = -(-K // 128)
+    _need(tuple(a_scales.shape) == (kb, rows), "a_scales is %s, not [ceil(K/128), rows] = %s",
+          tuple(a_scales.shape), (kb, rows))
+    _need(tuple(b_scales.shape) == b_shape + (kb,), "b_scales is %s, not %s", tuple(b_scales.shape), b_shape + (kb,))
+
+
+def _epilogue(Y, bias, shape, bias_shape, dtype, device):
+    torch = _torch()
+    if Y is None:
+        Y = torch.empty(shape, dtype=dtype, device=device)
+    _need(tuple(Y.shape) == shape, "Y is %s, not %s", tuple(Y.shape), shape)
+    if bias is not None:
+        _need(tuple(bias.shape) == bias_shape, "bias is %s, not %s", tuple(bias.shape), bias_shape)
+        if bias.dtype != Y.dtype:
+            raise TypeError("bias is %s, Y %s" % (bias.dtype, Y.dtype))
+    return Y
+
+
+def ox_quantize_fp8(X, index=None, block_rows=1, Q=None, scales=None, stream=None):
+    """e4m3 codes and fp32 block scales of a dense device matrix X (float32 or
+    bfloat16) [rows, K].  block_rows=1: a scale per row and 128 columns, scales
+    [ceil(K/128), R]; block_rows=128: a scale per 128 x 128, scales
+    [ceil(R/128), ceil(K/128)].  index (int32 [R], block_rows=1 only): row r of
+    the result is row index[r] of X.  Returns (Q float8_e4m3fn [R, K], scales)."""
+    torch = _torch()
+    rows, K = X.shape
+    R = rows if index is None else index.numel()
+    kb = -(-K // 128)
+    shape = (kb, R) if block_rows == 1 else (-(-R // 128), kb)
+    if index is not None and index.dtype != torch.int32:
+        raise TypeError("index must be int32")
+    if Q is None:
+        Q = torch.empty((R, K), dtype=torch.float8_e4m3fn, device=X.device)
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=X.device)
+    _operands((X, "X"), (index, "index"), (Q, "Q"), (scales, "scales"))
+    _need(tuple(Q.shape) == (R, K) and Q.element_size() == 1, "Q is not one byte [%d, %d]", R, K)
+    _need(tuple(scales.shape) == shape and scales.dtype == torch.float32, "scales is not float32 %s", shape)
+    _check(lib.ox_quantize_fp8(_dtype_code(X), rows, K, _ptr(X), R, _ptr(index), block_rows, _ptr(Q),
+                               _ptr(scales), _stream(stream)))
+    return Q, scales
+
+
+def ox_gemm_fp8(A, a_scales, B, b_scales, bias=None, act="none", Y=None, out_dtype=None, stream=None):
+    """Y [M, N] = act(A B^T + bias) for e4m3 A [M, K] and B [N, K] with block
+    scales (as ox_quantize_fp8 makes them with block_rows 1 and 128).  Y's type
+    (out_dtype, default bfloat16, or float32) is the bias's too."""
+    torch = _torch()
+    M, K = A.shape
+    N = B.shape[0]
+    _need(B.shape[1] == K, "B has %d columns, A %d", B.shape[1], K)
+    _f8_operands(A, a_scales, B, b_scales, K, M, (-(-N // 128),))
+    Y = _epilogue(Y, bias, (M, N), (N,), out_dtype or torch.bfloat16, A.device)
+    _operands((A, "A"), (a_scales, "a_scales"), (B, "B"), (b_scales, "b_scales"), (bias, "bias"), (Y, "Y"))
+    _check(lib.ox_gemm_fp8(_dtype_code(Y), M, N, K, _ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales),
+                           _ptr(bias), ACT[act], _ptr(Y), _stream(stream)))
+    return Y
+
+
+def _offsets(offsets, E):
+    if offsets.dtype != _torch().int32:
+        raise TypeError("offsets must be int32")
+    _need(tuple(offsets.shape) == (E + 1,), "offsets is %s, not [experts + 1] = (%d,)", tuple(offsets.shape), E + 1)
+
+
+def ox_gemm_grouped(A, B, offsets, bias=None, transB=True, act="none", Y=None, stream=None):
+    """Rows offsets[e] .. offsets[e+1]-1 of A [T, K] times expert e's weights:
+    B [E, N, K] (transB) or [E, K, N]; offsets int32 [E+1] on the device; bias
+    [E, N].  float32 or bfloat16 throughout.  Rows outside every expert's are
+    zero in Y [T, N]."""
+    T, K = A.shape
+    E, N, Kb = B.shape if transB else (B.shape[0], B.shape[2], B.shape[1])
+    _need(Kb == K, "B's reduction is %d, A's %d", Kb, K)
+    _offsets(offsets, E)
+    Y = _epilogue(Y, bias, (T, N), (E, N), A.dtype, A.device)
+    if B.dtype != A.dtype or Y.dtype != A.dtype:
+        raise TypeError("A is %s, B %s, Y %s" % (A.dtype, B.dtype, Y.dtype))
+    _operands((A, "A"), (B, "B"), (offsets, "offsets"), (bias, "bias"), (Y, "Y"))
+    _check(lib.ox_gemm_grouped(_dtype_code(A), T, N, K, E, int(bool(transB)), _ptr(A), _ptr(B), _ptr(offsets),
+                               _ptr(bias), ACT[act], _ptr(Y), _stream(stream)))
+    return Y
+
+
+def ox_gemm_grouped_fp8(A, a_scales, B, b_scales, offsets, bias=None, act="none", Y=None, out_dtype=None,
+                        stream=None):
+    """ox_gemm_grouped for e4m3 operands with block scales: A [T, K], a_scales
+    [ceil(K/128), T], B [E, N, K], b_scales [E, ceil(N/128), ceil(K/128)]."""
+    torch = _torch()
+    T, K = A.shape
+    E, N, Kb = B.shape
+    _need(Kb == K, "B's reduction is %d, A's %d", Kb, K)
+    _offsets(offsets, E)
+    _f8_operands(A, a_scales, B, b_scales, K, T, (E, -(-N // 128)))
+    Y = _epilogue(Y, bias, (T, N), (E, N), out_dtype or torch.bfloat16, A.device)
+    _operands((A, "A"), (a_scales, "a_scales"), (B, "B"), (b_scales, "b_scales"), (offsets, "offsets"),
+              (bias, "bias"), (Y, "Y"))
+    _check(lib.ox_gemm_grouped_fp8(_dtype_code(Y), T, N, K, E, _ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales),
+                                   _ptr(offsets), _ptr(bias), ACT[act], _ptr(Y), _stream(stream)))
     return Y
 
 

@@ -62,6 +62,8 @@ bool too_big(int64_t a, int64_t b = 1, int64_t c = 1, int64_t d = 1) {
 
 int esize(int dt) { return dt == DT_F32 || dt == DT_I32 ? 4 : dt == DT_BF16 ? 2 : 1; }
 
+bool aligned_to(const void* p, int n) { return ((uintptr_t)p) % (uintptr_t)n == 0; }
+
 bool aligned16(const void* p) { return (((uintptr_t)p) & 15) == 0; }
 
 const char* act_name(int a) {
@@ -1004,6 +1006,114 @@ ox_status ox_matmul_nbits(ox_dtype t, int64_t M, int64_t N, int64_t K, int bits,
   a.Y = Y;
   a.ldy = N;
   return hip_result(fn, launch_matmul_nbits(a, stream));
+}
+
+ox_status ox_quantize_fp8(ox_dtype t, int64_t rows, int64_t K, const void* X, int64_t R,
+                          const int32_t* index, int block_rows, uint8_t* Q, float* scales, void* stream) {
+  const char* fn = "ox_quantize_fp8";
+  ox_status st = check_float_dt(fn, t);
+  if (st) return st;
+  if (rows < 0 || K < 0 || R < 0)
+    return fail(OX_ERR_SHAPE, "%s: rows=%lld, K=%lld or R=%lld is negative", fn, (long long)rows, (long long)K,
+                (long long)R);
+  if (block_rows != 1 && block_rows != 128)
+    return fail(OX_ERR_UNSUPPORTED, "%s: block_rows=%d (1 or 128)", fn, block_rows);
+  if (index && block_rows != 1) return fail(OX_ERR_UNSUPPORTED, "%s: index needs block_rows = 1", fn);
+  if (!index && R != rows)
+    return fail(OX_ERR_SHAPE, "%s: R=%lld but rows=%lld without an index", fn, (long long)R, (long long)rows);
+  if (too_big(rows, K) || too_big(R, K)) return fail(OX_ERR_UNSUPPORTED, "%s: a tensor holds 2^31 elements or more", fn);
+  if (R == 0 || K == 0) return ok();
+  if ((!X && rows > 0) || !Q || !scales) return fail(OX_ERR_INVALID_ARG, "%s: X, Q or scales is NULL", fn);
+  if (!aligned_to(X, esize(t)) || !aligned_to(scales, 4) || !aligned_to(index, 4))
+    return fail(OX_ERR_INVALID_ARG, "%s: X, scales or index is not aligned to its element size", fn);
+  QuantF8Args a;
+  a.rows = (int)rows;
+  a.K = (int)K;
+  a.R = (int)R;
+  a.dt = t;
+  a.X = X;
+  a.index = index;
+  a.block_rows = block_rows;
+  a.Q = Q;
+  a.scales = scales;
+  a.vec = aligned16(X) && aligned_to(Q, 8) && K % 16 == 0;
+  return hip_result(fn, launch_quantize_fp8(a, stream));
+}
+
+namespace {
+
+// The shared half of the three products below: sizes, pointers, alignment.
+ox_status expert_call(const char* fn, int dt, ox_dtype y_type, int64_t T, int64_t N, int64_t K, int64_t E,
+                      int transB, const void* A, const float* a_scales, const void* B, const float* b_scales,
+                      const int32_t* offsets, const void* bias, ox_act act, void* Y, void* stream) {
+  ox_status st = check_float_dt(fn, y_type);
+  if (st) return st;
+  st = check_act(fn, act);
+  if (st) return st;
+  if (T < 0 || N < 0 || K < 0 || E < 0)
+    return fail(OX_ERR_SHAPE, "%s: a negative size (rows %lld, N %lld, K %lld, experts %lld)", fn, (long long)T,
+                (long long)N, (long long)K, (long long)E);
+  if (T > 0 && E == 0) return fail(OX_ERR_SHAPE, "%s: rows but no experts", fn);
+  if (too_big(T, K) || too_big(T, N) || too_big(E, N, K) || too_big(E, N) || E >= ((int64_t)1 << 30))
+    return fail(OX_ERR_UNSUPPORTED, "%s: a tensor holds 2^31 elements or more", fn);
+  if (T == 0 || N == 0) return ok();
+  if (!Y) return fail(OX_ERR_INVALID_ARG, "%s: Y is NULL", fn);
+  if (K > 0 && (!A || !B)) return fail(OX_ERR_INVALID_ARG, "%s: A or B is NULL", fn);
+  if (dt == DT_F8 && K > 0 && (!a_scales || !b_scales))
+    return fail(OX_ERR_INVALID_ARG, "%s: a_scales or b_scales is NULL", fn);
+  if (!aligned_to(A, esize(dt)) || !aligned_to(B, esize(dt)) || !aligned_to(bias, esize(y_type)) ||
+      !aligned_to(Y, esize(y_type)) || !aligned_to(a_scales, 4) || !aligned_to(b_scales, 4) || !aligned_to(offsets, 4))
+    return fail(OX_ERR_INVALID_ARG, "%s: a pointer is not aligned to its element size", fn);
+  ExpertArgs a;
+  a.T = (int)T;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.E = (int)E;
+  a.A = A;
+  a.sa = a_scales;
+  a.B = B;
+  a.sb = b_scales;
+  a.offsets = offsets;
+  a.bias = bias;
+  a.Y = Y;
+  a.dt = dt;
+  a.out_dt = y_type;
+  a.act = act;
+  a.kn = !transB;
+  const int64_t rowb = K * esize(dt), colb = N * esize(dt);
+  // (tile offsets: up to 256 rows of K, or 64 rows of N)
+  a.vec = aligned16(A) && aligned16(B) && rowb % 16 == 0 && rowb < (1 << 23) &&
+          (transB || (colb % 16 == 0 && colb < (1 << 23)));
+  a.y_vec = aligned16(Y) && N * esize(y_type) % 16 == 0;
+  return hip_result(fn, dt == DT_F8 ? launch_expert_fp8(a, stream)
+                        : dt == DT_BF16 ? launch_expert_bf16(a, stream)
+                                        : launch_expert_f32(a, stream));
+}
+
+}  // namespace
+
+ox_status ox_gemm_fp8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const uint8_t* A,
+                      const float* a_scales, const uint8_t* B, const float* b_scales, const void* bias,
+                      ox_act act, void* Y, void* stream) {
+  return expert_call("ox_gemm_fp8", DT_F8, y_type, M, N, K, 1, 1, A, a_scales, B, b_scales, nullptr, bias, act, Y,
+                     stream);
+}
+
+ox_status ox_gemm_grouped(ox_dtype t, int64_t T, int64_t N, int64_t K, int64_t E, int transB,
+                          const void* A, const void* B, const int32_t* offsets, const void* bias,
+                          ox_act act, void* Y, void* stream) {
+  const char* fn = "ox_gemm_grouped";
+  if (T > 0 && N > 0 && !offsets) return fail(OX_ERR_INVALID_ARG, "%s: offsets is NULL", fn);
+  return expert_call(fn, t, t, T, N, K, E, transB, A, nullptr, B, nullptr, offsets, bias, act, Y, stream);
+}
+
+ox_status ox_gemm_grouped_fp8(ox_dtype y_type, int64_t T, int64_t N, int64_t K, int64_t E,
+                              const uint8_t* A, const float* a_scales, const uint8_t* B,
+                              const float* b_scales, const int32_t* offsets, const void* bias,
+                              ox_act act, void* Y, void* stream) {
+  const char* fn = "ox_gemm_grouped_fp8";
+  if (T > 0 && N > 0 && !offsets) return fail(OX_ERR_INVALID_ARG, "%s: offsets is NULL", fn);
+  return expert_call(fn, DT_F8, y_type, T, N, K, E, 1, A, a_scales, B, b_scales, offsets, bias, act, Y, stream);
 }
 
 size_t ox_dynamic_quantize_workspace_bytes(void) { return dynq_workspace_bytes(); }

@@ -10,7 +10,7 @@
 namespace ox {
 
 // storage types (same values as ox_dtype)
-enum Dt : int { DT_F32 = 0, DT_BF16 = 1, DT_I8 = 2, DT_I32 = 3 };
+enum Dt : int { DT_F32 = 0, DT_BF16 = 1, DT_I8 = 2, DT_I32 = 3, DT_F8 = 4 };
 
 // activations (same values as ox_act)
 enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_RELU6 = 2, ACT_GELU = 3 };
@@ -277,6 +277,41 @@ struct NBitsArgs {
   int64_t ldy;
 };
 int launch_matmul_nbits(const NBitsArgs& a, void* stream);
+
+// Products with rows grouped by expert (offsets non-null) or with one group
+// of all rows, and their e4m3 form with block scales.
+struct ExpertArgs {
+  int T, N, K, E;          // rows, columns of Y, reduction, experts
+  const void* A;           // [T, K]
+  const float* sa;         // e4m3: scales [ceil(K/128)][T]
+  const void* B;           // [E][N, K], or [E][K, N] when kn
+  const float* sb;         // e4m3: scales [E][ceil(N/128)][ceil(K/128)]
+  const int32_t* offsets;  // DEVICE [E + 1], or null
+  const void* bias;        // [E][N] of Y's type, or null
+  void* Y;                 // [T, N]
+  int dt;                  // DT_F32, DT_BF16 or DT_F8
+  int out_dt;              // DT_F32 or DT_BF16
+  int act;
+  int kn;                  // weights are [K, N]
+  int vec;                 // A and B: every row starts on 16 bytes, and offsets inside a tile fit 32 bits
+  int y_vec;               // Y: rows start on 16 bytes and hold whole 16-byte pieces
+};
+int launch_expert_f32(const ExpertArgs& a, void* stream);
+int launch_expert_bf16(const ExpertArgs& a, void* stream);
+int launch_expert_fp8(const ExpertArgs& a, void* stream);
+
+// Quantisation to e4m3 with one fp32 scale per 1 x 128 or 128 x 128 block.
+struct QuantF8Args {
+  int rows, K, R;          // rows of X and their length, rows of Q
+  int dt;                  // X: DT_F32 or DT_BF16
+  const void* X;
+  const int32_t* index;    // DEVICE [R]: the row of X behind each row of Q, or null (R == rows)
+  int block_rows;          // 1 or 128
+  uint8_t* Q;              // [R, K]
+  float* scales;           // [ceil(K/128)][R], or [ceil(R/128)][ceil(K/128)]
+  int vec;                 // rows of X and Q take 16- and 8-byte accesses
+};
+int launch_quantize_fp8(const QuantF8Args& a, void* stream);
 
 size_t dynq_workspace_bytes();
 int launch_dynamic_quantize(int64_t n, const float* X, uint8_t* Y, float* y_scale, uint8_t* y_zp,

@@ -51,7 +51,7 @@ typedef enum {
   OX_ERR_HIP = 4            /* a HIP runtime call failed */
 } ox_status;
 
-typedef enum { OX_F32 = 0, OX_BF16 = 1, OX_I8 = 2, OX_I32 = 3 } ox_dtype;
+typedef enum { OX_F32 = 0, OX_BF16 = 1, OX_I8 = 2, OX_I32 = 3, OX_F8E4M3 = 4 } ox_dtype;
 
 /* Fused activations.  ReLU = max(v,0); ReLU6 = min(max(v,0),6) (the clamp the
  * Kyanite README "Optimizer" section merges relu/min/max into); GELU is the
@@ -376,6 +376,68 @@ size_t ox_dynamic_quantize_workspace_bytes(void);
 ox_status ox_dynamic_quantize_linear(int64_t n, const float* X, uint8_t* Y, float* y_scale,
                                      uint8_t* y_zp, void* workspace, size_t workspace_bytes,
                                      void* stream);
+
+/* ------------- 8-bit floating point with block scales, experts' products */
+
+/* Quantise X to e4m3 (ONNX FLOAT8E4M3FN codes: 4 exponent and 3 mantissa
+ * bits, largest value 448, no infinity) with one fp32 scale per block of 128
+ * along K:
+ *   m = max(|x| over the block's finite values, 2^-100)
+ *   scale = m / 448,  Q = e4m3(x * (448 / m)), round half to even,
+ * so that X is about Q * scale.  A NaN gives a NaN code, an infinity the
+ * code of +-448 (ONNX QuantizeLinear with saturation); neither moves the
+ * scale.
+ * t: the type of X, OX_F32 or OX_BF16; X: DEVICE [rows, K].
+ * block_rows = 1: a scale per row and block of 128 (activations), scales
+ *   DEVICE fp32 [ceil(K/128)][R], k-block first (the order in which a
+ *   product reads them);
+ * block_rows = 128: a scale per 128 rows x 128 (weights), scales
+ *   [ceil(R/128)][ceil(K/128)].
+ * index: DEVICE int32 [R] or NULL (then R == rows; required for block_rows =
+ *   128): row r of Q is row index[r] of X, e.g. the tokens in their experts'
+ *   order.  An index outside [0, rows) gives a row of zeros.
+ * Q: DEVICE uint8 [R, K].  Rows of a multiple of 16 elements in 16-byte
+ * aligned X and 8-byte aligned Q take the vector path. */
+ox_status ox_quantize_fp8(ox_dtype t, int64_t rows, int64_t K, const void* X, int64_t R,
+                          const int32_t* index, int block_rows, uint8_t* Q, float* scales, void* stream);
+
+/* Product of e4m3 matrices with block scales and a fused epilogue:
+ *   Y[m,n] = act( sum_b a_scales[b][m] * b_scales[n/128][b]
+ *                       * sum_{k in block b} A[m,k] * B[n,k]  + bias[n] )
+ * A: DEVICE e4m3 [M, K], a_scales DEVICE fp32 [ceil(K/128)][M];
+ * B: DEVICE e4m3 [N, K], b_scales DEVICE fp32 [ceil(N/128)][ceil(K/128)]
+ * (both as ox_quantize_fp8 writes them).  Products and sums in fp32, one
+ * rounding to y_type (OX_F32 or OX_BF16), the type of Y DEVICE [M, N] and of
+ * bias DEVICE [N] (or NULL).  NaN codes give NaN results.  With few rows the
+ * weights are streamed once and K is divided over the waves of a block; the
+ * order of every sum depends on the sizes alone. */
+ox_status ox_gemm_fp8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const uint8_t* A,
+                      const float* a_scales, const uint8_t* B, const float* b_scales, const void* bias,
+                      ox_act act, void* Y, void* stream);
+
+/* Products grouped by expert: rows offsets[e] .. offsets[e+1]-1 of A belong
+ * to expert e (none, when the two are equal), and
+ *   Y[m,:] = act( A[m,:] * B[e]' + bias[e] )
+ * with B[e]' = B[e]^T when transB (B stored [E][N, K]) else B[e] ([E][K, N]).
+ * t: OX_F32 or OX_BF16, the type of A, B, bias and Y; fp32 accumulation.
+ * A: DEVICE [T, K]; B: DEVICE [E, ...]; bias: DEVICE [E][N] or NULL; Y:
+ * DEVICE [T, N].  offsets: DEVICE int32 [E+1], not decreasing, in [0, T]:
+ * only the device reads them, so a router's kernels can write them and the
+ * call can be captured.  Rows before offsets[0] and from offsets[E] on (the
+ * unused end of a buffer of fixed capacity) are set to zero.  Offsets that
+ * decrease or leave [0, T] leave Y undefined, but nothing outside the
+ * tensors is touched. */
+ox_status ox_gemm_grouped(ox_dtype t, int64_t T, int64_t N, int64_t K, int64_t E, int transB,
+                          const void* A, const void* B, const int32_t* offsets, const void* bias,
+                          ox_act act, void* Y, void* stream);
+
+/* The same for e4m3 operands with block scales: A, a_scales and the result
+ * as for ox_gemm_fp8 (M = T), B DEVICE e4m3 [E][N, K], b_scales DEVICE fp32
+ * [E][ceil(N/128)][ceil(K/128)], bias DEVICE [E][N] of y_type or NULL. */
+ox_status ox_gemm_grouped_fp8(ox_dtype y_type, int64_t T, int64_t N, int64_t K, int64_t E,
+                              const uint8_t* A, const float* a_scales, const uint8_t* B,
+                              const float* b_scales, const int32_t* offsets, const void* bias,
+                              ox_act act, void* Y, void* stream);
 
 /* The message of the last failing call on this thread ("" if none). */
 const char* ox_last_error(void);
