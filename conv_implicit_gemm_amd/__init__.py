@@ -119,15 +119,20 @@ def _torch():
     return torch
 
 
+_DTYPE_CODES = {}
+
+
 def _dtype_code(t):
-    torch = _torch()
-    # uint8 tensors travel as bytes through the int8 calls: the parameter
-    # block (ox_int8_prepare(..., x_unsigned / y_unsigned)) says how to read them
-    m = {torch.float32: OX_F32, torch.bfloat16: OX_BF16, torch.int8: OX_I8, torch.uint8: OX_I8,
-         torch.int32: OX_I32}
-    if t.dtype not in m:
+    if not _DTYPE_CODES:
+        torch = _torch()
+        # uint8 tensors travel as bytes through the int8 calls: the parameter
+        # block (ox_int8_prepare(..., x_unsigned / y_unsigned)) says how to read them
+        _DTYPE_CODES.update({torch.float32: OX_F32, torch.bfloat16: OX_BF16, torch.int8: OX_I8,
+                             torch.uint8: OX_I8, torch.int32: OX_I32})
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
         raise TypeError("unsupported tensor dtype %s" % t.dtype)
-    return m[t.dtype]
+    return code
 
 
 def _ptr(t):
@@ -296,45 +301,57 @@ def ox_matmul_nbits(A, B, scales, K, zero_points=None, bias=None, Y=None, stream
     return Y
 
 
-def _need(ok, fmt, *args):
-    if not ok:
-        raise ValueError(fmt % args)
+# The calls below serve single tokens, where a kernel takes a few microseconds
+# and a call has to cost no more: the checks are written out flat, with the
+# words for a refusal only made when there is one, and the stream is asked for
+# as a raw handle (0.1 us; a current_stream() object takes 2.8 us).
+
+_F8 = []          # torch's types, looked up once: (float8_e4m3fn, uint8, float32, int32, raw stream function)
 
 
-def _operands(*named):
-    """Every tensor dense and on the first one's device; shapes come out of the
-    tensors, so the C call cannot see a mismatch between them."""
-    dev = named[0][0].device
-    for t, name in named:
-        if t is None:
-            continue
-        _dense(t, name)
-        _need(t.device == dev, "%s is on %s, not %s", name, t.device, dev)
+def _types():
+    if not _F8:
+        torch = _torch()
+        _F8.extend((torch.float8_e4m3fn, torch.uint8, torch.float32, torch.int32, torch._C._cuda_getCurrentRawStream))
+    return _F8
 
 
-def _f8_operands(A, a_scales, B, b_scales, K, rows, b_shape):
+def _shape_error(name, t, want):
+    return ValueError("%s is %s, not %s" % (name, tuple(t.shape), want))
+
+
+def _refuse_memory(names, *tensors):
+    """The refusal of tensors that are not all dense and on the first one's GPU."""
+    dev = tensors[0].get_device()
+    for name, t in zip(names, tensors):
+        if t is not None and not t.is_contiguous():
+            return ValueError("%s must be contiguous (dense row-major)" % name)
+        if t is not None and (dev < 0 or t.get_device() != dev):
+            return ValueError("%s must be on the GPU of %s, not on %s" % (name, names[0], t.device))
+    return ValueError("unusable tensors")
+
+
+def _refuse_f8(A, a_scales, B, b_scales, want_a, want_b):
+    f8, u8, f32 = _types()[:3]
+    if A.dtype not in (f8, u8) or B.dtype not in (f8, u8):
+        return TypeError("A and B must be float8_e4m3fn (or uint8 codes), not %s and %s" % (A.dtype, B.dtype))
+    if a_scales.dtype != f32 or b_scales.dtype != f32:
+        return TypeError("a_scales and b_scales must be float32")
+    if a_scales.shape != want_a:
+        return _shape_error("a_scales", a_scales, want_a)
+    return _shape_error("b_scales", b_scales, want_b)
+
+
+def _new_result(shape, dtype, device):
     torch = _torch()
-    f8 = (torch.float8_e4m3fn, torch.uint8)
-    if A.dtype not in f8 or B.dtype not in f8:
-        raise TypeError("A and B must be float8_e4m3fn (or uint8 codes), not %s and %s" % (A.dtype, B.dtype))
-    if a_scales.dtype != torch.float32 or b_scales.dtype != torch.float32:
-        raise TypeError("a_scales and b_scales must be float32")
-    kb = -(-K // 128)
-    _need(tuple(a_scales.shape) == (kb, rows), "a_scales is %s, not [ceil(K/128), rows] = %s",
-          tuple(a_scales.shape), (kb, rows))
-    _need(tuple(b_scales.shape) == b_shape + (kb,), "b_scales is %s, not %s", tuple(b_scales.shape), b_shape + (kb,))
+    return torch.empty(shape, dtype=dtype or torch.bfloat16, device=device)
 
 
-def _epilogue(Y, bias, shape, bias_shape, dtype, device):
-    torch = _torch()
-    if Y is None:
-        Y = torch.empty(shape, dtype=dtype, device=device)
-    _need(tuple(Y.shape) == shape, "Y is %s, not %s", tuple(Y.shape), shape)
-    if bias is not None:
-        _need(tuple(bias.shape) == bias_shape, "bias is %s, not %s", tuple(bias.shape), bias_shape)
-        if bias.dtype != Y.dtype:
-            raise TypeError("bias is %s, Y %s" % (bias.dtype, Y.dtype))
-    return Y
+def _check_bias(bias, shape, Y):
+    if bias.shape != shape:
+        raise _shape_error("bias", bias, shape)
+    if bias.dtype != Y.dtype:
+        raise TypeError("bias is %s, Y %s" % (bias.dtype, Y.dtype))
 
 
 def ox_quantize_fp8(X, index=None, block_rows=1, Q=None, scales=None, stream=None):
@@ -343,22 +360,40 @@ def ox_quantize_fp8(X, index=None, block_rows=1, Q=None, scales=None, stream=Non
     [ceil(K/128), R]; block_rows=128: a scale per 128 x 128, scales
     [ceil(R/128), ceil(K/128)].  index (int32 [R], block_rows=1 only): row r of
     the result is row index[r] of X.  Returns (Q float8_e4m3fn [R, K], scales)."""
-    torch = _torch()
+    f8, u8, f32, i32, raw = _F8 or _types()
     rows, K = X.shape
-    R = rows if index is None else index.numel()
-    kb = -(-K // 128)
-    shape = (kb, R) if block_rows == 1 else (-(-R // 128), kb)
-    if index is not None and index.dtype != torch.int32:
-        raise TypeError("index must be int32")
+    R, kb, at = rows, (K + 127) >> 7, None
+    if block_rows != 1 and block_rows != 128:
+        raise ValueError("block_rows must be 1 or 128")
+    if index is not None:
+        if index.dtype != i32:
+            raise TypeError("index must be int32")
+        if block_rows != 1:
+            raise ValueError("index needs block_rows=1")
+        R, at = index.numel(), index.data_ptr()
+    shape = (kb, R) if block_rows == 1 else ((R + 127) >> 7, kb)
     if Q is None:
-        Q = torch.empty((R, K), dtype=torch.float8_e4m3fn, device=X.device)
+        Q = _new_result((R, K), f8, X.device)
+    elif Q.shape != (R, K):
+        raise _shape_error("Q", Q, (R, K))
+    elif Q.dtype != f8 and Q.dtype != u8:
+        raise TypeError("Q must be float8_e4m3fn or uint8")
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=X.device)
-    _operands((X, "X"), (index, "index"), (Q, "Q"), (scales, "scales"))
-    _need(tuple(Q.shape) == (R, K) and Q.element_size() == 1, "Q is not one byte [%d, %d]", R, K)
-    _need(tuple(scales.shape) == shape and scales.dtype == torch.float32, "scales is not float32 %s", shape)
-    _check(lib.ox_quantize_fp8(_dtype_code(X), rows, K, _ptr(X), R, _ptr(index), block_rows, _ptr(Q),
-                               _ptr(scales), _stream(stream)))
+        scales = _new_result(shape, f32, X.device)
+    elif scales.shape != shape:
+        raise _shape_error("scales", scales, shape)
+    elif scales.dtype != f32:
+        raise TypeError("scales must be float32")
+    code = _dtype_code(X)
+    dev = X.get_device()
+    if not (dev >= 0 and Q.get_device() == dev and scales.get_device() == dev and X.is_contiguous()
+            and Q.is_contiguous() and scales.is_contiguous()
+            and (index is None or (index.get_device() == dev and index.is_contiguous()))):
+        raise _refuse_memory(("X", "Q", "scales", "index"), X, Q, scales, index)
+    st = lib.ox_quantize_fp8(code, rows, K, X.data_ptr(), R, at, block_rows, Q.data_ptr(), scales.data_ptr(),
+                             raw(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
     return Q, scales
 
 
@@ -366,22 +401,41 @@ def ox_gemm_fp8(A, a_scales, B, b_scales, bias=None, act="none", Y=None, out_dty
     """Y [M, N] = act(A B^T + bias) for e4m3 A [M, K] and B [N, K] with block
     scales (as ox_quantize_fp8 makes them with block_rows 1 and 128).  Y's type
     (out_dtype, default bfloat16, or float32) is the bias's too."""
-    torch = _torch()
+    f8, u8, f32, i32, raw = _F8 or _types()
     M, K = A.shape
-    N = B.shape[0]
-    _need(B.shape[1] == K, "B has %d columns, A %d", B.shape[1], K)
-    _f8_operands(A, a_scales, B, b_scales, K, M, (-(-N // 128),))
-    Y = _epilogue(Y, bias, (M, N), (N,), out_dtype or torch.bfloat16, A.device)
-    _operands((A, "A"), (a_scales, "a_scales"), (B, "B"), (b_scales, "b_scales"), (bias, "bias"), (Y, "Y"))
-    _check(lib.ox_gemm_fp8(_dtype_code(Y), M, N, K, _ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales),
-                           _ptr(bias), ACT[act], _ptr(Y), _stream(stream)))
+    N, Kb = B.shape
+    if Kb != K:
+        raise ValueError("B has %d columns, A %d" % (Kb, K))
+    kb = (K + 127) >> 7
+    if not ((A.dtype == f8 or A.dtype == u8) and (B.dtype == f8 or B.dtype == u8) and a_scales.dtype == f32
+            and b_scales.dtype == f32 and a_scales.shape == (kb, M) and b_scales.shape == ((N + 127) >> 7, kb)):
+        raise _refuse_f8(A, a_scales, B, b_scales, (kb, M), ((N + 127) >> 7, kb))
+    if Y is None:
+        Y = _new_result((M, N), out_dtype, A.device)
+    elif Y.shape != (M, N):
+        raise _shape_error("Y", Y, (M, N))
+    if bias is not None:
+        _check_bias(bias, (N,), Y)
+    code = _dtype_code(Y)
+    dev = A.get_device()
+    if not (dev >= 0 and a_scales.get_device() == dev and B.get_device() == dev and b_scales.get_device() == dev
+            and Y.get_device() == dev and A.is_contiguous() and a_scales.is_contiguous() and B.is_contiguous()
+            and b_scales.is_contiguous() and Y.is_contiguous()
+            and (bias is None or (bias.get_device() == dev and bias.is_contiguous()))):
+        raise _refuse_memory(("A", "a_scales", "B", "b_scales", "Y", "bias"), A, a_scales, B, b_scales, Y, bias)
+    st = lib.ox_gemm_fp8(code, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(), b_scales.data_ptr(),
+                         None if bias is None else bias.data_ptr(), ACT[act], Y.data_ptr(),
+                         raw(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
     return Y
 
 
-def _offsets(offsets, E):
-    if offsets.dtype != _torch().int32:
+def _check_offsets(offsets, E, i32):
+    if offsets.dtype != i32:
         raise TypeError("offsets must be int32")
-    _need(tuple(offsets.shape) == (E + 1,), "offsets is %s, not [experts + 1] = (%d,)", tuple(offsets.shape), E + 1)
+    if offsets.shape != (E + 1,):
+        raise _shape_error("offsets", offsets, (E + 1,))
 
 
 def ox_gemm_grouped(A, B, offsets, bias=None, transB=True, act="none", Y=None, stream=None):
@@ -389,16 +443,34 @@ def ox_gemm_grouped(A, B, offsets, bias=None, transB=True, act="none", Y=None, s
     B [E, N, K] (transB) or [E, K, N]; offsets int32 [E+1] on the device; bias
     [E, N].  float32 or bfloat16 throughout.  Rows outside every expert's are
     zero in Y [T, N]."""
+    f8, u8, f32, i32, raw = _F8 or _types()
     T, K = A.shape
-    E, N, Kb = B.shape if transB else (B.shape[0], B.shape[2], B.shape[1])
-    _need(Kb == K, "B's reduction is %d, A's %d", Kb, K)
-    _offsets(offsets, E)
-    Y = _epilogue(Y, bias, (T, N), (E, N), A.dtype, A.device)
-    if B.dtype != A.dtype or Y.dtype != A.dtype:
-        raise TypeError("A is %s, B %s, Y %s" % (A.dtype, B.dtype, Y.dtype))
-    _operands((A, "A"), (B, "B"), (offsets, "offsets"), (bias, "bias"), (Y, "Y"))
-    _check(lib.ox_gemm_grouped(_dtype_code(A), T, N, K, E, int(bool(transB)), _ptr(A), _ptr(B), _ptr(offsets),
-                               _ptr(bias), ACT[act], _ptr(Y), _stream(stream)))
+    E, N, Kb = B.shape
+    if not transB:
+        N, Kb = Kb, N
+    if Kb != K:
+        raise ValueError("B's reduction is %d, A's %d" % (Kb, K))
+    _check_offsets(offsets, E, i32)
+    dtype = A.dtype
+    if Y is None:
+        Y = _new_result((T, N), dtype, A.device)
+    elif Y.shape != (T, N):
+        raise _shape_error("Y", Y, (T, N))
+    if B.dtype != dtype or Y.dtype != dtype:
+        raise TypeError("A is %s, B %s, Y %s" % (dtype, B.dtype, Y.dtype))
+    if bias is not None:
+        _check_bias(bias, (E, N), Y)
+    code = _dtype_code(A)
+    dev = A.get_device()
+    if not (dev >= 0 and B.get_device() == dev and offsets.get_device() == dev and Y.get_device() == dev
+            and A.is_contiguous() and B.is_contiguous() and offsets.is_contiguous() and Y.is_contiguous()
+            and (bias is None or (bias.get_device() == dev and bias.is_contiguous()))):
+        raise _refuse_memory(("A", "B", "offsets", "Y", "bias"), A, B, offsets, Y, bias)
+    st = lib.ox_gemm_grouped(code, T, N, K, E, 1 if transB else 0, A.data_ptr(), B.data_ptr(), offsets.data_ptr(),
+                             None if bias is None else bias.data_ptr(), ACT[act], Y.data_ptr(),
+                             raw(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
     return Y
 
 
@@ -406,17 +478,35 @@ def ox_gemm_grouped_fp8(A, a_scales, B, b_scales, offsets, bias=None, act="none"
                         stream=None):
     """ox_gemm_grouped for e4m3 operands with block scales: A [T, K], a_scales
     [ceil(K/128), T], B [E, N, K], b_scales [E, ceil(N/128), ceil(K/128)]."""
-    torch = _torch()
+    f8, u8, f32, i32, raw = _F8 or _types()
     T, K = A.shape
     E, N, Kb = B.shape
-    _need(Kb == K, "B's reduction is %d, A's %d", Kb, K)
-    _offsets(offsets, E)
-    _f8_operands(A, a_scales, B, b_scales, K, T, (E, -(-N // 128)))
-    Y = _epilogue(Y, bias, (T, N), (E, N), out_dtype or torch.bfloat16, A.device)
-    _operands((A, "A"), (a_scales, "a_scales"), (B, "B"), (b_scales, "b_scales"), (offsets, "offsets"),
-              (bias, "bias"), (Y, "Y"))
-    _check(lib.ox_gemm_grouped_fp8(_dtype_code(Y), T, N, K, E, _ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales),
-                                   _ptr(offsets), _ptr(bias), ACT[act], _ptr(Y), _stream(stream)))
+    if Kb != K:
+        raise ValueError("B's reduction is %d, A's %d" % (Kb, K))
+    kb = (K + 127) >> 7
+    _check_offsets(offsets, E, i32)
+    if not ((A.dtype == f8 or A.dtype == u8) and (B.dtype == f8 or B.dtype == u8) and a_scales.dtype == f32
+            and b_scales.dtype == f32 and a_scales.shape == (kb, T) and b_scales.shape == (E, (N + 127) >> 7, kb)):
+        raise _refuse_f8(A, a_scales, B, b_scales, (kb, T), (E, (N + 127) >> 7, kb))
+    if Y is None:
+        Y = _new_result((T, N), out_dtype, A.device)
+    elif Y.shape != (T, N):
+        raise _shape_error("Y", Y, (T, N))
+    if bias is not None:
+        _check_bias(bias, (E, N), Y)
+    code = _dtype_code(Y)
+    dev = A.get_device()
+    if not (dev >= 0 and a_scales.get_device() == dev and B.get_device() == dev and b_scales.get_device() == dev
+            and offsets.get_device() == dev and Y.get_device() == dev and A.is_contiguous()
+            and a_scales.is_contiguous() and B.is_contiguous() and b_scales.is_contiguous() and offsets.is_contiguous()
+            and Y.is_contiguous() and (bias is None or (bias.get_device() == dev and bias.is_contiguous()))):
+        raise _refuse_memory(("A", "a_scales", "B", "b_scales", "offsets", "Y", "bias"), A, a_scales, B, b_scales,
+                             offsets, Y, bias)
+    st = lib.ox_gemm_grouped_fp8(code, T, N, K, E, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(),
+                                 b_scales.data_ptr(), offsets.data_ptr(), None if bias is None else bias.data_ptr(),
+                                 ACT[act], Y.data_ptr(), raw(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
     return Y
 
 

@@ -39,10 +39,87 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 // of the norm of a random result.  bf16 results, rounded at 2^-9, take it.
 // FMT_FP8X widens the codes to bf16 (exact) for the bf16 instruction, whose
 // sums are fp32 throughout, at half the rate: fp32 results take it.
-enum Fmt : int { FMT_BF16 = 0, FMT_FP8 = 1, FMT_FP8X = 2 };
+// fp32 operands take the K = 4 fp32 instruction, four to a 16-byte piece.
+enum Fmt : int { FMT_BF16 = 0, FMT_FP8 = 1, FMT_FP8X = 2, FMT_F32 = 3 };
+
+template <int FMT>
+struct FmtOps {
+  static constexpr bool F8 = FMT == FMT_FP8 || FMT == FMT_FP8X;
+  static constexpr int ESZ = F8 ? 1 : FMT == FMT_F32 ? 4 : 2;
+  // a fragment's 128 bytes of K as the matrix instructions take them
+  struct Frag { u32x4_t v[FMT == FMT_FP8X ? 4 : 2]; };
+  static __device__ __forceinline__ Frag widen(u32x4_t x, u32x4_t y) {
+    Frag f;
+    if constexpr (FMT == FMT_FP8X) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t c = i < 4 ? x[i] : y[i - 4];
+        f.v[i / 2][2 * (i % 2)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
+        f.v[i / 2][2 * (i % 2) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
+      }
+    } else {
+      f.v[0] = x;
+      f.v[1] = y;
+    }
+    return f;
+  }
+  static __device__ __forceinline__ i32x8_t cat(u32x4_t x, u32x4_t y) {
+    return i32x8_t{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+  }
+  // c += the products of piece h of both fragments
+  template <int H>
+  static __device__ __forceinline__ f32x4_t half(const Frag& b, const Frag& a, f32x4_t c) {
+    if constexpr (FMT == FMT_F32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b.v[H][i]), __uint_as_float(a.v[H][i]), c, 0, 0, 0);
+      return c;
+    } else {
+      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b.v[H]),
+                                                     __builtin_bit_cast(bf16x8_t, a.v[H]), c, 0, 0, 0);
+    }
+  }
+  // the 16 x 16 sums of one block of 128 k of e4m3
+  static __device__ __forceinline__ f32x4_t block(const Frag& b, const Frag& a) {
+    f32x4_t p = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (FMT == FMT_FP8) {
+      p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(cat(b.v[0], b.v[1]), cat(a.v[0], a.v[1]), p, 0, 0, 0, 0, 0, 0);
+    } else if constexpr (FMT == FMT_FP8X) {
+      p = half<0>(b, a, p);
+      p = half<1>(b, a, p);
+      p = half<2>(b, a, p);
+      p = half<3>(b, a, p);
+    }
+    return p;
+  }
+};
+
+// LDS by pointer and constant, so that the constant goes into the instruction
+__device__ __forceinline__ const OX_LDS char* lds_ptr(uint32_t a) { return (const OX_LDS char*)(uintptr_t)a; }
+__device__ __forceinline__ u32x4_t lds_read_at(const OX_LDS char* p, int o) { return *(const OX_LDS u32x4_t*)(p + o); }
 
 // One piece of 16 bytes at any address.
 struct __attribute__((packed, aligned(1))) Bytes16 { u32x4_t v; };
+
+// The descriptor in scalar registers, where the DMA wants it.  A vector
+// instruction that writes a scalar register (v_readfirstlane) needs five wait
+// states before a vector-memory instruction reads it; the compiler does not
+// see the reader inside the DMA's assembly, so they are spent here.
+__device__ __forceinline__ u32x4_t uniform_words(const char* p, int64_t bytes) {
+  u32x4_t w = buffer_words(p, (uint32_t)bytes);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_readfirstlane(w[i]);
+  asm volatile("s_nop 4" : "+s"(w));
+  return w;
+}
+
+// the same address in scalar registers
+template <typename T>
+__device__ __forceinline__ T* uniform_ptr(T* p) {
+  const uint64_t v = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (T*)(uintptr_t)(((uint64_t)hi << 32) | lo);
+}
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
@@ -72,61 +149,8 @@ struct ExpertTile {
   int e, row0, rows;   // expert, first row of the tile, rows in it (<= BM)
 };
 
-// Number of row tiles of all experts (every lane of the wave takes part).
-template <int BM>
-__device__ __forceinline__ int expert_tiles(const ExpertArgs& a) {
-  if (!a.offsets) return (a.T + BM - 1) / BM;
-  int total = 0;
-  for (int base = 0; base < a.E; base += 64) {
-    const int e = base + (threadIdx.x & 63);
-    int n = 0;
-    if (e < a.E) {
-      int lo, hi;
-      expert_rows(a, e, lo, hi);
-      n = (hi - lo + BM - 1) / BM;
-    }
-    total += __builtin_amdgcn_readlane(wave_scan(n), 63);
-  }
-  return total;
-}
-
-// Row tile t of those, 0 <= t < expert_tiles().
-template <int BM>
-__device__ __forceinline__ ExpertTile expert_tile(const ExpertArgs& a, int t) {
-  ExpertTile r = {0, 0, 0};
-  if (!a.offsets) {
-    r.row0 = t * BM;
-    r.rows = min(BM, a.T - r.row0);
-    return r;
-  }
-  int before = 0;
-  for (int base = 0; base < a.E; base += 64) {
-    const int e = base + (threadIdx.x & 63);
-    int lo = 0, hi = 0;
-    if (e < a.E) expert_rows(a, e, lo, hi);
-    const int n = (hi - lo + BM - 1) / BM;
-    const int s = before + wave_scan(n);          // tiles up to and including e's
-    const uint64_t past = __ballot(s > t);
-    if (past) {
-      const int l = __ffsll((unsigned long long)past) - 1;
-      const int first = __builtin_amdgcn_readlane(s - n, l);
-      r.e = base + l;
-      r.row0 = __builtin_amdgcn_readlane(lo, l) + (t - first) * BM;
-      r.rows = min(BM, __builtin_amdgcn_readlane(hi, l) - r.row0);
-      return r;
-    }
-    before = __builtin_amdgcn_readlane(s, 63);
-  }
-  return r;
-}
-
-// Zeros in the rows before the first expert's and past the last one's, spread
-// over the grid's blocks.
-__device__ __forceinline__ void zero_outside(const ExpertArgs& a) {
-  if (!a.offsets) return;
-  const int first = clampi(a.offsets[0], 0, a.T);
-  const int last = clampi(a.offsets[a.E], 0, a.T);
-  if (first == 0 && last == a.T) return;
+// Zeros in rows [0, first) and [last, T), spread over the grid's blocks.
+__device__ __forceinline__ void zero_outside(const ExpertArgs& a, int first, int last) {
   const int64_t head = (int64_t)first * a.N, tail = (int64_t)max(first, last) * a.N, all = (int64_t)a.T * a.N;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (int64_t)gridDim.x * blockDim.x) {
     if (i >= head && i < tail) continue;
@@ -135,7 +159,7 @@ __device__ __forceinline__ void zero_outside(const ExpertArgs& a) {
   }
 }
 
-// The block's tile among total row tiles x NT column tiles: each XCD runs one
+// The block's place in `total` row tiles x NT column tiles: each XCD runs one
 // contiguous range of an order that takes bands of four row tiles and walks
 // the columns inside a band, so the blocks that run together on an XCD share
 // both operands' tiles through its L2.
@@ -146,33 +170,100 @@ __device__ __forceinline__ void tile_order(int u, int total, int NT, int& t, int
   t = band * 4 + in - nt * h;
 }
 
+// This block's tile, from the offsets; false when the offsets have fewer.
+// Also writes its share of the zeros outside the experts' rows.  Up to 64
+// experts are one load and one scan across the wave (a second round for each
+// 64 more); every wave does it for itself, without a barrier.
+template <int BM>
+__device__ __forceinline__ bool find_tile(const ExpertArgs& a, int NT, ExpertTile& r, int& nt) {
+  const int b = blockIdx.x;
+  int t;
+  if (!a.offsets) {
+    const int total = (a.T + BM - 1) / BM;
+    tile_order(xcd_tile(b, total * NT), total, NT, t, nt);
+    r.e = 0;
+    r.row0 = t * BM;
+    r.rows = min(BM, a.T - r.row0);
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  int lo, n, s, total = 0, first = 0, last = 0;
+  for (int base = 0; base < a.E; base += 64) {
+    int hi = 0;
+    lo = 0;
+    if (base + lane < a.E) expert_rows(a, base + lane, lo, hi);
+    if (base == 0) first = __builtin_amdgcn_readlane(lo, 0);
+    last = max(last, __builtin_amdgcn_readlane(hi, min(63, a.E - 1 - base)));
+    n = (hi - lo + BM - 1) / BM;
+    s = wave_scan(n);
+    total += __builtin_amdgcn_readlane(s, 63);
+    r.rows = hi;
+  }
+  if (first != 0 || last != a.T) zero_outside(a, first, last);
+  if ((int64_t)b >= (int64_t)total * NT) return false;
+  tile_order(xcd_tile(b, total * NT), total, NT, t, nt);
+  int hi = r.rows, before = 0, base = 0;
+  for (;;) {
+    if (a.E > 64) {
+      lo = hi = 0;
+      if (base + lane < a.E) expert_rows(a, base + lane, lo, hi);
+      n = (hi - lo + BM - 1) / BM;
+      s = wave_scan(n);
+    }
+    const uint64_t past = __ballot(before + s > t);
+    if (past) {
+      const int l = __ffsll((unsigned long long)past) - 1;
+      const int skip = t - before - __builtin_amdgcn_readlane(s - n, l);   // tiles of this expert before this one
+      r.e = base + l;
+      r.row0 = __builtin_amdgcn_readlane(lo, l) + skip * BM;
+      r.rows = min(BM, __builtin_amdgcn_readlane(hi, l) - r.row0);
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(s, 63);
+    base += 64;
+  }
+}
+
 // The tile kernel: BM rows x BN columns per block, WM x WN waves, S stages of
-// 128 bytes of K.  DMA: both operands arrive by buffer-to-LDS loads (16-byte
+// U blocks of 128 bytes of K.  DMA: both operands arrive by buffer-to-LDS loads (16-byte
 // aligned rows); otherwise through registers, from any address.  KN (bf16):
-// B is [K, N] per expert; its stage holds 64 rows of BN columns, read back
-// with transposing LDS reads.
-template <int FMT, int BM, int BN, int WM, int WN, int S, bool DMA, bool KN>
+// B is [K, N] per expert; its stage holds 64 (fp32: 32) rows of BN columns, read
+// back with transposing LDS reads.
+template <int FMT, int BM, int BN, int WM, int WN, int S, int U, bool DMA, bool KN>
 struct ExpertTileKernel {
   static constexpr int NW = WM * WN, TH = NW * 64;
   static constexpr int TM = BM / WM, TN = BN / WN, MF = TM / 16, NF = TN / 16;
-  static constexpr bool F8 = FMT != FMT_BF16;
-  static constexpr int ESZ = F8 ? 1 : 2;
+  typedef FmtOps<FMT> Mm;
+  typedef typename Mm::Frag Frag;
+  static constexpr bool F8 = Mm::F8;
+  static constexpr int ESZ = Mm::ESZ;
   static constexpr int KE = 128 / ESZ;                       // elements of K per stage
+  static constexpr int MPP = FMT == FMT_F32 ? 4 : 1;         // matrix instructions per piece
+  static constexpr int KNR = FMT == FMT_F32 ? 8 : 4;         // [K, N]: LDS reads per fragment
+  static constexpr int PE = 16 / ESZ;                        // elements per piece
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   static constexpr int SA_BYTES = F8 ? (BM < 64 ? 64 : BM) * 4 : 0;
   static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES;
-  static constexpr int LDS_BYTES = S * STAGE;
+  static constexpr int LDS_BYTES = S * U * STAGE;
   static constexpr int DA = BM / 8 / NW, DB = BN / 8 / NW;   // DMA instructions per wave and stage
   static constexpr int D = DA + DB + (F8 ? 1 : 0);
   static_assert(!DMA || (DA * NW * 8 == BM && DB * NW * 8 == BN), "whole DMA instructions per wave");
-  static_assert(!KN || FMT == FMT_BF16, "[K, N] weights are bf16");
+  static_assert(DMA || U == 1, "one block per stage through registers");
+  static_assert(MF % 2 == 0, "row fragments alternate between two sets of block sums");
+  static_assert(!KN || (NF & (NF - 1)) == 0, "fragments are bits of the column");
+  static_assert(!KN || !F8, "e4m3 weights are [N, K]");
+  static_assert(!KN || FMT != FMT_F32 || BN % 64 == 0, "the swizzle of fp32 rows spans 64 columns");
   static_assert(!F8 || TN <= 128, "a wave's columns share a scale block");
 
   static __device__ __forceinline__ int sw_a(int r) { return (r >> 1) & 7; }
   // a lane of row group i/4 reads row (i/4)*4*NF + 4*j + i%4 for fragment j
   static __device__ __forceinline__ int sw_b(int r) { return ((r >> 1) & 1) | (((r / (4 * NF)) & 3) << 1); }
-  // [K, N]: a transposing read touches rows {0..3, 8..11} (+ 16, + 4) x 32 bytes
-  static __device__ __forceinline__ int sw_kn(int k) { return (((k & 3) | ((k >> 1) & 4)) << 1) & (BN / 8 - 1); }
+  // [K, N], bf16: a transposing read touches rows {0..3, 8..11} (+ 16, + 4) x
+  // 32 bytes; fp32: a read touches rows {0, 4, 8, 12} (+ 0..3, + 16) x 64 bytes
+  static __device__ __forceinline__ int sw_kn(int k) {
+    if constexpr (FMT == FMT_F32) return ((k >> 2) & 3) << 2;
+    return (((k & 3) | ((k >> 1) & 4)) << 1) & (BN / 8 - 1);
+  }
 
   const ExpertArgs& a;
   char* smem;
@@ -182,16 +273,16 @@ struct ExpertTileKernel {
   const float* sb;       // b_scales of this wave's block row
   int rows, cols;        // valid rows and columns of the tile
   int64_t lda, ldb;      // row strides in bytes
-  int nk;
+  int nk, wave;
   uint32_t va[DA ? DA : 1], vb[DB ? DB : 1], vs;
 
   __device__ __forceinline__ ExpertTileKernel(const ExpertArgs& a_, char* s) : a(a_), smem(s) {}
 
-  __device__ __forceinline__ uint32_t stage_base(int k) const { return lds_addr(smem) + (uint32_t)(k % S) * STAGE; }
+  __device__ __forceinline__ uint32_t stage_base(int k) const { return lds_addr(smem) + (uint32_t)(k % (S * U)) * STAGE; }
 
   // --- DMA staging
   __device__ __forceinline__ void init_dma() {
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, w = wave;
 #pragma unroll
     for (int i = 0; i < DA; ++i) {
       const int r = (w * DA + i) * 8 + (lane >> 3);
@@ -200,7 +291,7 @@ struct ExpertTileKernel {
 #pragma unroll
     for (int i = 0; i < DB; ++i) {
       if constexpr (KN) {
-        const int p = (w * DB + i) * 64 + lane, k = p / (BN / 8), c = p % (BN / 8);
+        const int p = (w * DB + i) * 64 + lane, k = p / (BN / PE), c = p % (BN / PE);
         vb[i] = (uint32_t)(k * (int)ldb + ((c ^ sw_kn(k)) << 4));
       } else {
         const int r = (w * DB + i) * 8 + (lane >> 3);
@@ -212,34 +303,43 @@ struct ExpertTileKernel {
       vs = r < rows ? (uint32_t)r * 4u : 0xFFFFFF00u;
     }
   }
+  // Blocks of K in the order of the stages: a block that K ends inside comes
+  // first, so that every later stage is whole and the loop has no branch (a
+  // branch inside it would let the compiler move additions past it).
+  int part;              // 1 when K ends inside a block
+  __device__ __forceinline__ int block_of(int k) const { return DMA && part ? (k == 0 ? nk - 1 : k - 1) : k; }
+
+  // Stage k into its slot.  PART: the pieces of the block from K on are zeros.
+  // A stage past the last one is loaded from an empty range (zeros, no
+  // traffic), which keeps the number of loads in flight the same for all.
+  template <bool PART>
   __device__ __forceinline__ void issue(int k) {
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, w = wave;
     const uint32_t base = __builtin_amdgcn_readfirstlane(stage_base(k));
-    const int left = a.K * ESZ - k * 128;       // bytes of K from this stage on
-    const bool tail = left < 128;
-    const u32x4_t ra = buffer_words(Ab + (int64_t)k * 128, (uint32_t)((int64_t)(rows - 1) * lda + left));
+    const bool any = k < nk;
+    const int kb = any ? block_of(k) : 0;
+    const int left = PART ? a.K * ESZ - kb * 128 : 128;       // bytes of K from this block on
+    const u32x4_t ra = uniform_words(Ab + (int64_t)kb * 128, any ? (int64_t)(rows - 1) * lda + left : 0);
 #pragma unroll
     for (int i = 0; i < DA; ++i) {
-      const int r = (w * DA + i) * 8 + (lane >> 3);
-      const bool past = tail && (((lane & 7) ^ sw_a(r)) << 4) >= left;
+      const bool past = PART && (((lane & 7) ^ sw_a((w * DA + i) * 8 + (lane >> 3))) << 4) >= left;
       dma16(base + (w * DA + i) * 1024, past ? 0xFFFFFF00u : va[i], ra);
     }
     if constexpr (KN) {
-      const int64_t kl = min(64, a.K - k * 64);   // rows of K in this stage
-      const u32x4_t rb = buffer_words(Bb + (int64_t)k * 64 * ldb, (uint32_t)((kl - 1) * ldb + (int64_t)cols * ESZ));
+      const int64_t kl = PART ? min(KE, a.K - kb * KE) : KE;   // rows of K in this block
+      const u32x4_t rb = uniform_words(Bb + (int64_t)kb * KE * ldb, any ? (kl - 1) * ldb + (int64_t)cols * ESZ : 0);
 #pragma unroll
       for (int i = 0; i < DB; ++i) dma16(base + A_BYTES + (w * DB + i) * 1024, vb[i], rb);
     } else {
-      const u32x4_t rb = buffer_words(Bb + (int64_t)k * 128, (uint32_t)((int64_t)(cols - 1) * ldb + left));
+      const u32x4_t rb = uniform_words(Bb + (int64_t)kb * 128, any ? (int64_t)(cols - 1) * ldb + left : 0);
 #pragma unroll
       for (int i = 0; i < DB; ++i) {
-        const int r = (w * DB + i) * 8 + (lane >> 3);
-        const bool past = tail && (((lane & 7) ^ sw_b(r)) << 4) >= left;
+        const bool past = PART && (((lane & 7) ^ sw_b((w * DB + i) * 8 + (lane >> 3))) << 4) >= left;
         dma16(base + A_BYTES + (w * DB + i) * 1024, past ? 0xFFFFFF00u : vb[i], rb);
       }
     }
     if constexpr (F8) {
-      const u32x4_t rs = buffer_words(sa + (int64_t)k * a.T, (uint32_t)rows * 4u);
+      const u32x4_t rs = uniform_words((const char*)(sa + (int64_t)kb * a.T), any ? (int64_t)rows * 4 : 0);
       dma4(base + A_BYTES + B_BYTES + (w * 256) % SA_BYTES, vs, rs);
     }
   }
@@ -271,9 +371,9 @@ struct ExpertTileKernel {
     for (int i = 0; i < CB; ++i) {
       const int q = threadIdx.x + i * TH;
       if constexpr (KN) {
-        const int kr = q / (BN / 8), c = (q % (BN / 8)) ^ sw_kn(kr);
-        g.rb[i] = piece(Bb + ((int64_t)k * 64 + kr) * ldb + c * 16,
-                        k * 64 + kr < a.K ? (int64_t)cols * ESZ - c * 16 : 0);
+        const int kr = q / (BN / PE), c = (q % (BN / PE)) ^ sw_kn(kr);
+        g.rb[i] = piece(Bb + ((int64_t)k * KE + kr) * ldb + c * 16,
+                        k * KE + kr < a.K ? (int64_t)cols * ESZ - c * 16 : 0);
       } else {
         const int r = q >> 3, c = (q & 7) ^ sw_b(r);
         g.rb[i] = piece(Bb + r * ldb + (int64_t)k * 128 + c * 16, r < cols ? left - c * 16 : 0);
@@ -282,7 +382,7 @@ struct ExpertTileKernel {
     if constexpr (F8) g.s = (int)threadIdx.x < rows ? sa[(int64_t)k * a.T + threadIdx.x] : 0.0f;
   }
   __device__ __forceinline__ void store_regs(int k, const Regs& g) {
-    char* st = smem + (k % S) * STAGE;
+    char* st = smem + (k % (S * U)) * STAGE;
 #pragma unroll
     for (int i = 0; i < CA; ++i) *(u32x4_t*)(st + (threadIdx.x + i * TH) * 16) = g.ra[i];
 #pragma unroll
@@ -297,115 +397,168 @@ struct ExpertTileKernel {
     const int g = (threadIdx.x & 63) >> 4;
     return wn * TN + (KN ? j * 16 + g * 4 + r : g * 4 * NF + j * 4 + r);
   }
-  __device__ __forceinline__ void frag_a(uint32_t st, int wm, int f, u32x4_t& x, u32x4_t& y) const {
-    const int lane = threadIdx.x & 63, g = lane >> 4;
-    const int r = wm * TM + f * 16 + (lane & 15);
-    const uint32_t p = st + r * 128;
-    x = lds_read_b128(p + ((g ^ sw_a(r)) << 4));
-    y = lds_read_b128(p + (((g + 4) ^ sw_a(r)) << 4));
-  }
-  __device__ __forceinline__ void frag_b(uint32_t st, int wn, int f, u32x4_t& x, u32x4_t& y) const {
+  // This lane's fragment addresses inside a stage.  f(r) is the same for every
+  // fragment of a lane, so fragment f lies f * 2048 (A), f * 512 ([N, K]) past
+  // the first, and the second piece of a row is the first's address ^ 64.
+  uint32_t oa, ob[KN ? 4 : 1];
+  __device__ __forceinline__ void init_frags(int wm, int wn) {
     const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
-    if constexpr (KN) {
-      const int c = wn * TN + f * 16 + 4 * (i & 3);            // first of this lane's four columns
-      auto rd = [&](int k) {
-        return lds_read_tr16(st + A_BYTES + k * (BN * 2) + (((c >> 3) ^ sw_kn(k)) << 4) + (c & 4) * 2);
-      };
-      const int k = g * 8 + (i >> 2);
-      const u32x2_t x0 = rd(k), x1 = rd(k + 4), y0 = rd(k + 32), y1 = rd(k + 36);
-      x = u32x4_t{x0[0], x0[1], x1[0], x1[1]};
-      y = u32x4_t{y0[0], y0[1], y1[0], y1[1]};
-    } else {
-      const int r = wn * TN + (i >> 2) * 4 * NF + f * 4 + (i & 3);
-      const uint32_t p = st + A_BYTES + r * 128;
-      x = lds_read_b128(p + ((g ^ sw_b(r)) << 4));
-      y = lds_read_b128(p + (((g + 4) ^ sw_b(r)) << 4));
-    }
-  }
-  static __device__ __forceinline__ i32x8_t cat(u32x4_t x, u32x4_t y) {
-    return i32x8_t{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
-  }
-  // a fragment's operands as the matrix instructions take them
-  struct Frag { u32x4_t v[FMT == FMT_FP8X ? 4 : 2]; };
-  static __device__ __forceinline__ Frag widen(u32x4_t x, u32x4_t y) {
-    Frag f;
-    if constexpr (FMT == FMT_FP8X) {
+    const int r = wm * TM + i;
+    oa = r * 128 + ((g ^ sw_a(r)) << 4);
+    if constexpr (KN && FMT == FMT_F32) {
+      // column i of the fragment, row g * 4 (+ e, + 16)
+      ob[0] = A_BYTES + g * 4 * (BN * 4) + (i & 3) * 4 + (((wn * TN / 4 + (i >> 2)) ^ sw_kn(g * 4)) << 4);
+    } else if constexpr (KN) {
+      // (column 4*(i & 3) of the fragment; the rows g*8 + i/4, + 4, + 32, + 36)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t c = i < 4 ? x[i] : y[i - 4];
-        f.v[i / 2][2 * (i % 2)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
-        f.v[i / 2][2 * (i % 2) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
+      for (int h = 0; h < 4; ++h) {
+        const int k = g * 8 + (i >> 2) + (h & 1) * 4 + (h >> 1) * 32;
+        ob[h] = A_BYTES + k * (BN * 2) + (i & 1) * 8 + (((wn * TN / 8 + ((i >> 1) & 1)) ^ sw_kn(k)) << 4);
       }
     } else {
-      f.v[0] = x;
-      f.v[1] = y;
+      const int q = wn * TN + (i >> 2) * 4 * NF + (i & 3);
+      ob[0] = A_BYTES + q * 128 + ((g ^ sw_b(q)) << 4);
     }
-    return f;
   }
-  static __device__ __forceinline__ f32x4_t mma_bf16(u32x4_t b, u32x4_t a, f32x4_t c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b), __builtin_bit_cast(bf16x8_t, a), c, 0,
-                                                   0, 0);
+  __device__ __forceinline__ void frag_a(uint32_t st, int f, u32x4_t& x, u32x4_t& y) const {
+    x = lds_read_at(lds_ptr(st + oa), f * 2048);
+    y = lds_read_at(lds_ptr(st + (oa ^ 64)), f * 2048);
   }
-  // the 16 x 16 sums of one block of 128 k of e4m3
-  static __device__ __forceinline__ f32x4_t mma_block(const Frag& b, const Frag& a) {
-    f32x4_t p = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (FMT == FMT_FP8) {
-      p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(cat(b.v[0], b.v[1]), cat(a.v[0], a.v[1]), p, 0, 0, 0, 0, 0, 0);
-    } else if constexpr (FMT == FMT_FP8X) {
+  __device__ __forceinline__ void frag_b(uint32_t st, int f, u32x4_t& x, u32x4_t& y) const {
+    if constexpr (KN && FMT == FMT_F32) {
+      const OX_LDS char* p = lds_ptr(st + (ob[0] ^ (uint32_t)(f * 64)));
 #pragma unroll
-      for (int h = 0; h < 4; ++h) p = mma_bf16(b.v[h], a.v[h], p);
+      for (int e = 0; e < 4; ++e) {
+        x[e] = *(const OX_LDS uint32_t*)(p + e * (BN * 4));
+        y[e] = *(const OX_LDS uint32_t*)(p + (16 + e) * (BN * 4));
+      }
+    } else if constexpr (KN) {
+      // f * 32 bytes further in the row, through the swizzle (a power of two per bit of f)
+      u32x2_t v[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) v[h] = lds_read_tr16(st + (ob[h] ^ (uint32_t)(f * 32)));
+      x = u32x4_t{v[0][0], v[0][1], v[1][0], v[1][1]};
+      y = u32x4_t{v[2][0], v[2][1], v[3][0], v[3][1]};
+    } else {
+      x = lds_read_at(lds_ptr(st + ob[0]), f * 512);
+      y = lds_read_at(lds_ptr(st + (ob[0] ^ 64)), f * 512);
     }
-    return p;
   }
-  __device__ __forceinline__ void compute(int k, int wm, int wn, float sbk, f32x4_t (&acc)[MF][NF]) {
-    const uint32_t st = stage_base(k);
+  // What a step hands to the next: the weights' fragments and the first row
+  // fragment of its stage, and the last block sums, not yet added.
+  struct Flow {
     Frag b[NF];
+    u32x4_t x, y;      // row fragment 0
+    float s;           // its row's scale
+    f32x4_t p[2][NF];  // block sums of the last two row fragments
+    float sp;          // the scale of the last ones
+  };
+  __device__ __forceinline__ float row_scale(uint32_t st, int wm, int f) const {
+    if constexpr (F8)
+      return *(const OX_LDS float*)(lds_ptr(st + A_BYTES + B_BYTES + (wm * TM + (threadIdx.x & 15)) * 4) + f * 64);
+    return 0.0f;
+  }
+  __device__ __forceinline__ void read_b(uint32_t st, int j, Flow& w) const {
+    u32x4_t x, y;
+    frag_b(st, j, x, y);
+    w.b[j] = Mm::widen(x, y);
+  }
+  __device__ __forceinline__ void reload(int k, int wm, Flow& w) const {
+    const uint32_t st = stage_base(k);
+    frag_a(st, 0, w.x, w.y);
+    w.s = row_scale(st, wm, 0);
 #pragma unroll
-    for (int j = 0; j < NF; ++j) {
-      u32x4_t x, y;
-      frag_b(st, wn, j, x, y);
-      b[j] = widen(x, y);
-    }
+    for (int j = 0; j < NF; ++j) read_b(st, j, w);
+  }
+  __device__ __forceinline__ void begin(int wm, Flow& w) const {
+    reload(0, wm, w);
 #pragma unroll
-    for (int f = 0; f < MF; ++f) {
-      u32x4_t x, y;
-      frag_a(st, wm, f, x, y);
-      const Frag a = widen(x, y);
+    for (int j = 0; j < NF; ++j) w.p[1][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    w.sp = 0.0f;
+  }
+  static __device__ __forceinline__ void add_block(f32x4_t (&c)[NF], const f32x4_t (&p)[NF], float s) {
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) c[j][r] = __builtin_fmaf(s, p[j][r], c[j][r]);
+  }
+  // One stage.  Row fragment f + 1 is read while f is multiplied, and the
+  // block sums of f are scaled and added under the products of f + 1 (those
+  // of the last f under the next stage's first).  Before the last fragment's
+  // products every read of this stage has returned: turn() waits for the next
+  // stage and passes the barrier, the next stage's first fragments are read
+  // under these products, and refill() loads this slot again behind them.  The
+  // scheduler would sink the reads to their uses, so the order is pinned.
+  template <bool NEXT, class Turn, class Refill>
+  __device__ __forceinline__ void compute(int k, int wm, float sbk, f32x4_t (&acc)[MF][NF], Flow& w, Turn&& turn,
+                                          Refill&& refill) {
+    const uint32_t st = stage_base(k), st1 = stage_base(k + 1);
+    static_for<MF>([&](auto F) {
+      constexpr int f = F.value;
+      constexpr bool last = f + 1 == MF, load = !last || NEXT;
+      const Frag a = Mm::widen(w.x, w.y);
+      const float s1 = w.s;
+      if constexpr (last && NEXT) {
+        turn();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (load) {
+        frag_a(last ? st1 : st, last ? 0 : f + 1, w.x, w.y);
+        w.s = row_scale(last ? st1 : st, wm, last ? 0 : f + 1);
+      }
       if constexpr (F8) {
-        const float s = sbk * *(const OX_LDS float*)(uintptr_t)(st + A_BYTES + B_BYTES +
-                                                               (wm * TM + f * 16 + (threadIdx.x & 15)) * 4);
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-          const f32x4_t p = mma_block(b[j], a);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[f][j][r] = __builtin_fmaf(s, p[r], acc[f][j][r]);
+          w.p[f & 1][j] = Mm::block(w.b[j], a);
+          if constexpr (last && NEXT) read_b(st1, j, w);
         }
+        add_block(acc[(f + MF - 1) % MF], w.p[(f & 1) ^ 1], w.sp);
+        w.sp = sbk * s1;
+        __builtin_amdgcn_sched_group_barrier(0x100, load ? 3 : 0, 0);
+        static_for<NF>([&](auto) {
+          __builtin_amdgcn_sched_group_barrier(0x008, FMT == FMT_FP8X ? 4 : 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, last && NEXT ? 2 : 0, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        });
       } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < NF; ++j) acc[f][j] = Mm::template half<0>(w.b[j], a, acc[f][j]);
 #pragma unroll
-          for (int j = 0; j < NF; ++j) acc[f][j] = mma_bf16(b[j].v[h], a.v[h], acc[f][j]);
+        for (int j = 0; j < NF; ++j) {
+          acc[f][j] = Mm::template half<1>(w.b[j], a, acc[f][j]);
+          if constexpr (last && NEXT) read_b(st1, j, w);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, load ? 2 : 0, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, NF * MPP, 0);
+        static_for<NF>([&](auto) {
+          __builtin_amdgcn_sched_group_barrier(0x008, MPP, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, last && NEXT ? (KN ? KNR : 2) : 0, 0);
+        });
       }
-    }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (last && NEXT) refill();
+    });
   }
 
   // --- results: bias, activation, one rounding
-  template <int ACT>
-  __device__ __forceinline__ void store(const ExpertTile& t, int n0, int wm, int wn, f32x4_t (&acc)[MF][NF]) {
-    const int lane = threadIdx.x & 63;
-    float bv[NF][4];
+  struct Where { int e, row0, rows, n0, cols; };
+  __device__ __forceinline__ void load_bias(const Where& t, int wn, float (&bv)[NF][4]) const {
 #pragma unroll
     for (int j = 0; j < NF; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int n = col_of(wn, j, r);
         bv[j][r] = 0.0f;
-        if (a.bias && n < cols) {
-          const int64_t at = (int64_t)t.e * a.N + n0 + n;
+        if (a.bias && n < t.cols) {
+          const int64_t at = (int64_t)t.e * a.N + t.n0 + n;
           bv[j][r] = a.out_dt == DT_F32 ? ((const float*)a.bias)[at] : bf16_to_f32(((const uint16_t*)a.bias)[at]);
         }
       }
-    wait_vmem();
+  }
+  template <int ACT>
+  __device__ __forceinline__ void store(const Where& t, int wm, int wn, const f32x4_t (&acc)[MF][NF],
+                                        const float (&bv)[NF][4]) const {
+    const int lane = threadIdx.x & 63, cols = t.cols;
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
       const int m = wm * TM + f * 16 + (lane & 15);
@@ -415,7 +568,7 @@ struct ExpertTileKernel {
       for (int j = 0; j < NF; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[j][r] = act_c<ACT>(acc[f][j][r] + bv[j][r]);
-      const int64_t at = (int64_t)(t.row0 + m) * a.N + n0;
+      const int64_t at = (int64_t)(t.row0 + m) * a.N + t.n0;
       if (a.out_dt == DT_F32) {
         float* y = (float*)a.Y + at;
 #pragma unroll
@@ -458,82 +611,337 @@ struct ExpertTileKernel {
     }
   }
 
+  // Where the tile lies, and its operands' addresses.
+  __device__ __forceinline__ void setup(const ExpertTile& x, int nt, int wn, Where& t) {
+    t.e = __builtin_amdgcn_readfirstlane(x.e);
+    t.row0 = __builtin_amdgcn_readfirstlane(x.row0);
+    t.rows = rows = __builtin_amdgcn_readfirstlane(x.rows);
+    t.n0 = __builtin_amdgcn_readfirstlane(nt) * BN;
+    t.cols = cols = min(BN, a.N - t.n0);
+    Ab = uniform_ptr((const char*)a.A + (int64_t)t.row0 * lda);
+    Bb = uniform_ptr((const char*)a.B + (int64_t)t.e * a.N * a.K * ESZ + (KN ? (int64_t)t.n0 * ESZ : (int64_t)t.n0 * ldb));
+    if constexpr (F8) {
+      sa = uniform_ptr(a.sa + t.row0);
+      const int nb = (a.N + 127) / 128;
+      sb = a.sb + ((int64_t)t.e * nb + min((t.n0 + wn * TN) / 128, nb - 1)) * ((a.K + 127) / 128);
+      if (nk > 0) {
+        sb0 = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(sb[block_of(0)])));
+        refill_scales(0);
+      }
+    }
+  }
+  // The wave's b_scales: lane l holds that of block (kb & ~63) + l, and the
+  // first stage's is kept apart (it may be the last block's).
+  float sbl, sb0;
+  __device__ __forceinline__ void refill_scales(int kb0) {
+    sbl = sb[min(kb0 + (int)(threadIdx.x & 63), (a.K + 127) / 128 - 1)];
+    asm volatile("" : "+v"(sbl));   // waited for here, not (with the DMA behind it) at every use
+  }
+  __device__ __forceinline__ float scale_of(int k) {
+    if constexpr (F8) {
+      const int kb0 = min(block_of(k), nk - 1);
+      if (k > 0 && (kb0 & 63) == 0 && kb0 > 0) refill_scales(kb0);
+      const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sbl), kb0 & 63));
+      return k == 0 ? sb0 : v;
+    }
+    return 1.0f;
+  }
+  __device__ __forceinline__ void start_loads() {
+    init_dma();
+    if (part) issue<true>(0);
+    else issue<false>(0);
+#pragma unroll
+    for (int k = 1; k < S * U; ++k) issue<false>(k);
+  }
+
   __device__ __forceinline__ void run() {
-    zero_outside(a);
     const int NT = (a.N + BN - 1) / BN;
-    const int total = expert_tiles<BM>(a);
-    if ((int64_t)blockIdx.x >= (int64_t)total * NT) return;
-    int ti, nt;
-    tile_order(xcd_tile(blockIdx.x, total * NT), total, NT, ti, nt);
-    ExpertTile t = expert_tile<BM>(a, ti);
-    t.e = __builtin_amdgcn_readfirstlane(t.e);
-    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
-    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
-    const int n0 = nt * BN;
-    rows = t.rows;
-    cols = min(BN, a.N - n0);
     lda = (int64_t)a.K * ESZ;
     ldb = KN ? (int64_t)a.N * ESZ : lda;
-    Ab = (const char*)a.A + (int64_t)t.row0 * lda;
-    Bb = (const char*)a.B + (int64_t)t.e * a.N * a.K * ESZ + (KN ? (int64_t)n0 * ESZ : (int64_t)n0 * ldb);
     nk = (a.K + KE - 1) / KE;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    part = (a.K * (int64_t)ESZ) % 128 != 0;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int kb = (a.K + 127) / 128;
-    if constexpr (F8) {
-      sa = a.sa + t.row0;
-      const int nb = (a.N + 127) / 128;
-      sb = a.sb + ((int64_t)t.e * nb + min((n0 + wn * TN) / 128, nb - 1)) * kb;
-    }
+    ExpertTile x;
+    int nt;
+    if (!find_tile<BM>(a, NT, x, nt)) return;
+    Where t;
+    setup(x, nt, wn, t);
+    init_frags(wm, wn);
+    auto nothing = [] {};
     f32x4_t acc[MF][NF];
 #pragma unroll
     for (int f = 0; f < MF; ++f)
 #pragma unroll
       for (int j = 0; j < NF; ++j) acc[f][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    float sbl = 0.0f;      // lane l: the wave's b_scale of k-block (k & ~63) + l
-    auto scale_of = [&](int k) -> float {
-      if constexpr (F8)
-        return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sbl), k & 63));
-      return 1.0f;
-    };
-    auto refill = [&](int k) {
-      if constexpr (F8)
-        if ((k & 63) == 0) sbl = sb[min(k + (int)(threadIdx.x & 63), kb - 1)];
-    };
+    Flow w;
     if constexpr (DMA) {
-      init_dma();
+      if (nk > 0) {
+        start_loads();
+        wait_dma_barrier<D * U*(S - 1)>();
+        begin(wm, w);
+        int k = 0;
+#pragma unroll 1
+        for (; k + U < nk; k += U)
+          static_for<U>([&](auto V) {
+            constexpr int v = V.value;
+            const float sk = scale_of(k + v);
+            if constexpr (v + 1 < U)
+              compute<true>(k + v, wm, sk, acc, w, nothing, nothing);
+            else
+              compute<true>(k + v, wm, sk, acc, w, [&] {
+                wait_dma_barrier<D * U*(S - 2)>();      // the next stage is there, the S - 2 after it may be in flight
+              }, [&] {
 #pragma unroll
-      for (int k = 0; k < S - 1; ++k)
-        if (k < nk) issue(k);
-      for (int k = 0; k < nk; ++k) {
-        // stages k+1 .. min(nk, k+S-1)-1 may still be in flight
-        wait_dma_barrier_rt<D, S - 2>(min(nk - 1 - k, S - 2));
-        refill(k);
-        if (k + S - 1 < nk) issue(k + S - 1);
-        compute(k, wm, wn, scale_of(k), acc);
+                for (int x = 0; x < U; ++x) issue<false>(k + S * U + x);
+              });
+          });
+        // the last stage; blocks past the last one hold zeros
+        static_for<U>([&](auto V) { compute<(V.value + 1 < U)>(k + V.value, wm, scale_of(k + V.value), acc, w, nothing, nothing); });
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       }
     } else {
       Regs g;
       if (nk > 0) load_regs(0, g);
       for (int k = 0; k < nk; ++k) {
-        refill(k);
+        const float sk = scale_of(k);
         store_regs(k, g);
         lds_barrier();
+        if (k == 0) begin(wm, w);
+        else reload(k, wm, w);
         if (k + 1 < nk) load_regs(k + 1, g);
-        compute(k, wm, wn, scale_of(k), acc);
+        compute<false>(k, wm, sk, acc, w, nothing, nothing);
       }
     }
-    with_act(a.act, [&](auto act) { store<decltype(act)::value>(t, n0, wm, wn, acc); });
+    if constexpr (F8)
+      if (nk > 0) add_block(acc[MF - 1], w.p[1], w.sp);
+    float bv[NF][4];
+    load_bias(t, wn, bv);
+    wait_vmem();
+    with_act(a.act, [&](auto act) { store<decltype(act)::value>(t, wm, wn, acc, bv); });
   }
 };
 
-template <int FMT, int BM, int BN, int WM, int WN, int S, bool DMA, bool KN>
+template <int FMT, int BM, int BN, int WM, int WN, int S, int U, bool DMA, bool KN>
 __global__ __launch_bounds__(WM* WN * 64) void expert_gemm_kernel(const ExpertArgs a) {
-  typedef ExpertTileKernel<FMT, BM, BN, WM, WN, S, DMA, KN> TK;
+  typedef ExpertTileKernel<FMT, BM, BN, WM, WN, S, U, DMA, KN> TK;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   TK k(a, smem);
   k.run();
+}
+
+// --- few rows: the weights are streamed once, straight into registers.
+//
+// A wave takes 16 columns of one expert and a slice of its K, 16 * MT rows of
+// tokens at a time (an expert with more rows runs the loop again).  A weight
+// fragment's pieces come from global memory as the matrix instruction takes
+// them (a wave reads whole 128-byte lines of 16 rows), U blocks in flight;
+// with SPL slices the waves' partial sums are added in LDS in slice order.
+// What bounds it is the weights' bytes: no LDS staging, no barrier before the
+// sums, and enough waves that their loads cover the latency of HBM.
+constexpr int kStreamWaves = 8;
+
+template <int FMT, int MT, int U>
+__global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const ExpertArgs a, int SPL) {
+  typedef FmtOps<FMT> Mm;
+  typedef typename Mm::Frag Frag;
+  constexpr bool F8 = Mm::F8;
+  constexpr int ESZ = Mm::ESZ, KE = 128 / ESZ, BM = 16 * MT;
+  __shared__ float part[kStreamWaves][MT * 4][64];
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int CT = kStreamWaves / SPL, NT = (a.N + 16 * CT - 1) / (16 * CT);
+  const int e = blockIdx.x / NT, nt = blockIdx.x - e * NT;
+  int lo, hi;
+  expert_rows(a, e, lo, hi);
+  if (a.offsets) {
+    const int first = clampi(a.offsets[0], 0, a.T), last = max(first, clampi(a.offsets[a.E], 0, a.T));
+    if (first != 0 || last != a.T) zero_outside(a, first, last);
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  if (lo >= hi) return;                     // the whole block
+  const int ct = wave / SPL, sl = wave - ct * SPL;
+  const int n0 = (nt * CT + ct) * 16;
+  const bool live = n0 < a.N;               // whole waves; the barrier below is passed by all
+  const int64_t ld = (int64_t)a.K * ESZ;
+  const int nk = (a.K + KE - 1) / KE, per = (nk + SPL - 1) / SPL;
+  const int k0 = sl * per, k1 = min(nk, k0 + per);
+  const char* W = (const char*)a.B + ((int64_t)e * a.N + min(n0 + i, a.N - 1)) * ld;
+  const float* sb = F8 ? a.sb + ((int64_t)e * ((a.N + 127) / 128) + min(n0, a.N - 1) / 128) * nk : nullptr;
+  const int last_piece = (int)ld - 16;
+
+  for (int row0 = lo; row0 < hi; row0 += BM) {
+    f32x4_t acc[MT];
+    const char* A[MT];
+    int m[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      m[t] = row0 + t * 16 + i;
+      A[t] = (const char*)a.A + (int64_t)min(m[t], hi - 1) * ld;
+    }
+    if (live) {
+#pragma unroll 1
+      for (int k = k0; k < k1; k += U) {
+        u32x4_t wx[U], wy[U], ax[U][MT], ay[U][MT];
+        float sa[U][MT], sw[U];
+        // a block past the slice is read again from its last one, with zero
+        // tokens; so is a piece past K
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int kk = min(k + u, k1 - 1), o = kk * 128 + g * 16;
+          const int ox_ = min(o, last_piece), oy = min(o + 64, last_piece);
+          wx[u] = *(const u32x4_t*)(W + ox_);
+          wy[u] = *(const u32x4_t*)(W + oy);
+          if constexpr (F8) sw[u] = sb[kk];
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            ax[u][t] = *(const u32x4_t*)(A[t] + ox_);
+            ay[u][t] = *(const u32x4_t*)(A[t] + oy);
+            if constexpr (F8) sa[u][t] = a.sa[(int64_t)kk * a.T + min(m[t], hi - 1)];
+          }
+        }
+        const u32x4_t zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int o = (k + u) * 128 + g * 16;
+          const bool in = k + u < k1;
+          const Frag b = Mm::widen(wx[u], wy[u]);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const Frag x = Mm::widen(in && o <= last_piece ? ax[u][t] : zero, in && o + 64 <= last_piece ? ay[u][t] : zero);
+            if constexpr (F8) {
+              const f32x4_t p = Mm::block(b, x);
+              const float s = sa[u][t] * sw[u];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[t][r] = __builtin_fmaf(s, p[r], acc[t][r]);
+            } else {
+              acc[t] = Mm::template half<0>(b, x, acc[t]);
+              acc[t] = Mm::template half<1>(b, x, acc[t]);
+            }
+          }
+        }
+      }
+    }
+    if (SPL > 1) {
+      if (row0 > lo) __syncthreads();
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) part[wave][t * 4 + r][lane] = acc[t][r];
+      __syncthreads();
+      if (sl != 0) continue;
+      for (int q = 1; q < SPL; ++q)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[t][r] += part[wave + q][t * 4 + r][lane];
+    }
+    if (!live) continue;
+    const int n = n0 + g * 4;
+    float bv[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      bv[r] = 0.0f;
+      if (a.bias && n + r < a.N) {
+        const int64_t at = (int64_t)e * a.N + n + r;
+        bv[r] = a.out_dt == DT_F32 ? ((const float*)a.bias)[at] : bf16_to_f32(((const uint16_t*)a.bias)[at]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      if (m[t] >= hi) continue;
+      float v[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = apply_act(a.act, acc[t][r] + bv[r]);
+      const int64_t at = (int64_t)m[t] * a.N + n;
+      if (a.out_dt == DT_F32) {
+        float* y = (float*)a.Y + at;
+        if (a.y_vec) {
+          if (n < a.N) *(f32x4_t*)y = f32x4_t{v[0], v[1], v[2], v[3]};
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (n + r < a.N) y[r] = v[r];
+        }
+      } else {
+        uint16_t* y = (uint16_t*)a.Y + at;
+        const u32x2_t o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        if (a.y_vec) {
+          if (n < a.N) *(u32x2_t*)y = o;
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (n + r < a.N) y[r] = (uint16_t)(o[r / 2] >> (16 * (r % 2)));
+        }
+      }
+    }
+  }
+}
+
+template <int FMT, int MT, int U>
+int launch_expert_stream(const ExpertArgs& a, hipStream_t s) {
+  // slices of at least U blocks of K, so that a wave has U blocks in flight
+  const int nk = (a.K + 128 / FmtOps<FMT>::ESZ - 1) / (128 / FmtOps<FMT>::ESZ);
+  int spl = 1;
+  while (spl < kStreamWaves && nk > spl * U) spl *= 2;
+  const int ct = kStreamWaves / spl;
+  const int64_t blocks = (int64_t)a.E * ((a.N + 16 * ct - 1) / (16 * ct));
+  if (blocks >= ((int64_t)1 << 31)) return (int)hipErrorInvalidValue;
+  hipLaunchKernelGGL((expert_stream_kernel<FMT, MT, U>), dim3((uint32_t)blocks), dim3(kStreamWaves * 64), 0, s, a, spl);
+  return (int)hipGetLastError();
+}
+
+// --- which tile
+//
+// A tile's time on this card, measured over uniform problems (microseconds):
+// a round of blocks, one on each of the 256 CUs, takes o + c1 * nk for nk
+// blocks of 128 bytes of K; with `per` blocks on every CU, o + c * nk.
+struct TileCost {
+  int bm, bn, per;
+  double o, c1, c;
+};
+constexpr int kCus = 256;
+
+// The estimate for this call.  The host knows only the rows per expert on
+// average: an expert's last tile is taken to be half full.
+inline double tile_time(const ExpertArgs& a, int esz, const TileCost& t) {
+  const double experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1, rows = a.T / experts;
+  double tall = (a.T + t.bm - 1) / t.bm;
+  if (experts > 1) tall = experts * (rows / t.bm + 0.5 > 1 ? rows / t.bm + 0.5 : 1);
+  const double tiles = tall * ((a.N + t.bn - 1) / t.bn), nk = ((int64_t)a.K * esz + 127) / 128;
+  const double slots = (double)kCus * t.per;
+  const double full = (double)(int64_t)(tiles / slots), rest = tiles - full * slots;
+  double time = full * (t.o + t.c * nk);
+  if (rest > 0) {
+    // (as slow as the CUs that hold the most blocks)
+    const int most = (int)((rest + kCus - 1) / kCus);
+    time += t.o + nk * (t.c1 + (t.per > 1 ? (t.c - t.c1) * (most - 1) / (t.per - 1) : 0));
+  }
+  return time;
+}
+template <int N>
+inline int best_tile(const ExpertArgs& a, int esz, const TileCost (&t)[N]) {
+  int best = 0;
+  for (int i = 1; i < N; ++i)
+    if (tile_time(a, esz, t[i]) < tile_time(a, esz, t[best])) best = i;
+  return best;
+}
+
+// Reading the weights of every expert that can have rows, at 5 TB/s.
+inline double weights_time(const ExpertArgs& a, int esz) {
+  const double experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1;
+  return experts * a.N * a.K * esz / 5e6;
+}
+
+// Whether the rows are few and the tiles too few to fill the chip with K
+// undivided (one token through 4096 x 4096 e4m3: 6.0 us streamed with K in
+// eight slices, 12.4 us on 32 x 64 tiles; 16 rows over 8 experts of
+// 4096 x 1024 bf16, 512 tiles: 14.4 us streamed, 12.0 on tiles).
+inline bool stream_pays(const ExpertArgs& a, int esz) {
+  const int64_t experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1;
+  return (a.T + experts - 1) / experts <= 64 && experts * ((a.N + 63) / 64) < kCus && (int64_t)a.K * esz >= 1024;
 }
 
 // The most row tiles that any offsets can give.
@@ -542,14 +950,23 @@ inline int64_t expert_tile_bound(const ExpertArgs& a, int BM) {
   return (int64_t)a.T / BM + (a.E < a.T ? a.E : a.T);
 }
 
-template <int FMT, int BM, int BN, int WM, int WN, int S, bool DMA, bool KN>
+template <int FMT, int BM, int BN, int WM, int WN, int S, int U, bool DMA, bool KN>
 int launch_expert_tile(const ExpertArgs& a, hipStream_t s) {
-  typedef ExpertTileKernel<FMT, BM, BN, WM, WN, S, DMA, KN> TK;
+  typedef ExpertTileKernel<FMT, BM, BN, WM, WN, S, U, DMA, KN> TK;
   int64_t blocks = expert_tile_bound(a, BM) * ((a.N + BN - 1) / BN);
   if (blocks >= ((int64_t)1 << 31)) return (int)hipErrorInvalidValue;
-  hipLaunchKernelGGL((expert_gemm_kernel<FMT, BM, BN, WM, WN, S, DMA, KN>), dim3((uint32_t)blocks), dim3(TK::TH),
+  hipLaunchKernelGGL((expert_gemm_kernel<FMT, BM, BN, WM, WN, S, U, DMA, KN>), dim3((uint32_t)blocks), dim3(TK::TH),
                      TK::LDS_BYTES, s, a);
   return (int)hipGetLastError();
+}
+
+// 16, 32 or 64 rows at a time, by the rows per expert on average
+template <int FMT>
+int launch_expert_few(const ExpertArgs& a, hipStream_t s) {
+  const int64_t experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1, rows = (a.T + experts - 1) / experts;
+  if (rows <= 16) return launch_expert_stream<FMT, 1, 4>(a, s);
+  if (rows <= 32) return launch_expert_stream<FMT, 2, 2>(a, s);
+  return launch_expert_stream<FMT, 4, 1>(a, s);
 }
 
 }  // namespace ox

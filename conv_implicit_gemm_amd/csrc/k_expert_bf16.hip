@@ -3,10 +3,39 @@
 
 namespace ox {
 
+namespace {
+
+constexpr TileCost kTiles[] = {{32, 64, 4, 2.5, 0.30, 0.60},
+                               {64, 64, 3, 2.5, 0.42, 0.57},
+                               {128, 128, 2, 5.3, 0.75, 1.16},
+                               {256, 128, 1, 8.0, 0.91, 0.91},
+                               {256, 256, 1, 11.3, 1.65, 1.65}};
+
+template <bool KN>
+int launch(const ExpertArgs& a, hipStream_t s) {
+  if (!a.vec) return launch_expert_tile<FMT_BF16, 64, 64, 2, 2, 2, 1, false, KN>(a, s);
+  if constexpr (!KN) {
+    if (stream_pays(a, 2)) return launch_expert_few<FMT_BF16>(a, s);
+  }
+  const int best = best_tile(a, 2, kTiles);
+  // [K, N] weights that take longer to read than to multiply: blocks as wide
+  // as 256 bytes of their rows (64 experts of 2048 x 1024, 4003 rows: 61 us,
+  // 70 us on 64 x 64 and 68 us on 256 x 256)
+  if (KN && tile_time(a, 2, kTiles[best]) < weights_time(a, 2))
+    return launch_expert_tile<FMT_BF16, 64, 128, 1, 4, 3, 1, true, KN>(a, s);
+  switch (best) {
+    case 0: return launch_expert_tile<FMT_BF16, 32, 64, 1, 4, 3, 1, true, KN>(a, s);
+    case 1: return launch_expert_tile<FMT_BF16, 64, 64, 2, 2, 3, 1, true, KN>(a, s);
+    case 2: return launch_expert_tile<FMT_BF16, 128, 128, 2, 4, 2, 1, true, KN>(a, s);
+    case 3: return launch_expert_tile<FMT_BF16, 256, 128, 4, 2, 3, 1, true, KN>(a, s);
+    default: return launch_expert_tile<FMT_BF16, 256, 256, 2, 4, 2, 1, true, KN>(a, s);
+  }
+}
+
+}  // namespace
+
 int launch_expert_bf16(const ExpertArgs& a, void* stream) {
-  hipStream_t s = (hipStream_t)stream;
-  if (a.kn) return launch_expert_tile<FMT_BF16, 64, 64, 2, 2, 2, false, true>(a, s);
-  return launch_expert_tile<FMT_BF16, 64, 64, 2, 2, 2, false, false>(a, s);
+  return a.kn ? launch<true>(a, (hipStream_t)stream) : launch<false>(a, (hipStream_t)stream);
 }
 
 }  // namespace ox

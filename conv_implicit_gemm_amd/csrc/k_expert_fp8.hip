@@ -4,10 +4,37 @@
 
 namespace ox {
 
+namespace {
+
+// codes straight to the matrix unit (bf16 results)
+constexpr TileCost kCodes[] = {{32, 64, 4, 2.5, 0.30, 0.60},
+                               {64, 64, 3, 2.5, 0.42, 0.57},
+                               {128, 128, 2, 5.3, 0.69, 1.07},
+                               {256, 256, 1, 11.3, 1.68, 1.68}};
+// codes widened to bf16 (fp32 results)
+constexpr TileCost kWide[] = {{32, 64, 4, 2.5, 0.50, 0.90},
+                              {64, 64, 3, 2.5, 0.63, 0.93},
+                              {128, 128, 2, 5.3, 1.00, 2.20},
+                              {128, 256, 1, 6.0, 1.90, 1.90}};
+
+template <int FMT>
+int launch(const ExpertArgs& a, hipStream_t s) {
+  if (!a.vec) return launch_expert_tile<FMT, 64, 64, 2, 2, 2, 1, false, false>(a, s);
+  if (stream_pays(a, 1)) return launch_expert_few<FMT>(a, s);
+  switch (FMT == FMT_FP8 ? best_tile(a, 1, kCodes) : best_tile(a, 1, kWide)) {
+    case 0: return launch_expert_tile<FMT, 32, 64, 1, 4, 3, 1, true, false>(a, s);
+    case 1: return launch_expert_tile<FMT, 64, 64, 2, 2, 3, 1, true, false>(a, s);
+    case 2: return launch_expert_tile<FMT, 128, 128, 2, 4, 2, 1, true, false>(a, s);
+    default:
+      if constexpr (FMT == FMT_FP8) return launch_expert_tile<FMT, 256, 256, 2, 4, 2, 1, true, false>(a, s);
+      else return launch_expert_tile<FMT, 128, 256, 2, 4, 2, 1, true, false>(a, s);
+  }
+}
+
+}  // namespace
+
 int launch_expert_fp8(const ExpertArgs& a, void* stream) {
-  hipStream_t s = (hipStream_t)stream;
-  if (a.out_dt == DT_F32) return launch_expert_tile<FMT_FP8X, 64, 64, 2, 2, 2, false, false>(a, s);
-  return launch_expert_tile<FMT_FP8, 64, 64, 2, 2, 2, false, false>(a, s);
+  return a.out_dt == DT_F32 ? launch<FMT_FP8X>(a, (hipStream_t)stream) : launch<FMT_FP8>(a, (hipStream_t)stream);
 }
 
 }  // namespace ox

@@ -115,5 +115,11 @@ def test_binding_checks_shapes_and_types(ox):
         ox.ox_quantize_fp8(X, index=off.long())
     with pytest.raises(ValueError):
         ox.ox_quantize_fp8(X, scales=torch.zeros(4, 1))
-    with pytest.raises(ox.OxError):
-        ox.ox_quantize_fp8(X, block_rows=32, stream=0)
+    with pytest.raises(ValueError):
+        ox.ox_quantize_fp8(X, block_rows=32)
+    with pytest.raises(ValueError):
+        ox.ox_quantize_fp8(X, index=off, block_rows=128)
+    with pytest.raises(ValueError):
+        ox.ox_quantize_fp8(X)                                  # host memory
+    with pytest.raises(ValueError):
+        ox.ox_gemm_grouped(X, W, off)
