@@ -6,7 +6,8 @@
 //
 // One correctly rounded division per block; the elements are multiplied by
 // the rounded 448 / m.  Sixteen lanes share a row's block, eight elements
-// each; the maximum crosses them with four DPP steps.
+// each; the maximum crosses them with four DPP steps.  What bounds it is the
+// bytes: each element is read once and its code written once.
 #include "engine.hpp"
 
 namespace ox {
@@ -62,18 +63,29 @@ __device__ __forceinline__ float amax8(const float (&x)[8]) {
 
 // the maximum over the sixteen lanes of a row's block
 __device__ __forceinline__ float max16(float m) {
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+  // lane ^ 1, ^ 2 within quads, then the mirrored half row and row (every
+  // lane of a quad, of a half row, already agrees)
+  auto step = [&](auto ctrl) {
+    const int o = __builtin_amdgcn_mov_dpp(__float_as_int(m), decltype(ctrl)::value, 0xf, 0xf, true);
+    m = fmaxf(m, __int_as_float(o));
+  };
+  step(std::integral_constant<int, 0xB1>{});    // quad_perm 1,0,3,2
+  step(std::integral_constant<int, 0x4E>{});    // quad_perm 2,3,0,1
+  step(std::integral_constant<int, 0x141>{});   // row_half_mirror
+  step(std::integral_constant<int, 0x140>{});   // row_mirror
   return m;
 }
 
-// Eight codes.  An infinite product is an infinite x: +-448.
+// Eight codes.  INF: an infinite x gives +-448 (asked for only where the block
+// holds one; finite products cannot leave the format, |x| * (448 / m) <= 448
+// but for roundings that the conversion takes back).
+template <bool INF>
 __device__ __forceinline__ u32x2_t codes8(const float (&x)[8], float r) {
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     v[i] = x[i] * r;
-    if (__builtin_isinf(v[i])) v[i] = __builtin_copysignf(kMax, v[i]);
+    if (INF && __builtin_isinf(v[i])) v[i] = __builtin_copysignf(kMax, v[i]);
   }
   int lo = 0, hi = 0;
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
@@ -95,29 +107,56 @@ __device__ __forceinline__ void store8(const QuantF8Args& a, int r, int k, u32x2
   }
 }
 
-// A scale per row and block: each wave takes one row's four blocks (512
-// columns).
-template <bool F32, bool VEC>
+// A scale per row and block.  A wave takes RW rows' four blocks (512 columns):
+// all RW loads go out before the first maximum, and a block's scales of RW
+// consecutive rows, which lie side by side, leave as one store.
+template <bool F32, bool VEC, int RW>
 __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const QuantF8Args a) {
   const int lane = threadIdx.x & 63;
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int per = (a.K + 511) / 512;
-  const int r = (int)(unit / per), k = (int)(unit - (int64_t)r * per) * 512 + lane * 8;
-  if (r >= a.R) return;
-  const int src = a.index ? a.index[r] : r;
-  float x[8];
-  if (src >= 0 && src < a.rows) {
-    load8<F32, VEC>(a, src, k, x);
-  } else {
+  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + wave;
+  const int r0 = (int)(unit / per) * RW, k = (int)(unit % per) * 512 + lane * 8;
+  if (r0 >= a.R) return;
+  int src[RW];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+  for (int i = 0; i < RW; ++i) {
+    const int r = min(r0 + i, a.R - 1);
+    src[i] = a.index ? a.index[r] : r;
   }
-  float m = max16(amax8<false>(x));
-  if (m == __builtin_inff()) m = max16(amax8<true>(x));   // (all sixteen lanes agree)
-  m = fmaxf(m, kTiny);
-  if (k < a.K) {
-    if ((lane & 15) == 0) a.scales[(int64_t)(k >> 7) * a.R + r] = m / kMax;
-    store8<VEC>(a, r, k, codes8(x, kMax / m));
+  float x[RW][8];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    // (an index outside X reads row 0 and is then zeroed; X may have no row)
+    const bool in = src[i] >= 0 && src[i] < a.rows;
+    if (a.rows > 0) load8<F32, VEC>(a, in ? src[i] : 0, k, x[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[i][j] = in ? x[i][j] : 0.0f;
+  }
+  float sc[RW];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    float m = max16(amax8<false>(x[i]));
+    u32x2_t q;
+    if (m == __builtin_inff()) {                               // (all sixteen lanes agree)
+      m = fmaxf(max16(amax8<true>(x[i])), kTiny);
+      q = codes8<true>(x[i], kMax / m);
+    } else {
+      m = fmaxf(m, kTiny);
+      q = codes8<false>(x[i], kMax / m);
+    }
+    sc[i] = m / kMax;
+    if (k < a.K && r0 + i < a.R) store8<VEC>(a, r0 + i, k, q);
+  }
+  if (k < a.K && (lane & 15) == 0) {
+    float* s = a.scales + (int64_t)(k >> 7) * a.R + r0;
+    if (RW == 4 && a.R % 4 == 0 && (uintptr_t)a.scales % 16 == 0) {
+      *(f32x4_t*)s = f32x4_t{sc[0], sc[1 % RW], sc[2 % RW], sc[3 % RW]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < RW; ++i)
+        if (r0 + i < a.R) s[i] = sc[i];
+    }
   }
 }
 
@@ -156,15 +195,18 @@ __global__ __launch_bounds__(kThreads) void quant_tiles_kernel(const QuantF8Args
   const float r = kMax / m;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (r0 + 16 * i < a.R) store8<VEC>(a, r0 + 16 * i, k, codes8(x[i], r));
+    if (r0 + 16 * i < a.R) store8<VEC>(a, r0 + 16 * i, k, codes8<true>(x[i], r));
 }
 
 template <bool F32, bool VEC>
 int launch(const QuantF8Args& a, hipStream_t s) {
-  const int64_t units = (int64_t)a.R * ((a.K + 511) / 512);
   if (a.block_rows == 1) {
-    const int64_t blocks = (units + kThreads / 64 - 1) / (kThreads / 64);
-    hipLaunchKernelGGL((quant_rows_kernel<F32, VEC>), dim3((uint32_t)blocks), dim3(kThreads), 0, s, a);
+    // four rows a wave once that still gives every CU 16 waves
+    const int64_t per = (a.K + 511) / 512;
+    const int rw = (int64_t)a.R * per >= 4 * 256 * 16 ? 4 : 1;
+    const int64_t blocks = ((a.R + rw - 1) / rw * per + kThreads / 64 - 1) / (kThreads / 64);
+    if (rw == 4) hipLaunchKernelGGL((quant_rows_kernel<F32, VEC, 4>), dim3((uint32_t)blocks), dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((quant_rows_kernel<F32, VEC, 1>), dim3((uint32_t)blocks), dim3(kThreads), 0, s, a);
   } else {
     const int64_t blocks = (int64_t)((a.R + 127) / 128) * ((a.K + 127) / 128);
     hipLaunchKernelGGL((quant_tiles_kernel<F32, VEC>), dim3((uint32_t)blocks), dim3(kThreads), 0, s, a);
