@@ -225,13 +225,15 @@ __device__ __forceinline__ bool find_tile(const ExpertArgs& a, int NT, ExpertTil
 }
 
 // The tile kernel: BM rows x BN columns per block, WM x WN waves, S stages of
-// U blocks of 128 bytes of K.  DMA: both operands arrive by buffer-to-LDS loads (16-byte
+// KS blocks of 128 bytes of K: KS groups of WM x WN waves take one block of
+// each stage and their sums are added at the end, in order (with few tiles a
+// stage costs its latency, not its products: KS = 2 halves the stages).  DMA: both operands arrive by buffer-to-LDS loads (16-byte
 // aligned rows); otherwise through registers, from any address.  KN (bf16):
 // B is [K, N] per expert; its stage holds 64 (fp32: 32) rows of BN columns, read
 // back with transposing LDS reads.
-template <int FMT, int BM, int BN, int WM, int WN, int S, int U, bool DMA, bool KN>
+template <int FMT, int BM, int BN, int WM, int WN, int S, int KS, bool DMA, bool KN>
 struct ExpertTileKernel {
-  static constexpr int NW = WM * WN, TH = NW * 64;
+  static constexpr int NW = WM * WN, TH = NW * KS * 64;     // waves of a group, threads of a block
   static constexpr int TM = BM / WM, TN = BN / WN, MF = TM / 16, NF = TN / 16;
   typedef FmtOps<FMT> Mm;
   typedef typename Mm::Frag Frag;
@@ -244,11 +246,12 @@ struct ExpertTileKernel {
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   static constexpr int SA_BYTES = F8 ? (BM < 64 ? 64 : BM) * 4 : 0;
   static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES;
-  static constexpr int LDS_BYTES = S * U * STAGE;
+  static constexpr int LDS_BYTES = S * KS * STAGE;
+  static_assert(KS == 1 || LDS_BYTES >= (KS - 1) * BM * BN * 4, "the groups' sums go through the stages' memory");
   static constexpr int DA = BM / 8 / NW, DB = BN / 8 / NW;   // DMA instructions per wave and stage
   static constexpr int D = DA + DB + (F8 ? 1 : 0);
   static_assert(!DMA || (DA * NW * 8 == BM && DB * NW * 8 == BN), "whole DMA instructions per wave");
-  static_assert(DMA || U == 1, "one block per stage through registers");
+  static_assert(DMA || KS == 1, "one block per stage through registers");
   static_assert(MF % 2 == 0, "row fragments alternate between two sets of block sums");
   static_assert(!KN || (NF & (NF - 1)) == 0, "fragments are bits of the column");
   static_assert(!KN || !F8, "e4m3 weights are [N, K]");
@@ -273,16 +276,16 @@ struct ExpertTileKernel {
   const float* sb;       // b_scales of this wave's block row
   int rows, cols;        // valid rows and columns of the tile
   int64_t lda, ldb;      // row strides in bytes
-  int nk, wave;
+  int nk, gwave;         // blocks of K; this wave in its group, which loads the blocks that it multiplies
   uint32_t va[DA ? DA : 1], vb[DB ? DB : 1], vs;
 
   __device__ __forceinline__ ExpertTileKernel(const ExpertArgs& a_, char* s) : a(a_), smem(s) {}
 
-  __device__ __forceinline__ uint32_t stage_base(int k) const { return lds_addr(smem) + (uint32_t)(k % (S * U)) * STAGE; }
+  __device__ __forceinline__ uint32_t stage_base(int k) const { return lds_addr(smem) + (uint32_t)(k % (S * KS)) * STAGE; }
 
   // --- DMA staging
   __device__ __forceinline__ void init_dma() {
-    const int lane = threadIdx.x & 63, w = wave;
+    const int lane = threadIdx.x & 63, w = gwave;
 #pragma unroll
     for (int i = 0; i < DA; ++i) {
       const int r = (w * DA + i) * 8 + (lane >> 3);
@@ -314,7 +317,7 @@ struct ExpertTileKernel {
   // traffic), which keeps the number of loads in flight the same for all.
   template <bool PART>
   __device__ __forceinline__ void issue(int k) {
-    const int lane = threadIdx.x & 63, w = wave;
+    const int lane = threadIdx.x & 63, w = gwave;
     const uint32_t base = __builtin_amdgcn_readfirstlane(stage_base(k));
     const bool any = k < nk;
     const int kb = any ? block_of(k) : 0;
@@ -382,7 +385,7 @@ struct ExpertTileKernel {
     if constexpr (F8) g.s = (int)threadIdx.x < rows ? sa[(int64_t)k * a.T + threadIdx.x] : 0.0f;
   }
   __device__ __forceinline__ void store_regs(int k, const Regs& g) {
-    char* st = smem + (k % (S * U)) * STAGE;
+    char* st = smem + (k % (S * KS)) * STAGE;
 #pragma unroll
     for (int i = 0; i < CA; ++i) *(u32x4_t*)(st + (threadIdx.x + i * TH) * 16) = g.ra[i];
 #pragma unroll
@@ -470,8 +473,8 @@ struct ExpertTileKernel {
 #pragma unroll
     for (int j = 0; j < NF; ++j) read_b(st, j, w);
   }
-  __device__ __forceinline__ void begin(int wm, Flow& w) const {
-    reload(0, wm, w);
+  __device__ __forceinline__ void begin(int k, int wm, Flow& w) const {
+    reload(k, wm, w);
 #pragma unroll
     for (int j = 0; j < NF; ++j) w.p[1][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     w.sp = 0.0f;
@@ -492,7 +495,7 @@ struct ExpertTileKernel {
   template <bool NEXT, class Turn, class Refill>
   __device__ __forceinline__ void compute(int k, int wm, float sbk, f32x4_t (&acc)[MF][NF], Flow& w, Turn&& turn,
                                           Refill&& refill) {
-    const uint32_t st = stage_base(k), st1 = stage_base(k + 1);
+    const uint32_t st = stage_base(k), st1 = stage_base(k + KS);
     static_for<MF>([&](auto F) {
       constexpr int f = F.value;
       constexpr bool last = f + 1 == MF, load = !last || NEXT;
@@ -646,12 +649,12 @@ struct ExpertTileKernel {
     }
     return 1.0f;
   }
-  __device__ __forceinline__ void start_loads() {
+  __device__ __forceinline__ void start_loads(int grp) {
     init_dma();
-    if (part) issue<true>(0);
-    else issue<false>(0);
+    if (part && grp == 0) issue<true>(0);
+    else issue<false>(grp);
 #pragma unroll
-    for (int k = 1; k < S * U; ++k) issue<false>(k);
+    for (int x = 1; x < S; ++x) issue<false>(x * KS + grp);
   }
 
   __device__ __forceinline__ void run() {
@@ -660,8 +663,9 @@ struct ExpertTileKernel {
     ldb = KN ? (int64_t)a.N * ESZ : lda;
     nk = (a.K + KE - 1) / KE;
     part = (a.K * (int64_t)ESZ) % 128 != 0;
-    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / WN, wn = wave % WN;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wave / NW;
+    gwave = wave % NW;
+    const int wm = gwave / WN, wn = gwave % WN;
     ExpertTile x;
     int nt;
     if (!find_tile<BM>(a, NT, x, nt)) return;
@@ -677,27 +681,19 @@ struct ExpertTileKernel {
     Flow w;
     if constexpr (DMA) {
       if (nk > 0) {
-        start_loads();
-        wait_dma_barrier<D * U*(S - 1)>();
-        begin(wm, w);
+        start_loads(grp);
+        wait_dma_barrier<D*(S - 1)>();
+        begin(grp, wm, w);
         int k = 0;
 #pragma unroll 1
-        for (; k + U < nk; k += U)
-          static_for<U>([&](auto V) {
-            constexpr int v = V.value;
-            const float sk = scale_of(k + v);
-            if constexpr (v + 1 < U)
-              compute<true>(k + v, wm, sk, acc, w, nothing, nothing);
-            else
-              compute<true>(k + v, wm, sk, acc, w, [&] {
-                wait_dma_barrier<D * U*(S - 2)>();      // the next stage is there, the S - 2 after it may be in flight
-              }, [&] {
-#pragma unroll
-                for (int x = 0; x < U; ++x) issue<false>(k + S * U + x);
-              });
-          });
-        // the last stage; blocks past the last one hold zeros
-        static_for<U>([&](auto V) { compute<(V.value + 1 < U)>(k + V.value, wm, scale_of(k + V.value), acc, w, nothing, nothing); });
+        for (; k + KS < nk; k += KS) {
+          const float sk = scale_of(k + grp);
+          compute<true>(k + grp, wm, sk, acc, w, [&] {
+            wait_dma_barrier<D*(S - 2)>();      // the next stage is there, the S - 2 after it may be in flight
+          }, [&] { issue<false>(k + S * KS + grp); });
+        }
+        // (a block past the last one holds zeros)
+        compute<false>(k + grp, wm, scale_of(k + grp), acc, w, nothing, nothing);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       }
     } else {
@@ -707,7 +703,7 @@ struct ExpertTileKernel {
         const float sk = scale_of(k);
         store_regs(k, g);
         lds_barrier();
-        if (k == 0) begin(wm, w);
+        if (k == 0) begin(0, wm, w);
         else reload(k, wm, w);
         if (k + 1 < nk) load_regs(k + 1, g);
         compute<false>(k, wm, sk, acc, w, nothing, nothing);
@@ -715,6 +711,30 @@ struct ExpertTileKernel {
     }
     if constexpr (F8)
       if (nk > 0) add_block(acc[MF - 1], w.p[1], w.sp);
+    if constexpr (KS > 1) {
+      // the groups' sums, through the stages' memory: this lane's results side
+      // by side, 16 bytes apart from the next lane's
+      lds_barrier();
+      f32x4_t* part = (f32x4_t*)smem + (gwave * MF * NF) * 64 + (threadIdx.x & 63);
+      if (grp > 0) {
+#pragma unroll
+        for (int f = 0; f < MF; ++f)
+#pragma unroll
+          for (int j = 0; j < NF; ++j) part[((grp - 1) * NW * MF * NF + f * NF + j) * 64] = acc[f][j];
+      }
+      __syncthreads();
+      if (grp > 0) return;
+#pragma unroll
+      for (int q = 0; q < KS - 1; ++q)
+#pragma unroll
+        for (int f = 0; f < MF; ++f)
+#pragma unroll
+          for (int j = 0; j < NF; ++j) {
+            const f32x4_t o = part[(q * NW * MF * NF + f * NF + j) * 64];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[f][j][r] += o[r];
+          }
+    }
     float bv[NF][4];
     load_bias(t, wn, bv);
     wait_vmem();
@@ -722,9 +742,9 @@ struct ExpertTileKernel {
   }
 };
 
-template <int FMT, int BM, int BN, int WM, int WN, int S, int U, bool DMA, bool KN>
-__global__ __launch_bounds__(WM* WN * 64) void expert_gemm_kernel(const ExpertArgs a) {
-  typedef ExpertTileKernel<FMT, BM, BN, WM, WN, S, U, DMA, KN> TK;
+template <int FMT, int BM, int BN, int WM, int WN, int S, int KS, bool DMA, bool KN>
+__global__ __launch_bounds__(WM* WN* KS * 64) void expert_gemm_kernel(const ExpertArgs a) {
+  typedef ExpertTileKernel<FMT, BM, BN, WM, WN, S, KS, DMA, KN> TK;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   TK k(a, smem);
   k.run();
@@ -732,22 +752,23 @@ __global__ __launch_bounds__(WM* WN * 64) void expert_gemm_kernel(const ExpertAr
 
 // --- few rows: the weights are streamed once, straight into registers.
 //
-// A wave takes 16 columns of one expert and a slice of its K, 16 * MT rows of
+// A wave takes 16 columns of one expert and a slice of its K, 16 rows of
 // tokens at a time (an expert with more rows runs the loop again).  A weight
 // fragment's pieces come from global memory as the matrix instruction takes
-// them (a wave reads whole 128-byte lines of 16 rows), U blocks in flight;
-// with SPL slices the waves' partial sums are added in LDS in slice order.
-// What bounds it is the weights' bytes: no LDS staging, no barrier before the
-// sums, and enough waves that their loads cover the latency of HBM.
-constexpr int kStreamWaves = 8;
+// them (a wave reads whole 128-byte lines of 16 rows), kStreamDepth blocks in
+// flight; with SPL slices the waves' partial sums are added in LDS in slice
+// order.  What bounds it is the weights' bytes and one trip to HBM: no LDS
+// staging, no barrier before the sums, and enough waves that their loads cover
+// the latency.
+constexpr int kStreamWaves = 8, kStreamDepth = 4;
 
-template <int FMT, int MT, int U>
+template <int FMT>
 __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const ExpertArgs a, int SPL) {
   typedef FmtOps<FMT> Mm;
   typedef typename Mm::Frag Frag;
   constexpr bool F8 = Mm::F8;
-  constexpr int ESZ = Mm::ESZ, KE = 128 / ESZ, BM = 16 * MT;
-  __shared__ float part[kStreamWaves][MT * 4][64];
+  constexpr int ESZ = Mm::ESZ, KE = 128 / ESZ, U = kStreamDepth;
+  __shared__ float part[kStreamWaves][4][64];
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int CT = kStreamWaves / SPL, NT = (a.N + 16 * CT - 1) / (16 * CT);
@@ -771,35 +792,28 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
   const float* sb = F8 ? a.sb + ((int64_t)e * ((a.N + 127) / 128) + min(n0, a.N - 1) / 128) * nk : nullptr;
   const int last_piece = (int)ld - 16;
 
-  for (int row0 = lo; row0 < hi; row0 += BM) {
-    f32x4_t acc[MT];
-    const char* A[MT];
-    int m[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      m[t] = row0 + t * 16 + i;
-      A[t] = (const char*)a.A + (int64_t)min(m[t], hi - 1) * ld;
-    }
+  for (int row0 = lo; row0 < hi; row0 += 16) {
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    const int m = row0 + i, mr = min(m, hi - 1);
+    const char* A = (const char*)a.A + (int64_t)mr * ld;
     if (live) {
 #pragma unroll 1
       for (int k = k0; k < k1; k += U) {
-        u32x4_t wx[U], wy[U], ax[U][MT], ay[U][MT];
-        float sa[U][MT], sw[U];
+        u32x4_t wx[U], wy[U], ax[U], ay[U];
+        float sa[U], sw[U];
         // a block past the slice is read again from its last one, with zero
         // tokens; so is a piece past K
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int kk = min(k + u, k1 - 1), o = kk * 128 + g * 16;
-          const int ox_ = min(o, last_piece), oy = min(o + 64, last_piece);
-          wx[u] = *(const u32x4_t*)(W + ox_);
-          wy[u] = *(const u32x4_t*)(W + oy);
-          if constexpr (F8) sw[u] = sb[kk];
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            ax[u][t] = *(const u32x4_t*)(A[t] + ox_);
-            ay[u][t] = *(const u32x4_t*)(A[t] + oy);
-            if constexpr (F8) sa[u][t] = a.sa[(int64_t)kk * a.T + min(m[t], hi - 1)];
+          const int px = min(o, last_piece), py = min(o + 64, last_piece);
+          wx[u] = *(const u32x4_t*)(W + px);
+          wy[u] = *(const u32x4_t*)(W + py);
+          ax[u] = *(const u32x4_t*)(A + px);
+          ay[u] = *(const u32x4_t*)(A + py);
+          if constexpr (F8) {
+            sw[u] = sb[kk];
+            sa[u] = a.sa[(int64_t)kk * a.T + mr];
           }
         }
         const u32x4_t zero = {0u, 0u, 0u, 0u};
@@ -808,18 +822,15 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
           const int o = (k + u) * 128 + g * 16;
           const bool in = k + u < k1;
           const Frag b = Mm::widen(wx[u], wy[u]);
+          const Frag x = Mm::widen(in && o <= last_piece ? ax[u] : zero, in && o + 64 <= last_piece ? ay[u] : zero);
+          if constexpr (F8) {
+            const f32x4_t p = Mm::block(b, x);
+            const float s = sa[u] * sw[u];
 #pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            const Frag x = Mm::widen(in && o <= last_piece ? ax[u][t] : zero, in && o + 64 <= last_piece ? ay[u][t] : zero);
-            if constexpr (F8) {
-              const f32x4_t p = Mm::block(b, x);
-              const float s = sa[u][t] * sw[u];
-#pragma unroll
-              for (int r = 0; r < 4; ++r) acc[t][r] = __builtin_fmaf(s, p[r], acc[t][r]);
-            } else {
-              acc[t] = Mm::template half<0>(b, x, acc[t]);
-              acc[t] = Mm::template half<1>(b, x, acc[t]);
-            }
+            for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(s, p[r], acc[r]);
+          } else {
+            acc = Mm::template half<0>(b, x, acc);
+            acc = Mm::template half<1>(b, x, acc);
           }
         }
       }
@@ -827,69 +838,59 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
     if (SPL > 1) {
       if (row0 > lo) __syncthreads();
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) part[wave][t * 4 + r][lane] = acc[t][r];
+      for (int r = 0; r < 4; ++r) part[wave][r][lane] = acc[r];
       __syncthreads();
       if (sl != 0) continue;
       for (int q = 1; q < SPL; ++q)
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[t][r] += part[wave + q][t * 4 + r][lane];
+        for (int r = 0; r < 4; ++r) acc[r] += part[wave + q][r][lane];
     }
-    if (!live) continue;
     const int n = n0 + g * 4;
-    float bv[4];
+    if (!live || m >= hi || n >= a.N) continue;
+    float v[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      bv[r] = 0.0f;
+      float bv = 0.0f;
       if (a.bias && n + r < a.N) {
         const int64_t at = (int64_t)e * a.N + n + r;
-        bv[r] = a.out_dt == DT_F32 ? ((const float*)a.bias)[at] : bf16_to_f32(((const uint16_t*)a.bias)[at]);
+        bv = a.out_dt == DT_F32 ? ((const float*)a.bias)[at] : bf16_to_f32(((const uint16_t*)a.bias)[at]);
       }
+      v[r] = apply_act(a.act, acc[r] + bv);
     }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      if (m[t] >= hi) continue;
-      float v[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = apply_act(a.act, acc[t][r] + bv[r]);
-      const int64_t at = (int64_t)m[t] * a.N + n;
-      if (a.out_dt == DT_F32) {
-        float* y = (float*)a.Y + at;
-        if (a.y_vec) {
-          if (n < a.N) *(f32x4_t*)y = f32x4_t{v[0], v[1], v[2], v[3]};
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (n + r < a.N) y[r] = v[r];
-        }
+    const int64_t at = (int64_t)m * a.N + n;
+    if (a.out_dt == DT_F32) {
+      float* y = (float*)a.Y + at;
+      if (a.y_vec) {
+        *(f32x4_t*)y = f32x4_t{v[0], v[1], v[2], v[3]};
       } else {
-        uint16_t* y = (uint16_t*)a.Y + at;
-        const u32x2_t o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        if (a.y_vec) {
-          if (n < a.N) *(u32x2_t*)y = o;
-        } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (n + r < a.N) y[r] = (uint16_t)(o[r / 2] >> (16 * (r % 2)));
-        }
+        for (int r = 0; r < 4; ++r)
+          if (n + r < a.N) y[r] = v[r];
+      }
+    } else {
+      uint16_t* y = (uint16_t*)a.Y + at;
+      const u32x2_t o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      if (a.y_vec) {
+        *(u32x2_t*)y = o;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n + r < a.N) y[r] = (uint16_t)(o[r / 2] >> (16 * (r % 2)));
       }
     }
   }
 }
 
-template <int FMT, int MT, int U>
+template <int FMT>
 int launch_expert_stream(const ExpertArgs& a, hipStream_t s) {
-  // slices of at least U blocks of K, so that a wave has U blocks in flight
+  // slices of at least kStreamDepth blocks of K, so that a wave has as many in flight
   const int nk = (a.K + 128 / FmtOps<FMT>::ESZ - 1) / (128 / FmtOps<FMT>::ESZ);
   int spl = 1;
-  while (spl < kStreamWaves && nk > spl * U) spl *= 2;
+  while (spl < kStreamWaves && nk > spl * kStreamDepth) spl *= 2;
   const int ct = kStreamWaves / spl;
   const int64_t blocks = (int64_t)a.E * ((a.N + 16 * ct - 1) / (16 * ct));
   if (blocks >= ((int64_t)1 << 31)) return (int)hipErrorInvalidValue;
-  hipLaunchKernelGGL((expert_stream_kernel<FMT, MT, U>), dim3((uint32_t)blocks), dim3(kStreamWaves * 64), 0, s, a, spl);
+  hipLaunchKernelGGL((expert_stream_kernel<FMT>), dim3((uint32_t)blocks), dim3(kStreamWaves * 64), 0, s, a, spl);
   return (int)hipGetLastError();
 }
 
@@ -935,13 +936,13 @@ inline double weights_time(const ExpertArgs& a, int esz) {
   return experts * a.N * a.K * esz / 5e6;
 }
 
-// Whether the rows are few and the tiles too few to fill the chip with K
-// undivided (one token through 4096 x 4096 e4m3: 6.0 us streamed with K in
-// eight slices, 12.4 us on 32 x 64 tiles; 16 rows over 8 experts of
-// 4096 x 1024 bf16, 512 tiles: 14.4 us streamed, 12.0 on tiles).
+// Whether an expert has one fragment of rows or less and the tiles are too few
+// to fill the chip (one token through 4096 x 4096 e4m3: 6.0 us streamed, 12.4
+// us on 32 x 64 tiles; 16 rows over 8 experts of 4096 x 1024 bf16, 512 tiles:
+// 14.4 us streamed, 12.0 on tiles).
 inline bool stream_pays(const ExpertArgs& a, int esz) {
   const int64_t experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1;
-  return (a.T + experts - 1) / experts <= 64 && experts * ((a.N + 63) / 64) < kCus && (int64_t)a.K * esz >= 1024;
+  return a.T <= 16 * experts && experts * ((a.N + 63) / 64) < kCus && (int64_t)a.K * esz >= 1024;
 }
 
 // The most row tiles that any offsets can give.
@@ -950,23 +951,14 @@ inline int64_t expert_tile_bound(const ExpertArgs& a, int BM) {
   return (int64_t)a.T / BM + (a.E < a.T ? a.E : a.T);
 }
 
-template <int FMT, int BM, int BN, int WM, int WN, int S, int U, bool DMA, bool KN>
+template <int FMT, int BM, int BN, int WM, int WN, int S, int KS, bool DMA, bool KN>
 int launch_expert_tile(const ExpertArgs& a, hipStream_t s) {
-  typedef ExpertTileKernel<FMT, BM, BN, WM, WN, S, U, DMA, KN> TK;
+  typedef ExpertTileKernel<FMT, BM, BN, WM, WN, S, KS, DMA, KN> TK;
   int64_t blocks = expert_tile_bound(a, BM) * ((a.N + BN - 1) / BN);
   if (blocks >= ((int64_t)1 << 31)) return (int)hipErrorInvalidValue;
-  hipLaunchKernelGGL((expert_gemm_kernel<FMT, BM, BN, WM, WN, S, U, DMA, KN>), dim3((uint32_t)blocks), dim3(TK::TH),
+  hipLaunchKernelGGL((expert_gemm_kernel<FMT, BM, BN, WM, WN, S, KS, DMA, KN>), dim3((uint32_t)blocks), dim3(TK::TH),
                      TK::LDS_BYTES, s, a);
   return (int)hipGetLastError();
-}
-
-// 16, 32 or 64 rows at a time, by the rows per expert on average
-template <int FMT>
-int launch_expert_few(const ExpertArgs& a, hipStream_t s) {
-  const int64_t experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1, rows = (a.T + experts - 1) / experts;
-  if (rows <= 16) return launch_expert_stream<FMT, 1, 4>(a, s);
-  if (rows <= 32) return launch_expert_stream<FMT, 2, 2>(a, s);
-  return launch_expert_stream<FMT, 4, 1>(a, s);
 }
 
 }  // namespace ox

@@ -9,13 +9,16 @@ constexpr TileCost kTiles[] = {{32, 64, 4, 2.5, 0.30, 0.60},
                                {64, 64, 3, 2.5, 0.42, 0.57},
                                {128, 128, 2, 5.3, 0.75, 1.16},
                                {256, 128, 1, 8.0, 0.91, 0.91},
-                               {256, 256, 1, 11.3, 1.65, 1.65}};
+                               {256, 256, 1, 11.3, 1.65, 1.65},
+                               {32, 32, 2, 3.0, 0.19, 0.22},       // K in four groups
+                               {64, 64, 1, 3.0, 0.285, 0.285},     // in two
+                               {128, 128, 1, 5.5, 0.70, 0.70}};    // in two
 
 template <bool KN>
 int launch(const ExpertArgs& a, hipStream_t s) {
   if (!a.vec) return launch_expert_tile<FMT_BF16, 64, 64, 2, 2, 2, 1, false, KN>(a, s);
   if constexpr (!KN) {
-    if (stream_pays(a, 2)) return launch_expert_few<FMT_BF16>(a, s);
+    if (stream_pays(a, 2)) return launch_expert_stream<FMT_BF16>(a, s);
   }
   const int best = best_tile(a, 2, kTiles);
   // [K, N] weights that take longer to read than to multiply: blocks as wide
@@ -28,6 +31,9 @@ int launch(const ExpertArgs& a, hipStream_t s) {
     case 1: return launch_expert_tile<FMT_BF16, 64, 64, 2, 2, 3, 1, true, KN>(a, s);
     case 2: return launch_expert_tile<FMT_BF16, 128, 128, 2, 4, 2, 1, true, KN>(a, s);
     case 3: return launch_expert_tile<FMT_BF16, 256, 128, 4, 2, 3, 1, true, KN>(a, s);
+    case 5: return launch_expert_tile<FMT_BF16, 32, 32, 1, 2, 2, 4, true, KN>(a, s);
+    case 6: return launch_expert_tile<FMT_BF16, 64, 64, 2, 2, 3, 2, true, KN>(a, s);
+    case 7: return launch_expert_tile<FMT_BF16, 128, 128, 2, 4, 2, 2, true, KN>(a, s);
     default: return launch_expert_tile<FMT_BF16, 256, 256, 2, 4, 2, 1, true, KN>(a, s);
   }
 }
