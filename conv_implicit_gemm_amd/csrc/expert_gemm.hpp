@@ -25,6 +25,8 @@
 // chosen so that the 16 rows a read touches fall on all 64 banks.
 #pragma once
 
+#include <string.h>
+
 #include "lds_dma.hpp"
 
 namespace ox {
@@ -816,6 +818,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
             sa[u] = a.sa[(int64_t)kk * a.T + mr];
           }
         }
+        __builtin_amdgcn_sched_barrier(0);      // every load goes out before the first product
         const u32x4_t zero = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -900,6 +903,7 @@ int launch_expert_stream(const ExpertArgs& a, hipStream_t s) {
 // a round of blocks, one on each of the 256 CUs, takes o + c1 * nk for nk
 // blocks of 128 bytes of K; with `per` blocks on every CU, o + c * nk.
 struct TileCost {
+  const char* name;
   int bm, bn, per;
   double o, c1, c;
 };
@@ -929,13 +933,6 @@ inline int best_tile(const ExpertArgs& a, int esz, const TileCost (&t)[N]) {
     if (tile_time(a, esz, t[i]) < tile_time(a, esz, t[best])) best = i;
   return best;
 }
-
-// Reading the weights of every expert that can have rows, at 5 TB/s.
-inline double weights_time(const ExpertArgs& a, int esz) {
-  const double experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1;
-  return experts * a.N * a.K * esz / 5e6;
-}
-
 // Whether an expert has one fragment of rows or less and the tiles are too few
 // to fill the chip (one token through 4096 x 4096 e4m3: 6.0 us streamed, 12.4
 // us on 32 x 64 tiles; 16 rows over 8 experts of 4096 x 1024 bf16, 512 tiles:
@@ -943,6 +940,45 @@ inline double weights_time(const ExpertArgs& a, int esz) {
 inline bool stream_pays(const ExpertArgs& a, int esz) {
   const int64_t experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1;
   return a.T <= 16 * experts && experts * ((a.N + 63) / 64) < kCus && (int64_t)a.K * esz >= 1024;
+}
+
+// The named variant's place in the table, or -1.
+template <int N>
+inline int named_tile(const char* name, const TileCost (&t)[N]) {
+  for (int i = 0; i < N; ++i)
+    if (strcmp(name, t[i].name) == 0) return i;
+  return -1;
+}
+// Which kernel a call takes: an index of its table, or one of these.
+enum Pick : int { PICK_REGS = -2, PICK_REGS_LARGE = -3, PICK_STREAM = -4, PICK_NONE = -1 };
+// Rows from any address go through registers: 128 x 128 tiles once those
+// number two for every CU, else 64 x 64.
+inline int pick_regs(const ExpertArgs& a) {
+  const int64_t experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1;
+  const int64_t tall = a.T / 128 > experts ? a.T / 128 : experts;
+  return tall * ((a.N + 127) / 128) >= 2 * kCus && a.T >= 128 * experts ? PICK_REGS_LARGE : PICK_REGS;
+}
+template <int N>
+inline int pick_variant(ExpertArgs& a, int esz, const TileCost (&t)[N]) {
+  int p;
+  if (a.force) {
+    p = !strcmp(a.force, "regs") ? PICK_REGS : !strcmp(a.force, "regs128") ? PICK_REGS_LARGE
+        : !strcmp(a.force, "stream") && !a.kn && a.vec ? PICK_STREAM : a.vec ? named_tile(a.force, t) : PICK_NONE;
+  } else if (!a.vec) {
+    p = pick_regs(a);
+  } else if (!a.kn && stream_pays(a, esz)) {
+    p = PICK_STREAM;
+  } else {
+    p = best_tile(a, esz, t);
+  }
+  a.chosen = p >= 0 ? t[p].name : p == PICK_REGS ? "regs" : p == PICK_REGS_LARGE ? "regs128" : "stream";
+  return p;
+}
+
+// Reading the weights of every expert that can have rows, at 5 TB/s.
+inline double weights_time(const ExpertArgs& a, int esz) {
+  const double experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1;
+  return experts * a.N * a.K * esz / 5e6;
 }
 
 // The most row tiles that any offsets can give.

@@ -5,42 +5,45 @@ namespace ox {
 
 namespace {
 
-constexpr TileCost kTiles[] = {{32, 64, 4, 2.5, 0.30, 0.60},
-                               {64, 64, 3, 2.5, 0.42, 0.57},
-                               {128, 128, 2, 5.3, 0.75, 1.16},
-                               {256, 128, 1, 8.0, 0.91, 0.91},
-                               {256, 256, 1, 11.3, 1.65, 1.65},
-                               {32, 32, 2, 3.0, 0.19, 0.22},       // K in four groups
-                               {64, 64, 1, 3.0, 0.285, 0.285},     // in two
-                               {128, 128, 1, 5.5, 0.70, 0.70}};    // in two
+// (xN: K divided over N groups of waves)
+constexpr TileCost kTiles[] = {{"32x64", 32, 64, 4, 2.5, 0.30, 0.60},
+                               {"64x64", 64, 64, 3, 2.5, 0.42, 0.57},
+                               {"128x128", 128, 128, 2, 5.3, 0.75, 1.16},
+                               {"256x128", 256, 128, 1, 8.0, 0.91, 0.91},
+                               {"256x256", 256, 256, 1, 11.3, 1.65, 1.65},
+                               {"32x32x4", 32, 32, 2, 3.0, 0.19, 0.22},
+                               {"64x64x2", 64, 64, 1, 3.0, 0.285, 0.285},
+                               {"128x128x2", 128, 128, 1, 5.5, 0.70, 0.70}};
 
 template <bool KN>
-int launch(const ExpertArgs& a, hipStream_t s) {
-  if (!a.vec) return launch_expert_tile<FMT_BF16, 64, 64, 2, 2, 2, 1, false, KN>(a, s);
-  if constexpr (!KN) {
-    if (stream_pays(a, 2)) return launch_expert_stream<FMT_BF16>(a, s);
-  }
-  const int best = best_tile(a, 2, kTiles);
+int launch(ExpertArgs& a, hipStream_t s) {
+  const int p = pick_variant(a, 2, kTiles);
   // [K, N] weights that take longer to read than to multiply: blocks as wide
   // as 256 bytes of their rows (64 experts of 2048 x 1024, 4003 rows: 61 us,
   // 70 us on 64 x 64 and 68 us on 256 x 256)
-  if (KN && tile_time(a, 2, kTiles[best]) < weights_time(a, 2))
+  if (KN && (a.force ? !strcmp(a.force, "64x128") && a.vec : p >= 0 && tile_time(a, 2, kTiles[p]) < weights_time(a, 2))) {
+    a.chosen = "64x128";
     return launch_expert_tile<FMT_BF16, 64, 128, 1, 4, 3, 1, true, KN>(a, s);
-  switch (best) {
+  }
+  switch (p) {
+    case PICK_REGS: return launch_expert_tile<FMT_BF16, 64, 64, 2, 2, 2, 1, false, KN>(a, s);
+    case PICK_REGS_LARGE: return launch_expert_tile<FMT_BF16, 128, 128, 2, 4, 2, 1, false, KN>(a, s);
+    case PICK_STREAM: return launch_expert_stream<FMT_BF16>(a, s);
     case 0: return launch_expert_tile<FMT_BF16, 32, 64, 1, 4, 3, 1, true, KN>(a, s);
     case 1: return launch_expert_tile<FMT_BF16, 64, 64, 2, 2, 3, 1, true, KN>(a, s);
     case 2: return launch_expert_tile<FMT_BF16, 128, 128, 2, 4, 2, 1, true, KN>(a, s);
     case 3: return launch_expert_tile<FMT_BF16, 256, 128, 4, 2, 3, 1, true, KN>(a, s);
+    case 4: return launch_expert_tile<FMT_BF16, 256, 256, 2, 4, 2, 1, true, KN>(a, s);
     case 5: return launch_expert_tile<FMT_BF16, 32, 32, 1, 2, 2, 4, true, KN>(a, s);
     case 6: return launch_expert_tile<FMT_BF16, 64, 64, 2, 2, 3, 2, true, KN>(a, s);
     case 7: return launch_expert_tile<FMT_BF16, 128, 128, 2, 4, 2, 2, true, KN>(a, s);
-    default: return launch_expert_tile<FMT_BF16, 256, 256, 2, 4, 2, 1, true, KN>(a, s);
+    default: return kNoVariant;
   }
 }
 
 }  // namespace
 
-int launch_expert_bf16(const ExpertArgs& a, void* stream) {
+int launch_expert_bf16(ExpertArgs& a, void* stream) {
   return a.kn ? launch<true>(a, (hipStream_t)stream) : launch<false>(a, (hipStream_t)stream);
 }
 

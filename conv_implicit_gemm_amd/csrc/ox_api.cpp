@@ -1085,9 +1085,18 @@ ox_status expert_call(const char* fn, int dt, ox_dtype y_type, int64_t T, int64_
   a.vec = aligned16(A) && aligned16(B) && rowb % 16 == 0 && rowb < (1 << 23) &&
           (transB || (colb % 16 == 0 && colb < (1 << 23)));
   a.y_vec = aligned16(Y) && N * esize(y_type) % 16 == 0;
-  return hip_result(fn, dt == DT_F8 ? launch_expert_fp8(a, stream)
-                        : dt == DT_BF16 ? launch_expert_bf16(a, stream)
-                                        : launch_expert_f32(a, stream));
+  const Force f = read_force();
+  a.force = f.variant;
+  a.chosen = "";
+  const int rc = dt == DT_F8 ? launch_expert_fp8(a, stream)
+                 : dt == DT_BF16 ? launch_expert_bf16(a, stream)
+                                 : launch_expert_f32(a, stream);
+  if (rc == kNoVariant)
+    return fail(OX_ERR_UNSUPPORTED, "%s: OX_FORCE_KERNEL=%s does not apply to this call", fn, f.variant);
+  if (log_on())
+    fprintf(stderr, "[ox] %s %lldx%lldx%lld experts %lld: %s\n", fn, (long long)T, (long long)N, (long long)K,
+            (long long)E, a.chosen);
+  return hip_result(fn, rc);
 }
 
 }  // namespace

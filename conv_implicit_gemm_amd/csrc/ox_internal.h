@@ -295,10 +295,14 @@ struct ExpertArgs {
   int kn;                  // weights are [K, N]
   int vec;                 // A and B: every row starts on 16 bytes, and offsets inside a tile fit 32 bits
   int y_vec;               // Y: rows start on 16 bytes and hold whole 16-byte pieces
+  const char* force;       // a variant's name (OX_FORCE_KERNEL), or null
+  const char* chosen;      // set by the launchers: the variant that runs
 };
-int launch_expert_f32(const ExpertArgs& a, void* stream);
-int launch_expert_bf16(const ExpertArgs& a, void* stream);
-int launch_expert_fp8(const ExpertArgs& a, void* stream);
+// the launchers' answer to a forced variant that this call cannot take
+constexpr int kNoVariant = -1;
+int launch_expert_f32(ExpertArgs& a, void* stream);
+int launch_expert_bf16(ExpertArgs& a, void* stream);
+int launch_expert_fp8(ExpertArgs& a, void* stream);
 
 // Quantisation to e4m3 with one fp32 scale per 1 x 128 or 128 x 128 block.
 struct QuantF8Args {

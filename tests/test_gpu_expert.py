@@ -390,3 +390,45 @@ def test_other_stream_and_graph_replays(ox):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(want, Y), seed
+
+
+# every kernel of the products, forced, on experts with full, partial and no
+# tiles, a last partial block of K (fp8 368 = 2 * 128 + 112) and more blocks
+# than any tile keeps in flight
+VARIANTS = {"fp8": ["regs", "regs128", "stream", "32x64", "64x64", "128x128", "256x256", "32x32x4", "64x64x2", "128x128x2"],
+            "fp8x": ["regs", "regs128", "stream", "32x64", "64x64", "128x128", "128x256", "32x32x4", "64x64x2", "128x128x2"],
+            "bf16": ["regs", "regs128", "stream", "32x64", "64x64", "128x128", "256x128", "256x256", "32x32x4", "64x64x2",
+                     "128x128x2"],
+            "bf16 kn": ["regs", "regs128", "32x64", "64x64", "64x128", "128x128", "256x128", "256x256", "32x32x4", "64x64x2",
+                        "128x128x2"],
+            "f32": ["regs", "regs128", "stream", "32x64", "64x64", "128x128", "64x64x2"],
+            "f32 kn": ["regs", "regs128", "32x64", "64x64", "128x128", "64x64x2"]}
+
+
+@pytest.mark.parametrize("fmt,variant", [(f, v) for f in VARIANTS for v in VARIANTS[f]])
+@pytest.mark.parametrize("name,N,K", [("large", 264, 368), ("gaps", 304, 1040), ("mixed", 40, 32)])
+def test_every_variant(ox, monkeypatch, fmt, variant, name, N, K):
+    say("variant", fmt, variant, name, N, K)
+    monkeypatch.setenv("OX_FORCE_KERNEL", variant)
+    kind = {"fp8x": "fp8", "bf16 kn": "bf16", "f32 kn": "f32"}.get(fmt, fmt)
+    grouped_case(ox, kind, name, N, K, not fmt.endswith("kn"), "relu", 0, out=torch.float32 if fmt == "fp8x" else None)
+
+
+def test_forced_variants_that_do_not_apply_are_refused(ox, monkeypatch):
+    A, B = torch.zeros(4, 64, device="cuda"), torch.zeros(1, 64, 64, device="cuda")
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    monkeypatch.setenv("OX_FORCE_KERNEL", "256x256")           # fp32 has none
+    with pytest.raises(ox.OxError):
+        ox.ox_gemm_grouped(A, B, off)
+    monkeypatch.setenv("OX_FORCE_KERNEL", "stream")            # [K, N] weights are not streamed
+    with pytest.raises(ox.OxError):
+        ox.ox_gemm_grouped(A, B, off, transB=False)
+
+
+@pytest.mark.parametrize("fmt,T,E,N,K,transB", [("fp8", 700, 1, 1600, 1088, True), ("bf16", 1500, 3, 1100, 704, True),
+                                                ("bf16", 1500, 3, 1104, 704, False), ("f32", 600, 2, 520, 260, True),
+                                                ("fp8", 3000, 2, 2100, 520, True)])
+def test_larger_problems_as_chosen(ox, fmt, T, E, N, K, transB):
+    COUNTS["tmp"] = ([T // E + (7 if e == 0 else 0) for e in range(E)], 0, 3)
+    say("larger", fmt, T, E, N, K, transB)
+    grouped_case(ox, fmt, "tmp", N, K, transB, "none", 0)
