@@ -432,3 +432,57 @@ def test_larger_problems_as_chosen(ox, fmt, T, E, N, K, transB):
     COUNTS["tmp"] = ([T // E + (7 if e == 0 else 0) for e in range(E)], 0, 3)
     say("larger", fmt, T, E, N, K, transB)
     grouped_case(ox, fmt, "tmp", N, K, transB, "none", 0)
+
+
+def check_gpu(got, A, B, K, dtype):
+    """check() for one expert's rows, in 64 bits on the GPU."""
+    ref, S = A.double() @ B.double().t(), A.double().abs() @ B.double().abs().t()
+    eps = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    bad = (got.double() - ref).abs() > 1.2 * (K + 8) * 2.0 ** -23 * S + eps * ref.abs()
+    assert not bad.any().item() and not torch.isnan(got).any().item()
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_weights_past_32_bits(ox, rows):
+    # 7 x 16384 x 16384 fp32 weights: the last expert starts 6.4 GB in
+    E, N = 7, 16384
+    say("weights past 32 bits", rows)
+    B = torch.empty(E, N, N, device="cuda")
+    B[0].fill_(float("nan"))
+    B[E - 1].normal_()
+    A = torch.randn(rows, N, device="cuda")
+    off = torch.tensor([0] * E + [rows], dtype=torch.int32, device="cuda")
+    Y = ox.ox_gemm_grouped(A, B, off)
+    check_gpu(Y[:, :2048], A, B[E - 1, :2048], N, torch.float32)
+    check_gpu(Y[:, -2048:], A, B[E - 1, -2048:], N, torch.float32)
+
+
+def test_rows_past_32_bits(ox):
+    # 130000 x 16384 bf16 rows (4.3 GB) quantised, and as the left operand
+    T, K, N = 130000, 16384, 72
+    say("rows past 32 bits")
+    A = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    A[-300:].normal_()
+    B = torch.randn(1, N, K, device="cuda").bfloat16()
+    Y = ox.ox_gemm_grouped(A, B, torch.tensor([0, T], dtype=torch.int32, device="cuda"))
+    check_gpu(Y[-300:], A[-300:], B[0], K, torch.bfloat16)
+    assert (Y[:-300] == 0).all().item()
+    Q, S = ox.ox_quantize_fp8(A)
+    q, s = ox.ox_quantize_fp8(A[-300:].contiguous())
+    assert torch.equal(Q[-300:].view(torch.uint8), q.view(torch.uint8)) and torch.equal(S[:, -300:], s)
+    assert (Q[:-300].view(torch.uint8) == 0).all().item()
+
+
+@pytest.mark.parametrize("tokens,experts,width,hidden", [(5, 8, 256, 512), (200, 4, 384, 1024)])
+def test_example_layer(tokens, experts, width, hidden):
+    # two e4m3 roundings of 2^-4 relative at most (half a step) on either side of
+    # each product: independent errors of a sum average out far below the 4 * 2^-4
+    # that they could reach together
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "expert_layer.py")
+    spec = importlib.util.spec_from_file_location("expert_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    off, same = mod.main(["--tokens", str(tokens), "--experts", str(experts), "--width", str(width), "--hidden", str(hidden)])
+    assert same and off < 4 * 2.0 ** -4
