@@ -312,7 +312,8 @@ _F8 = []          # torch's types, looked up once: (float8_e4m3fn, uint8, float3
 def _types():
     if not _F8:
         torch = _torch()
-        _F8.extend((torch.float8_e4m3fn, torch.uint8, torch.float32, torch.int32, torch._C._cuda_getCurrentRawStream))
+        _F8.extend((torch.float8_e4m3fn, torch.uint8, torch.float32, torch.int32,
+                    getattr(torch._C, "_cuda_getCurrentRawStream", None)))
     return _F8
 
 

@@ -136,14 +136,15 @@ __device__ __forceinline__ void expert_rows(const ExpertArgs& a, int e, int& lo,
   hi = clampi(a.offsets[e + 1], lo, a.T);
 }
 
-// inclusive prefix sum over the wave
+// inclusive prefix sum over the wave: shifts within rows of 16 lanes, then
+// each row's last lane broadcast to the rows behind it
 __device__ __forceinline__ int wave_scan(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(v, o);
-    if (lane >= o) v += u;
-  }
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
   return v;
 }
 
@@ -204,8 +205,8 @@ __device__ __forceinline__ bool find_tile(const ExpertArgs& a, int NT, ExpertTil
   if (first != 0 || last != a.T) zero_outside(a, first, last);
   if ((int64_t)b >= (int64_t)total * NT) return false;
   tile_order(xcd_tile(b, total * NT), total, NT, t, nt);
-  int hi = r.rows, before = 0, base = 0;
-  for (;;) {
+  int hi = r.rows, before = 0;
+  for (int base = 0; base < a.E; base += 64) {
     if (a.E > 64) {
       lo = hi = 0;
       if (base + lane < a.E) expert_rows(a, base + lane, lo, hi);
@@ -219,11 +220,11 @@ __device__ __forceinline__ bool find_tile(const ExpertArgs& a, int NT, ExpertTil
       r.e = base + l;
       r.row0 = __builtin_amdgcn_readlane(lo, l) + skip * BM;
       r.rows = min(BM, __builtin_amdgcn_readlane(hi, l) - r.row0);
-      return true;
+      return r.rows > 0;
     }
     before += __builtin_amdgcn_readlane(s, 63);
-    base += 64;
   }
+  return false;      // (offsets so wrong that the count left 32 bits)
 }
 
 // The tile kernel: BM rows x BN columns per block, WM x WN waves, S stages of
@@ -628,27 +629,14 @@ struct ExpertTileKernel {
     if constexpr (F8) {
       sa = uniform_ptr(a.sa + t.row0);
       const int nb = (a.N + 127) / 128;
-      sb = a.sb + ((int64_t)t.e * nb + min((t.n0 + wn * TN) / 128, nb - 1)) * ((a.K + 127) / 128);
-      if (nk > 0) {
-        sb0 = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(sb[block_of(0)])));
-        refill_scales(0);
-      }
+      sb = uniform_ptr(a.sb + ((int64_t)t.e * nb + min((t.n0 + wn * TN) / 128, nb - 1)) * nk);
     }
   }
-  // The wave's b_scales: lane l holds that of block (kb & ~63) + l, and the
-  // first stage's is kept apart (it may be the last block's).
-  float sbl, sb0;
-  __device__ __forceinline__ void refill_scales(int kb0) {
-    sbl = sb[min(kb0 + (int)(threadIdx.x & 63), (a.K + 127) / 128 - 1)];
-    asm volatile("" : "+v"(sbl));   // waited for here, not (with the DMA behind it) at every use
-  }
-  __device__ __forceinline__ float scale_of(int k) {
-    if constexpr (F8) {
-      const int kb0 = min(block_of(k), nk - 1);
-      if (k > 0 && (kb0 & 63) == 0 && kb0 > 0) refill_scales(kb0);
-      const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sbl), kb0 & 63));
-      return k == 0 ? sb0 : v;
-    }
+  // The b_scale of stage block k, by a scalar load (a vector load would have to
+  // be waited for with the DMA behind it).
+  __device__ __forceinline__ float scale_of(int k) const {
+    typedef const __attribute__((address_space(4))) float* Scalar;
+    if constexpr (F8) return *(Scalar)(uintptr_t)(sb + min(block_of(k), nk - 1));
     return 1.0f;
   }
   __device__ __forceinline__ void start_loads(int grp) {
@@ -659,8 +647,7 @@ struct ExpertTileKernel {
     for (int x = 1; x < S; ++x) issue<false>(x * KS + grp);
   }
 
-  __device__ __forceinline__ void run() {
-    const int NT = (a.N + BN - 1) / BN;
+  __device__ __forceinline__ void run(const ExpertTile& x, int nt) {
     lda = (int64_t)a.K * ESZ;
     ldb = KN ? (int64_t)a.N * ESZ : lda;
     nk = (a.K + KE - 1) / KE;
@@ -668,9 +655,6 @@ struct ExpertTileKernel {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wave / NW;
     gwave = wave % NW;
     const int wm = gwave / WN, wn = gwave % WN;
-    ExpertTile x;
-    int nt;
-    if (!find_tile<BM>(a, NT, x, nt)) return;
     Where t;
     setup(x, nt, wn, t);
     init_frags(wm, wn);
@@ -687,15 +671,17 @@ struct ExpertTileKernel {
         wait_dma_barrier<D*(S - 1)>();
         begin(grp, wm, w);
         int k = 0;
+        float sk = scale_of(grp);
 #pragma unroll 1
         for (; k + KS < nk; k += KS) {
-          const float sk = scale_of(k + grp);
+          const float next = scale_of(k + KS + grp);
           compute<true>(k + grp, wm, sk, acc, w, [&] {
             wait_dma_barrier<D*(S - 2)>();      // the next stage is there, the S - 2 after it may be in flight
           }, [&] { issue<false>(k + S * KS + grp); });
+          sk = next;
         }
         // (a block past the last one holds zeros)
-        compute<false>(k + grp, wm, scale_of(k + grp), acc, w, nothing, nothing);
+        compute<false>(k + grp, wm, sk, acc, w, nothing, nothing);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       }
     } else {
@@ -748,8 +734,11 @@ template <int FMT, int BM, int BN, int WM, int WN, int S, int KS, bool DMA, bool
 __global__ __launch_bounds__(WM* WN* KS * 64) void expert_gemm_kernel(const ExpertArgs a) {
   typedef ExpertTileKernel<FMT, BM, BN, WM, WN, S, KS, DMA, KN> TK;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
+  ExpertTile x;
+  int nt;
+  if (!find_tile<BM>(a, (a.N + BN - 1) / BN, x, nt)) return;
   TK k(a, smem);
-  k.run();
+  k.run(x, nt);
 }
 
 // --- few rows: the weights are streamed once, straight into registers.
