@@ -41,12 +41,17 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 // of the norm of a random result.  bf16 results, rounded at 2^-9, take it.
 // FMT_FP8X widens the codes to bf16 (exact) for the bf16 instruction, whose
 // sums are fp32 throughout, at half the rate: fp32 results take it.
-// fp32 operands take the K = 4 fp32 instruction, four to a 16-byte piece.
+// fp32 operands take the K = 4 fp32 instruction, four to a 16-byte piece; each
+// block's products are summed from zero and then added to the running sum, as
+// the e4m3 blocks are (one long chain of K additions is 2-3 times further off:
+// 9e-7 of the norm at K = 4000).
 enum Fmt : int { FMT_BF16 = 0, FMT_FP8 = 1, FMT_FP8X = 2, FMT_F32 = 3 };
 
 template <int FMT>
 struct FmtOps {
   static constexpr bool F8 = FMT == FMT_FP8 || FMT == FMT_FP8X;
+  static constexpr bool BLOCKS = FMT != FMT_BF16;      // sums of blocks, added in the vector unit
+  static constexpr int PER_BLOCK = FMT == FMT_FP8 ? 1 : FMT == FMT_FP8X ? 4 : 8;   // matrix instructions (where BLOCKS)
   static constexpr int ESZ = F8 ? 1 : FMT == FMT_F32 ? 4 : 2;
   // a fragment's 128 bytes of K as the matrix instructions take them
   struct Frag { u32x4_t v[FMT == FMT_FP8X ? 4 : 2]; };
@@ -81,7 +86,7 @@ struct FmtOps {
                                                      __builtin_bit_cast(bf16x8_t, a.v[H]), c, 0, 0, 0);
     }
   }
-  // the 16 x 16 sums of one block of 128 k of e4m3
+  // the 16 x 16 sums of one block of K
   static __device__ __forceinline__ f32x4_t block(const Frag& b, const Frag& a) {
     f32x4_t p = {0.f, 0.f, 0.f, 0.f};
     if constexpr (FMT == FMT_FP8) {
@@ -91,6 +96,9 @@ struct FmtOps {
       p = half<1>(b, a, p);
       p = half<2>(b, a, p);
       p = half<3>(b, a, p);
+    } else {
+      p = half<0>(b, a, p);
+      p = half<1>(b, a, p);
     }
     return p;
   }
@@ -240,10 +248,9 @@ struct ExpertTileKernel {
   static constexpr int TM = BM / WM, TN = BN / WN, MF = TM / 16, NF = TN / 16;
   typedef FmtOps<FMT> Mm;
   typedef typename Mm::Frag Frag;
-  static constexpr bool F8 = Mm::F8;
+  static constexpr bool F8 = Mm::F8, BLOCKS = Mm::BLOCKS;
   static constexpr int ESZ = Mm::ESZ;
   static constexpr int KE = 128 / ESZ;                       // elements of K per stage
-  static constexpr int MPP = FMT == FMT_F32 ? 4 : 1;         // matrix instructions per piece
   static constexpr int KNR = FMT == FMT_F32 ? 8 : 4;         // [K, N]: LDS reads per fragment
   static constexpr int PE = 16 / ESZ;                        // elements per piece
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
@@ -462,7 +469,7 @@ struct ExpertTileKernel {
   __device__ __forceinline__ float row_scale(uint32_t st, int wm, int f) const {
     if constexpr (F8)
       return *(const OX_LDS float*)(lds_ptr(st + A_BYTES + B_BYTES + (wm * TM + (threadIdx.x & 15)) * 4) + f * 64);
-    return 0.0f;
+    return 1.0f;
   }
   __device__ __forceinline__ void read_b(uint32_t st, int j, Flow& w) const {
     u32x4_t x, y;
@@ -512,7 +519,7 @@ struct ExpertTileKernel {
         frag_a(last ? st1 : st, last ? 0 : f + 1, w.x, w.y);
         w.s = row_scale(last ? st1 : st, wm, last ? 0 : f + 1);
       }
-      if constexpr (F8) {
+      if constexpr (BLOCKS) {
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
           w.p[f & 1][j] = Mm::block(w.b[j], a);
@@ -520,10 +527,10 @@ struct ExpertTileKernel {
         }
         add_block(acc[(f + MF - 1) % MF], w.p[(f & 1) ^ 1], w.sp);
         w.sp = sbk * s1;
-        __builtin_amdgcn_sched_group_barrier(0x100, load ? 3 : 0, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, !load ? 0 : F8 ? 3 : 2, 0);
         static_for<NF>([&](auto) {
-          __builtin_amdgcn_sched_group_barrier(0x008, FMT == FMT_FP8X ? 4 : 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, last && NEXT ? 2 : 0, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, Mm::PER_BLOCK, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, last && NEXT ? (KN ? KNR : 2) : 0, 0);
           __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
         });
       } else {
@@ -535,9 +542,9 @@ struct ExpertTileKernel {
           if constexpr (last && NEXT) read_b(st1, j, w);
         }
         __builtin_amdgcn_sched_group_barrier(0x100, load ? 2 : 0, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, NF * MPP, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, NF, 0);
         static_for<NF>([&](auto) {
-          __builtin_amdgcn_sched_group_barrier(0x008, MPP, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
           __builtin_amdgcn_sched_group_barrier(0x100, last && NEXT ? (KN ? KNR : 2) : 0, 0);
         });
       }
@@ -697,7 +704,7 @@ struct ExpertTileKernel {
         compute<false>(k, wm, sk, acc, w, nothing, nothing);
       }
     }
-    if constexpr (F8)
+    if constexpr (BLOCKS)
       if (nk > 0) add_block(acc[MF - 1], w.p[1], w.sp);
     if constexpr (KS > 1) {
       // the groups' sums, through the stages' memory: this lane's results side
@@ -815,9 +822,9 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
           const bool in = k + u < k1;
           const Frag b = Mm::widen(wx[u], wy[u]);
           const Frag x = Mm::widen(in && o <= last_piece ? ax[u] : zero, in && o + 64 <= last_piece ? ay[u] : zero);
-          if constexpr (F8) {
+          if constexpr (Mm::BLOCKS) {
             const f32x4_t p = Mm::block(b, x);
-            const float s = sa[u] * sw[u];
+            const float s = F8 ? sa[u] * sw[u] : 1.0f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(s, p[r], acc[r]);
           } else {
