@@ -41,17 +41,16 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 // of the norm of a random result.  bf16 results, rounded at 2^-9, take it.
 // FMT_FP8X widens the codes to bf16 (exact) for the bf16 instruction, whose
 // sums are fp32 throughout, at half the rate: fp32 results take it.
-// fp32 operands take the K = 4 fp32 instruction, four to a 16-byte piece; each
-// block's products are summed from zero and then added to the running sum, as
-// the e4m3 blocks are (one long chain of K additions is 2-3 times further off:
-// 9e-7 of the norm at K = 4000).
+// fp32 operands take the K = 4 fp32 instruction, four to a 16-byte piece; every
+// eight blocks (256 k) the chain of sums is added to a second set and starts
+// from zero again (one chain over K = 2800 is 9e-7 of the norm off, this 3e-7
+// for any K; adding every block costs 10% of the time, as the fp32 instruction
+// leaves the vector unit no room beside it).
 enum Fmt : int { FMT_BF16 = 0, FMT_FP8 = 1, FMT_FP8X = 2, FMT_F32 = 3 };
 
 template <int FMT>
 struct FmtOps {
   static constexpr bool F8 = FMT == FMT_FP8 || FMT == FMT_FP8X;
-  static constexpr bool BLOCKS = FMT != FMT_BF16;      // sums of blocks, added in the vector unit
-  static constexpr int PER_BLOCK = FMT == FMT_FP8 ? 1 : FMT == FMT_FP8X ? 4 : 8;   // matrix instructions (where BLOCKS)
   static constexpr int ESZ = F8 ? 1 : FMT == FMT_F32 ? 4 : 2;
   // a fragment's 128 bytes of K as the matrix instructions take them
   struct Frag { u32x4_t v[FMT == FMT_FP8X ? 4 : 2]; };
@@ -86,7 +85,7 @@ struct FmtOps {
                                                      __builtin_bit_cast(bf16x8_t, a.v[H]), c, 0, 0, 0);
     }
   }
-  // the 16 x 16 sums of one block of K
+  // the 16 x 16 sums of one block of 128 k of e4m3
   static __device__ __forceinline__ f32x4_t block(const Frag& b, const Frag& a) {
     f32x4_t p = {0.f, 0.f, 0.f, 0.f};
     if constexpr (FMT == FMT_FP8) {
@@ -96,9 +95,6 @@ struct FmtOps {
       p = half<1>(b, a, p);
       p = half<2>(b, a, p);
       p = half<3>(b, a, p);
-    } else {
-      p = half<0>(b, a, p);
-      p = half<1>(b, a, p);
     }
     return p;
   }
@@ -248,9 +244,10 @@ struct ExpertTileKernel {
   static constexpr int TM = BM / WM, TN = BN / WN, MF = TM / 16, NF = TN / 16;
   typedef FmtOps<FMT> Mm;
   typedef typename Mm::Frag Frag;
-  static constexpr bool F8 = Mm::F8, BLOCKS = Mm::BLOCKS;
+  static constexpr bool F8 = Mm::F8;
   static constexpr int ESZ = Mm::ESZ;
   static constexpr int KE = 128 / ESZ;                       // elements of K per stage
+  static constexpr int MPP = FMT == FMT_F32 ? 4 : 1;         // matrix instructions per piece
   static constexpr int KNR = FMT == FMT_F32 ? 8 : 4;         // [K, N]: LDS reads per fragment
   static constexpr int PE = 16 / ESZ;                        // elements per piece
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
@@ -469,7 +466,7 @@ struct ExpertTileKernel {
   __device__ __forceinline__ float row_scale(uint32_t st, int wm, int f) const {
     if constexpr (F8)
       return *(const OX_LDS float*)(lds_ptr(st + A_BYTES + B_BYTES + (wm * TM + (threadIdx.x & 15)) * 4) + f * 64);
-    return 1.0f;
+    return 0.0f;
   }
   __device__ __forceinline__ void read_b(uint32_t st, int j, Flow& w) const {
     u32x4_t x, y;
@@ -519,7 +516,7 @@ struct ExpertTileKernel {
         frag_a(last ? st1 : st, last ? 0 : f + 1, w.x, w.y);
         w.s = row_scale(last ? st1 : st, wm, last ? 0 : f + 1);
       }
-      if constexpr (BLOCKS) {
+      if constexpr (F8) {
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
           w.p[f & 1][j] = Mm::block(w.b[j], a);
@@ -527,10 +524,10 @@ struct ExpertTileKernel {
         }
         add_block(acc[(f + MF - 1) % MF], w.p[(f & 1) ^ 1], w.sp);
         w.sp = sbk * s1;
-        __builtin_amdgcn_sched_group_barrier(0x100, !load ? 0 : F8 ? 3 : 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, load ? 3 : 0, 0);
         static_for<NF>([&](auto) {
-          __builtin_amdgcn_sched_group_barrier(0x008, Mm::PER_BLOCK, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, last && NEXT ? (KN ? KNR : 2) : 0, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, FMT == FMT_FP8X ? 4 : 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, last && NEXT ? 2 : 0, 0);
           __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
         });
       } else {
@@ -542,9 +539,9 @@ struct ExpertTileKernel {
           if constexpr (last && NEXT) read_b(st1, j, w);
         }
         __builtin_amdgcn_sched_group_barrier(0x100, load ? 2 : 0, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, NF, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, NF * MPP, 0);
         static_for<NF>([&](auto) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, MPP, 0);
           __builtin_amdgcn_sched_group_barrier(0x100, last && NEXT ? (KN ? KNR : 2) : 0, 0);
         });
       }
@@ -671,6 +668,28 @@ struct ExpertTileKernel {
     for (int f = 0; f < MF; ++f)
 #pragma unroll
       for (int j = 0; j < NF; ++j) acc[f][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    constexpr bool F32 = FMT == FMT_F32;
+    f32x4_t sum[F32 ? MF : 1][F32 ? NF : 1];
+    auto flush = [&](int stage) {
+      if constexpr (F32) {
+        if ((stage & 7) != 7) return;
+#pragma unroll
+        for (int f = 0; f < MF; ++f)
+#pragma unroll
+          for (int j = 0; j < NF; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              sum[f][j][r] += acc[f][j][r];
+              acc[f][j][r] = 0.0f;
+            }
+      }
+    };
+    if constexpr (F32) {
+#pragma unroll
+      for (int f = 0; f < MF; ++f)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) sum[f][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
     Flow w;
     if constexpr (DMA) {
       if (nk > 0) {
@@ -686,6 +705,7 @@ struct ExpertTileKernel {
             wait_dma_barrier<D*(S - 2)>();      // the next stage is there, the S - 2 after it may be in flight
           }, [&] { issue<false>(k + S * KS + grp); });
           sk = next;
+          flush(k / KS);
         }
         // (a block past the last one holds zeros)
         compute<false>(k + grp, wm, sk, acc, w, nothing, nothing);
@@ -702,10 +722,18 @@ struct ExpertTileKernel {
         else reload(k, wm, w);
         if (k + 1 < nk) load_regs(k + 1, g);
         compute<false>(k, wm, sk, acc, w, nothing, nothing);
+        flush(k);
       }
     }
-    if constexpr (BLOCKS)
+    if constexpr (F8)
       if (nk > 0) add_block(acc[MF - 1], w.p[1], w.sp);
+    flush(7);
+    if constexpr (F32) {
+#pragma unroll
+      for (int f = 0; f < MF; ++f)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) acc[f][j] = sum[f][j];
+    }
     if constexpr (KS > 1) {
       // the groups' sums, through the stages' memory: this lane's results side
       // by side, 16 bytes apart from the next lane's
@@ -816,21 +844,26 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
         }
         __builtin_amdgcn_sched_barrier(0);      // every load goes out before the first product
         const u32x4_t zero = {0u, 0u, 0u, 0u};
+        f32x4_t chain = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int o = (k + u) * 128 + g * 16;
           const bool in = k + u < k1;
           const Frag b = Mm::widen(wx[u], wy[u]);
           const Frag x = Mm::widen(in && o <= last_piece ? ax[u] : zero, in && o + 64 <= last_piece ? ay[u] : zero);
-          if constexpr (Mm::BLOCKS) {
+          if constexpr (F8) {
             const f32x4_t p = Mm::block(b, x);
-            const float s = F8 ? sa[u] * sw[u] : 1.0f;
+            const float s = sa[u] * sw[u];
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(s, p[r], acc[r]);
           } else {
-            acc = Mm::template half<0>(b, x, acc);
-            acc = Mm::template half<1>(b, x, acc);
+            chain = Mm::template half<0>(b, x, chain);
+            chain = Mm::template half<1>(b, x, chain);
           }
+        }
+        if constexpr (!F8) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[r] += chain[r];
         }
       }
     }
