@@ -383,7 +383,7 @@ ox_status ox_dynamic_quantize_linear(int64_t n, const float* X, uint8_t* Y, floa
  * bits, largest value 448, no infinity) with one fp32 scale per block of 128
  * along K:
  *   m = max(|x| over the block's finite values, 2^-100)
- *   scale = m / 448,  Q = e4m3(x * (448 / m)), round half to even,
+ *   scale = m / 448,  Q = e4m3(448 * x / m), round half to even,
  * so that X is about Q * scale.  A NaN gives a NaN code, an infinity the
  * code of +-448 (ONNX QuantizeLinear with saturation); neither moves the
  * scale.

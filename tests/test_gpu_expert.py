@@ -47,11 +47,10 @@ def round_e4m3(v):
 
 
 def quantize_plain(X, block_rows):
-    """(values of the codes, scales [row blocks, k-blocks]) in 64 bits; the
-    scale is 448 / m rounded to fp32 as the definition says."""
+    """(values of the codes, scales [row blocks, k-blocks], 448 x / m) in 64 bits"""
     R, K = X.shape
     rb, kb = -(-R // block_rows), blocks(K)
-    Q, S = np.zeros((R, K)), np.zeros((rb, kb))
+    Q, S, V = np.zeros((R, K)), np.zeros((rb, kb)), np.zeros((R, K))
     for i in range(rb):
         for j in range(kb):
             at = (slice(i * block_rows, min(R, (i + 1) * block_rows)), slice(j * 128, min(K, (j + 1) * 128)))
@@ -59,12 +58,21 @@ def quantize_plain(X, block_rows):
             fin = np.isfinite(x)
             m = max(np.abs(x[fin]).max(initial=0.0), 2.0 ** -100)
             S[i, j] = np.float32(m) / np.float32(448)
-            with np.errstate(invalid="ignore"):
-                v = (x.astype(np.float32) * (np.float32(448) / np.float32(m))).astype(np.float64)
-            q = round_e4m3(np.where(fin, v, 0.0))
+            V[at] = np.where(fin, x, 0.0) * 448.0 / m
+            q = round_e4m3(V[at])
             q = np.where(np.isinf(x), np.copysign(448.0, np.where(np.isnan(x), 0, x)), q)
             Q[at] = np.where(np.isnan(x), np.nan, q)
-    return Q, S
+    return Q, S, V
+
+
+def check_codes(got, Q, V, dtype):
+    """bf16: every code.  fp32: the quotient, taken in fp32, may be off by
+    2^-23 of itself, which moves a code only if a halfway point is that near."""
+    got = got.float().cpu().numpy().astype(np.float64)
+    if dtype == torch.float32:
+        near = round_e4m3(V * (1 + 2.0 ** -23)) != round_e4m3(V * (1 - 2.0 ** -23))
+        got = np.where(near & (np.abs(got - Q) <= np.abs(Q) / 7 + 2.0 ** -9), Q, got)
+    np.testing.assert_array_equal(got, Q)
 
 
 def act64(v, act):
@@ -157,9 +165,9 @@ def test_quantize(ox, rows, K, br, shift, dtype):
     ox.ox_quantize_fp8(shifted(X, shift), block_rows=br, Q=Q, scales=S)
     torch.cuda.synchronize()
     okq(), oks()
-    q, s = quantize_plain(X.double().numpy(), br)
+    q, s, v = quantize_plain(X.double().numpy(), br)
     np.testing.assert_array_equal(S.cpu().numpy(), (s.T if br == 1 else s).astype(np.float32))
-    np.testing.assert_array_equal(Q.float().cpu().numpy(), q)
+    check_codes(Q, q, v, dtype)
 
 
 @pytest.mark.parametrize("br", [1, 128])
@@ -178,9 +186,9 @@ def test_quantize_zeros_infinities_nans_and_tiny(ox, dtype, br):
         X[3] = 1.0
     X = torch.from_numpy(X).to(dtype)
     Q, S = ox.ox_quantize_fp8(X.cuda(), block_rows=br)
-    q, s = quantize_plain(X.double().numpy(), br)
+    q, s, v = quantize_plain(X.double().numpy(), br)
     np.testing.assert_array_equal(S.cpu().numpy(), (s.T if br == 1 else s).astype(np.float32))
-    np.testing.assert_array_equal(Q.float().cpu().numpy(), q)
+    check_codes(Q, q, v, dtype)
     assert np.isfinite(S.cpu().numpy()).all() and (S > 0).all().item()
 
 
@@ -193,6 +201,21 @@ def test_quantize_rounds_ties_to_even(ox):
     np.testing.assert_array_equal(Q.float().cpu().numpy(), round_e4m3(X.numpy()))
 
 
+def test_quantize_bf16_halfway_points(ox):
+    # every bf16 significand under every one as the block's maximum: the halfway
+    # points among their quotients go to even
+    sig = torch.arange(128, 256, dtype=torch.float32)
+    X = torch.cat([sig.repeat(128, 1) * 2.0 ** -7, sig.repeat(128, 1) * 2.0 ** -12], dim=1)
+    X[:, 0] = sig / 32
+    X[:, 128] = sig / 32
+    X = X.bfloat16()
+    Q, S = ox.ox_quantize_fp8(X.cuda())
+    q, s, v = quantize_plain(X.double().numpy(), 1)
+    step = np.exp2(np.maximum(np.floor(np.log2(np.abs(v))), -6.0) - 3.0)
+    assert (np.abs(v / step - np.floor(v / step) - 0.5) == 0).sum() > 100
+    check_codes(Q, q, v, torch.bfloat16)
+
+
 @pytest.mark.parametrize("K", [256, 200, 1024])
 def test_quantize_gathers_rows(ox, K):
     rng = np.random.default_rng(7)
@@ -201,9 +224,9 @@ def test_quantize_gathers_rows(ox, K):
     Q, S = ox.ox_quantize_fp8(X.cuda(), index=torch.from_numpy(idx.astype(np.int32)).cuda())
     inside = (idx >= 0) & (idx < 11)
     rows = np.where(inside[:, None], X.double().numpy()[np.where(inside, idx, 0)], 0.0)
-    q, s = quantize_plain(rows, 1)
+    q, s, v = quantize_plain(rows, 1)
     np.testing.assert_array_equal(S.cpu().numpy(), s.T.astype(np.float32))
-    np.testing.assert_array_equal(Q.float().cpu().numpy(), q)
+    check_codes(Q, q, v, torch.bfloat16)
 
 
 # ---------------------------------------------------------------- products --
