@@ -10,7 +10,7 @@
 // it is representable, halfway points among them.  Sixteen lanes share a row's block, eight elements
 // each; the maximum crosses them with four DPP steps.  What bounds it is the
 // bytes: each element is read once and its code written once (16384 gathered
-// rows of 4096 bf16, 201 MB: 36 us, 5.5 TB/s; 24 rows: 2.5 us, one trip to HBM).
+// rows of 4096 bf16, 201 MB: 37 us, 5.4 TB/s; 24 rows: 2.5 us, one trip to HBM).
 #include "engine.hpp"
 
 namespace ox {
@@ -52,32 +52,33 @@ __device__ __forceinline__ void load8(const QuantF8Args& a, int row, int k, floa
   }
 }
 
-// Largest magnitude; fmaxf passes over a NaN.  FINITE: infinities are passed over too.
+// Largest magnitude, as the bits of a float: magnitudes order as their bits
+// do, with infinities and NaN above every number.  FINITE: those are passed
+// over.
+constexpr uint32_t kInfBits = 0x7f800000u;
 template <bool FINITE>
-__device__ __forceinline__ float amax8(const float (&x)[8]) {
-  float m = 0.0f;
+__device__ __forceinline__ uint32_t amax8(const float (&x)[8]) {
+  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float v = fabsf(x[i]);
-    m = fmaxf(m, FINITE && v == __builtin_inff() ? 0.0f : v);
+    const uint32_t v = __float_as_uint(x[i]) & 0x7fffffffu;
+    m = max(m, FINITE && v >= kInfBits ? 0u : v);
   }
   return m;
 }
 
 // the maximum over the sixteen lanes of a row's block
-__device__ __forceinline__ float max16(float m) {
+__device__ __forceinline__ uint32_t max16(uint32_t m) {
   // lane ^ 1, ^ 2 within quads, then the mirrored half row and row (every
   // lane of a quad, of a half row, already agrees)
-  auto step = [&](auto ctrl) {
-    const int o = __builtin_amdgcn_mov_dpp(__float_as_int(m), decltype(ctrl)::value, 0xf, 0xf, true);
-    m = fmaxf(m, __int_as_float(o));
-  };
-  step(std::integral_constant<int, 0xB1>{});    // quad_perm 1,0,3,2
-  step(std::integral_constant<int, 0x4E>{});    // quad_perm 2,3,0,1
-  step(std::integral_constant<int, 0x141>{});   // row_half_mirror
-  step(std::integral_constant<int, 0x140>{});   // row_mirror
-  return m;
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xf, 0xf, true));    // quad_perm 1,0,3,2
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xf, 0xf, true));    // quad_perm 2,3,0,1
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xf, 0xf, true));   // row_half_mirror
+  return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xf, 0xf, true));   // row_mirror
 }
+
+// m of a block from the bits of its largest finite magnitude
+__device__ __forceinline__ float block_max(uint32_t bits) { return fmaxf(__uint_as_float(bits), kTiny); }
 
 // Eight codes.  v = x * r is off by the rounding of r = 448 / m; the remainder
 // 448 x - v m, taken 2^-9 times (0.875 x and m / 512 are exact and stay in
@@ -129,7 +130,7 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const QuantF8Args 
 #pragma unroll
   for (int i = 0; i < RW; ++i) {
     const int r = min(r0 + i, a.R - 1);
-    src[i] = a.index ? a.index[r] : r;
+    src[i] = __builtin_amdgcn_readfirstlane(a.index ? a.index[r] : r);
   }
   float x[RW][8];
 #pragma unroll
@@ -137,19 +138,22 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const QuantF8Args 
     // (an index outside X reads row 0 and is then zeroed; X may have no row)
     const bool in = src[i] >= 0 && src[i] < a.rows;
     if (a.rows > 0) load8<F32, VEC>(a, in ? src[i] : 0, k, x[i]);
+    if (!in) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[i][j] = in ? x[i][j] : 0.0f;
+      for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
+    }
   }
   float sc[RW];
 #pragma unroll
   for (int i = 0; i < RW; ++i) {
-    float m = max16(amax8<false>(x[i]));
+    const uint32_t bits = max16(amax8<false>(x[i]));
+    float m;
     u32x2_t q;
-    if (m == __builtin_inff()) {                               // (all sixteen lanes agree)
-      m = fmaxf(max16(amax8<true>(x[i])), kTiny);
+    if (bits >= kInfBits) {                                    // (all sixteen lanes agree)
+      m = block_max(max16(amax8<true>(x[i])));
       q = codes8<true>(x[i], m);
     } else {
-      m = fmaxf(m, kTiny);
+      m = block_max(bits);
       q = codes8<false>(x[i], m);
     }
     sc[i] = m / kMax;
@@ -170,7 +174,7 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const QuantF8Args 
 // A scale per 128 x 128: one block of threads each, its values in registers.
 template <bool F32, bool VEC>
 __global__ __launch_bounds__(kThreads) void quant_tiles_kernel(const QuantF8Args a) {
-  __shared__ float part[2][kThreads / 64];
+  __shared__ uint32_t part[2][kThreads / 64];
   const int kb = (a.K + 127) / 128;
   const int rb = blockIdx.x / kb, b = blockIdx.x - rb * kb;
   const int k = b * 128 + (threadIdx.x & 15) * 8, r0 = rb * 128 + (threadIdx.x >> 4);
@@ -184,20 +188,20 @@ __global__ __launch_bounds__(kThreads) void quant_tiles_kernel(const QuantF8Args
       for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
     }
   }
-  float m = 0.0f;
+  uint32_t bits = 0;
   for (int pass = 0; pass < 2; ++pass) {
-    m = 0.0f;
+    bits = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, pass ? amax8<true>(x[i]) : amax8<false>(x[i]));
-    m = max16(m);
-    m = fmaxf(m, __shfl_xor(m, 16));
-    m = fmaxf(m, __shfl_xor(m, 32));
-    if ((threadIdx.x & 63) == 0) part[pass][threadIdx.x >> 6] = m;
+    for (int i = 0; i < 8; ++i) bits = max(bits, pass ? amax8<true>(x[i]) : amax8<false>(x[i]));
+    bits = max16(bits);
+    bits = max(bits, (uint32_t)__shfl_xor((int)bits, 16));
+    bits = max(bits, (uint32_t)__shfl_xor((int)bits, 32));
+    if ((threadIdx.x & 63) == 0) part[pass][threadIdx.x >> 6] = bits;
     __syncthreads();
-    m = fmaxf(fmaxf(part[pass][0], part[pass][1]), fmaxf(part[pass][2], part[pass][3]));
-    if (m != __builtin_inff()) break;
+    bits = max(max(part[pass][0], part[pass][1]), max(part[pass][2], part[pass][3]));
+    if (bits < kInfBits) break;
   }
-  m = fmaxf(m, kTiny);
+  const float m = block_max(bits);
   if (threadIdx.x == 0) a.scales[(int64_t)rb * kb + b] = m / kMax;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
