@@ -406,9 +406,12 @@ ox_status ox_quantize_fp8(ox_dtype t, int64_t rows, int64_t K, const void* X, in
  *                       * sum_{k in block b} A[m,k] * B[n,k]  + bias[n] )
  * A: DEVICE e4m3 [M, K], a_scales DEVICE fp32 [ceil(K/128)][M];
  * B: DEVICE e4m3 [N, K], b_scales DEVICE fp32 [ceil(N/128)][ceil(K/128)]
- * (both as ox_quantize_fp8 writes them).  Products and sums in fp32, one
- * rounding to y_type (OX_F32 or OX_BF16), the type of Y DEVICE [M, N] and of
- * bias DEVICE [N] (or NULL).  NaN codes give NaN results.  With few rows the
+ * (both as ox_quantize_fp8 writes them).  Block sums are scaled and added in
+ * fp32 and rounded once to y_type (OX_F32 or OX_BF16), the type of Y DEVICE
+ * [M, N].  Inside a block, OX_F32 results are summed in fp32 as well; OX_BF16
+ * results take the e4m3 matrix instruction, which adds neighbouring products
+ * with about 15 bits below the largest (within 2^-15 of sum |a b| scaled).
+ * bias: DEVICE [N] of y_type, or NULL.  NaN codes give NaN results.  With few rows the
  * weights are streamed once and K is divided over the waves of a block; the
  * order of every sum depends on the sizes alone. */
 ox_status ox_gemm_fp8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const uint8_t* A,
