@@ -411,7 +411,8 @@ ox_status ox_quantize_fp8(ox_dtype t, int64_t rows, int64_t K, const void* X, in
  * [M, N].  Inside a block, OX_F32 results are summed in fp32 as well; OX_BF16
  * results take the e4m3 matrix instruction, which adds neighbouring products
  * with about 15 bits below the largest (within 2^-15 of sum |a b| scaled).
- * bias: DEVICE [N] of y_type, or NULL.  NaN codes give NaN results.  With few rows the
+ * bias: DEVICE [N] of y_type, or NULL.  NaN codes give NaN sums (which ReLU
+ * and ReLU6 take to 0, as everywhere in this library).  With few rows the
  * weights are streamed once and K is divided over the waves of a block; the
  * order of every sum depends on the sizes alone. */
 ox_status ox_gemm_fp8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const uint8_t* A,
