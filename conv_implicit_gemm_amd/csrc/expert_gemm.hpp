@@ -27,6 +27,7 @@
 
 #include <string.h>
 
+#include "expert_tiles.hpp"
 #include "lds_dma.hpp"
 
 namespace ox {
@@ -152,10 +153,6 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-struct ExpertTile {
-  int e, row0, rows;   // expert, first row of the tile, rows in it (<= BM)
-};
-
 // Zeros in rows [0, first) and [last, T), spread over the grid's blocks.
 __device__ __forceinline__ void zero_outside(const ExpertArgs& a, int first, int last) {
   const int64_t head = (int64_t)first * a.N, tail = (int64_t)max(first, last) * a.N, all = (int64_t)a.T * a.N;
@@ -166,18 +163,10 @@ __device__ __forceinline__ void zero_outside(const ExpertArgs& a, int first, int
   }
 }
 
-// The block's place in `total` row tiles x NT column tiles: each XCD runs one
-// contiguous range of an order that takes bands of four row tiles and walks
-// the columns inside a band, so the blocks that run together on an XCD share
-// both operands' tiles through its L2.
-__device__ __forceinline__ void tile_order(int u, int total, int NT, int& t, int& nt) {
-  const int band = u / (4 * NT), in = u - band * 4 * NT;
-  const int h = min(4, total - band * 4);
-  nt = in / h;
-  t = band * 4 + in - nt * h;
-}
-
-// This block's tile, from the offsets; false when the offsets have fewer.
+// This block's tile, from the offsets; false when the offsets have fewer (and
+// for all blocks when decreasing offsets make more than the grid was sized
+// for).  Each XCD runs one contiguous range of tile_order(), so the blocks that
+// run together on an XCD share both operands' tiles through its L2.
 // Also writes its share of the zeros outside the experts' rows.  Up to 64
 // experts are one load and one scan across the wave (a second round for each
 // 64 more); every wave does it for itself, without a barrier.
@@ -194,7 +183,8 @@ __device__ __forceinline__ bool find_tile(const ExpertArgs& a, int NT, ExpertTil
     return true;
   }
   const int lane = threadIdx.x & 63;
-  int lo, n, s, total = 0, first = 0, last = 0;
+  int lo, n, s, first = 0, last = 0;
+  int64_t total = 0;
   for (int base = 0; base < a.E; base += 64) {
     int hi = 0;
     lo = 0;
@@ -207,9 +197,10 @@ __device__ __forceinline__ bool find_tile(const ExpertArgs& a, int NT, ExpertTil
     r.rows = hi;
   }
   if (first != 0 || last != a.T) zero_outside(a, first, last);
-  if ((int64_t)b >= (int64_t)total * NT) return false;
-  tile_order(xcd_tile(b, total * NT), total, NT, t, nt);
-  int hi = r.rows, before = 0;
+  if (!block_has_tile(b, total, NT, expert_tile_bound(a.T, a.E, BM))) return false;
+  tile_order(xcd_tile(b, (int)total * NT), (int)total, NT, t, nt);
+  int hi = r.rows;
+  int64_t before = 0;
   for (int base = 0; base < a.E; base += 64) {
     if (a.E > 64) {
       lo = hi = 0;
@@ -220,15 +211,13 @@ __device__ __forceinline__ bool find_tile(const ExpertArgs& a, int NT, ExpertTil
     const uint64_t past = __ballot(before + s > t);
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
-      const int skip = t - before - __builtin_amdgcn_readlane(s - n, l);   // tiles of this expert before this one
+      const int64_t skip = t - before - __builtin_amdgcn_readlane(s - n, l);   // tiles of this expert before this one
       r.e = base + l;
-      r.row0 = __builtin_amdgcn_readlane(lo, l) + skip * BM;
-      r.rows = min(BM, __builtin_amdgcn_readlane(hi, l) - r.row0);
-      return r.rows > 0;
+      return expert_tile_rows(__builtin_amdgcn_readlane(lo, l), __builtin_amdgcn_readlane(hi, l), skip, BM, r);
     }
     before += __builtin_amdgcn_readlane(s, 63);
   }
-  return false;      // (offsets so wrong that the count left 32 bits)
+  return false;
 }
 
 // The tile kernel: BM rows x BN columns per block, WM x WN waves, S stages of
@@ -1051,16 +1040,11 @@ inline double weights_time(const ExpertArgs& a, int esz) {
   return experts * a.N * a.K * esz / 5e6;
 }
 
-// The most row tiles that any offsets can give.
-inline int64_t expert_tile_bound(const ExpertArgs& a, int BM) {
-  if (!a.offsets) return ((int64_t)a.T + BM - 1) / BM;
-  return (int64_t)a.T / BM + (a.E < a.T ? a.E : a.T);
-}
-
 template <int FMT, int BM, int BN, int WM, int WN, int S, int KS, bool DMA, bool KN>
 int launch_expert_tile(const ExpertArgs& a, hipStream_t s) {
   typedef ExpertTileKernel<FMT, BM, BN, WM, WN, S, KS, DMA, KN> TK;
-  int64_t blocks = expert_tile_bound(a, BM) * ((a.N + BN - 1) / BN);
+  const int64_t tall = a.offsets ? expert_tile_bound(a.T, a.E, BM) : ((int64_t)a.T + BM - 1) / BM;
+  const int64_t blocks = tall * ((a.N + BN - 1) / BN);
   if (blocks >= ((int64_t)1 << 31)) return (int)hipErrorInvalidValue;
   hipLaunchKernelGGL((expert_gemm_kernel<FMT, BM, BN, WM, WN, S, KS, DMA, KN>), dim3((uint32_t)blocks), dim3(TK::TH),
                      TK::LDS_BYTES, s, a);
