@@ -20,12 +20,16 @@ namespace {
 constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100: below it 448 / m would leave fp32
 constexpr float kMax = 448.0f;
 
+// Columns and rows of a last block run past K and R, which end below 2^31: they
+// are counted in 32 bits without a sign.
+
 // Eight elements of a row from column k (zeros from column K on).
 template <bool F32, bool VEC>
-__device__ __forceinline__ void load8(const QuantF8Args& a, int row, int k, float (&x)[8]) {
-  const int64_t at = (int64_t)row * a.K + k;
+__device__ __forceinline__ void load8(const QuantF8Args& a, int64_t row, uint32_t k, float (&x)[8]) {
+  const int64_t at = row * a.K + k;
+  const uint32_t K = (uint32_t)a.K;
   if constexpr (VEC) {
-    if (k >= a.K) {
+    if (k >= K) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = 0.0f;
     } else if constexpr (F32) {
@@ -47,7 +51,7 @@ __device__ __forceinline__ void load8(const QuantF8Args& a, int row, int k, floa
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       x[i] = 0.0f;
-      if (k + i < a.K) x[i] = F32 ? ((const float*)a.X)[at + i] : bf16_to_f32(((const uint16_t*)a.X)[at + i]);
+      if (k + i < K) x[i] = F32 ? ((const float*)a.X)[at + i] : bf16_to_f32(((const uint16_t*)a.X)[at + i]);
     }
   }
 }
@@ -104,14 +108,15 @@ __device__ __forceinline__ u32x2_t codes8(const float (&x)[8], float m) {
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store8(const QuantF8Args& a, int r, int k, u32x2_t q) {
-  uint8_t* y = a.Q + (int64_t)r * a.K + k;
+__device__ __forceinline__ void store8(const QuantF8Args& a, int64_t r, uint32_t k, u32x2_t q) {
+  uint8_t* y = a.Q + r * a.K + k;
+  const uint32_t K = (uint32_t)a.K;
   if constexpr (VEC) {
-    if (k < a.K) *(u32x2_t*)y = q;
+    if (k < K) *(u32x2_t*)y = q;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (k + i < a.K) y[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+      if (k + i < K) y[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
   }
 }
 
@@ -122,14 +127,15 @@ template <bool F32, bool VEC, int RW>
 __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const QuantF8Args a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int per = (a.K + 511) / 512;
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + wave;
-  const int r0 = (int)(unit / per) * RW, k = (int)(unit % per) * 512 + lane * 8;
-  if (r0 >= a.R) return;
+  const uint32_t K = (uint32_t)a.K, per = (K + 511) / 512;
+  const uint32_t unit = blockIdx.x * (kThreads / 64) + wave, row = unit / per;
+  const uint32_t k = unit % per * 512 + lane * 8;
+  if ((int64_t)row * RW >= a.R) return;
+  const int r0 = (int)row * RW, rows = min(RW, a.R - r0);
   int src[RW];
 #pragma unroll
   for (int i = 0; i < RW; ++i) {
-    const int r = min(r0 + i, a.R - 1);
+    const int r = r0 + min(i, rows - 1);
     src[i] = __builtin_amdgcn_readfirstlane(a.index ? a.index[r] : r);
   }
   float x[RW][8];
@@ -157,16 +163,16 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const QuantF8Args 
       q = codes8<false>(x[i], m);
     }
     sc[i] = m / kMax;
-    if (k < a.K && r0 + i < a.R) store8<VEC>(a, r0 + i, k, q);
+    if (k < K && i < rows) store8<VEC>(a, r0 + i, k, q);
   }
-  if (k < a.K && (lane & 15) == 0) {
+  if (k < K && (lane & 15) == 0) {
     float* s = a.scales + (int64_t)(k >> 7) * a.R + r0;
     if (RW == 4 && a.R % 4 == 0 && (uintptr_t)a.scales % 16 == 0) {
       *(f32x4_t*)s = f32x4_t{sc[0], sc[1 % RW], sc[2 % RW], sc[3 % RW]};
     } else {
 #pragma unroll
       for (int i = 0; i < RW; ++i)
-        if (r0 + i < a.R) s[i] = sc[i];
+        if (i < rows) s[i] = sc[i];
     }
   }
 }
@@ -175,13 +181,13 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const QuantF8Args 
 template <bool F32, bool VEC>
 __global__ __launch_bounds__(kThreads) void quant_tiles_kernel(const QuantF8Args a) {
   __shared__ uint32_t part[2][kThreads / 64];
-  const int kb = (a.K + 127) / 128;
-  const int rb = blockIdx.x / kb, b = blockIdx.x - rb * kb;
-  const int k = b * 128 + (threadIdx.x & 15) * 8, r0 = rb * 128 + (threadIdx.x >> 4);
+  const uint32_t R = (uint32_t)a.R, kb = ((uint32_t)a.K + 127) / 128;
+  const uint32_t rb = blockIdx.x / kb, b = blockIdx.x - rb * kb;
+  const uint32_t k = b * 128 + (threadIdx.x & 15) * 8, r0 = rb * 128 + (threadIdx.x >> 4);
   float x[8][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (r0 + 16 * i < a.R) {
+    if (r0 + 16 * i < R) {
       load8<F32, VEC>(a, r0 + 16 * i, k, x[i]);
     } else {
 #pragma unroll
@@ -205,20 +211,20 @@ __global__ __launch_bounds__(kThreads) void quant_tiles_kernel(const QuantF8Args
   if (threadIdx.x == 0) a.scales[(int64_t)rb * kb + b] = m / kMax;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (r0 + 16 * i < a.R) store8<VEC>(a, r0 + 16 * i, k, codes8<true>(x[i], m));
+    if (r0 + 16 * i < R) store8<VEC>(a, r0 + 16 * i, k, codes8<true>(x[i], m));
 }
 
 template <bool F32, bool VEC>
 int launch(const QuantF8Args& a, hipStream_t s) {
   if (a.block_rows == 1) {
     // four rows a wave once that still gives every CU 16 waves
-    const int64_t per = (a.K + 511) / 512;
-    const int rw = (int64_t)a.R * per >= 4 * 256 * 16 ? 4 : 1;
-    const int64_t blocks = ((a.R + rw - 1) / rw * per + kThreads / 64 - 1) / (kThreads / 64);
+    const int64_t R = a.R, per = ((int64_t)a.K + 511) / 512;
+    const int rw = R * per >= 4 * 256 * 16 ? 4 : 1;
+    const int64_t blocks = ((R + rw - 1) / rw * per + kThreads / 64 - 1) / (kThreads / 64);
     if (rw == 4) hipLaunchKernelGGL((quant_rows_kernel<F32, VEC, 4>), dim3((uint32_t)blocks), dim3(kThreads), 0, s, a);
     else hipLaunchKernelGGL((quant_rows_kernel<F32, VEC, 1>), dim3((uint32_t)blocks), dim3(kThreads), 0, s, a);
   } else {
-    const int64_t blocks = (int64_t)((a.R + 127) / 128) * ((a.K + 127) / 128);
+    const int64_t blocks = ((int64_t)a.R + 127) / 128 * (((int64_t)a.K + 127) / 128);
     hipLaunchKernelGGL((quant_tiles_kernel<F32, VEC>), dim3((uint32_t)blocks), dim3(kThreads), 0, s, a);
   }
   return (int)hipGetLastError();

@@ -34,3 +34,19 @@ def test_offsets_whose_tiles_leave_32_bits(ox):
     ox.ox_gemm_grouped(A, B, off, Y=whole[2048:2048 + T * N].view(T, N))
     torch.cuda.synchronize()
     assert (whole[:2048] == 77).all().item() and (whole[-2048:] == 77).all().item()
+
+
+@pytest.mark.parametrize("K", [2 ** 31 - 1, 2 ** 31 - 16, 2 ** 31 - 500])
+def test_quantize_a_row_next_to_the_limit(ox, K):
+    # 128-wide blocks whose last one ends on, or a little before, 2^31 elements
+    say("quantise one row of", K)
+    tail = 640 + K % 128
+    X = torch.zeros(1, K, dtype=torch.bfloat16, device="cuda")
+    X[0, -tail:].normal_()
+    whole = torch.full((K + 4096,), 77, dtype=torch.uint8, device="cuda")
+    Q, S = ox.ox_quantize_fp8(X, Q=whole[2048:2048 + K].view(1, K))
+    q, s = ox.ox_quantize_fp8(X[:, -tail:].contiguous())
+    torch.cuda.synchronize()
+    assert (whole[:2048] == 77).all().item() and (whole[-2048:] == 77).all().item()
+    assert torch.equal(Q[:, -tail:], q.view(torch.uint8)) and torch.equal(S[-s.shape[0]:], s)
+    assert not Q[:, :-tail].any().item()
