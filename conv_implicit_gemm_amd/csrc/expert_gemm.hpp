@@ -175,7 +175,7 @@ __device__ __forceinline__ bool find_tile(const ExpertArgs& a, int NT, ExpertTil
   const int b = blockIdx.x;
   int t;
   if (!a.offsets) {
-    const int total = (a.T + BM - 1) / BM;
+    const int total = ceil_div(a.T, BM);
     tile_order(xcd_tile(b, total * NT), total, NT, t, nt);
     r.e = 0;
     r.row0 = t * BM;
@@ -191,7 +191,7 @@ __device__ __forceinline__ bool find_tile(const ExpertArgs& a, int NT, ExpertTil
     if (base + lane < a.E) expert_rows(a, base + lane, lo, hi);
     if (base == 0) first = __builtin_amdgcn_readlane(lo, 0);
     last = max(last, __builtin_amdgcn_readlane(hi, min(63, a.E - 1 - base)));
-    n = (hi - lo + BM - 1) / BM;
+    n = ceil_div(hi - lo, BM);
     s = wave_scan(n);
     total += __builtin_amdgcn_readlane(s, 63);
     r.rows = hi;
@@ -205,7 +205,7 @@ __device__ __forceinline__ bool find_tile(const ExpertArgs& a, int NT, ExpertTil
     if (a.E > 64) {
       lo = hi = 0;
       if (base + lane < a.E) expert_rows(a, base + lane, lo, hi);
-      n = (hi - lo + BM - 1) / BM;
+      n = ceil_div(hi - lo, BM);
       s = wave_scan(n);
     }
     const uint64_t past = __ballot(before + s > t);
@@ -372,7 +372,7 @@ struct ExpertTileKernel {
   __device__ __forceinline__ void load_regs(int k, Regs& g) {
     const int64_t left = (int64_t)a.K * ESZ - (int64_t)k * 128;
     if constexpr (F8) g.s = (int)threadIdx.x < rows ? sa[(int64_t)k * a.T + threadIdx.x] : 0.0f;
-    if (KN ? left >= 128 && (k + 1) * KE <= a.K && cols == BN : left >= 128) {
+    if (KN ? left >= 128 && k < a.K / KE && cols == BN : left >= 128) {
 #pragma unroll
       for (int i = 0; i < CA; ++i) {
         const int q = threadIdx.x + i * TH, r = q >> 3, c = (q & 7) ^ sw_a(r);
@@ -650,8 +650,8 @@ struct ExpertTileKernel {
     Bb = uniform_ptr((const char*)a.B + (int64_t)t.e * a.N * a.K * ESZ + (KN ? (int64_t)t.n0 * ESZ : (int64_t)t.n0 * ldb));
     if constexpr (F8) {
       sa = uniform_ptr(a.sa + t.row0);
-      const int nb = (a.N + 127) / 128;
-      sb = uniform_ptr(a.sb + ((int64_t)t.e * nb + min((t.n0 + wn * TN) / 128, nb - 1)) * nk);
+      const int nb = ceil_div(a.N, 128);
+      sb = uniform_ptr(a.sb + ((int64_t)t.e * nb + min((int)(((uint32_t)t.n0 + wn * TN) / 128), nb - 1)) * nk);
     }
   }
   // The b_scale of stage block k, by a scalar load (a vector load would have to
@@ -672,7 +672,7 @@ struct ExpertTileKernel {
   __device__ __forceinline__ void run(const ExpertTile& x, int nt) {
     lda = (int64_t)a.K * ESZ;
     ldb = KN ? (int64_t)a.N * ESZ : lda;
-    nk = (a.K + KE - 1) / KE;
+    nk = ceil_div(a.K, KE);
     part = (a.K * (int64_t)ESZ) % 128 != 0;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wave / NW;
     gwave = wave % NW;
@@ -800,7 +800,7 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void expert_gemm_kernel(const Expe
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   ExpertTile x;
   int nt;
-  if (!find_tile<BM>(a, (a.N + BN - 1) / BN, x, nt)) return;
+  if (!find_tile<BM>(a, ceil_div(a.N, BN), x, nt)) return;
   TK k(a, smem);
   k.run(x, nt);
 }
@@ -827,7 +827,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
   __shared__ float part[kStreamWaves][4][64];
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int CT = kStreamWaves / SPL, NT = (a.N + 16 * CT - 1) / (16 * CT);
+  const int CT = kStreamWaves / SPL, NT = ceil_div(a.N, 16 * CT);
   const int e = blockIdx.x / NT, nt = blockIdx.x - e * NT;
   int lo, hi;
   expert_rows(a, e, lo, hi);
@@ -842,10 +842,10 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
   const int n0 = (nt * CT + ct) * 16;
   const bool live = n0 < a.N;               // whole waves; the barrier below is passed by all
   const int64_t ld = (int64_t)a.K * ESZ;
-  const int nk = (a.K + KE - 1) / KE, per = (nk + SPL - 1) / SPL;
+  const int nk = ceil_div(a.K, KE), per = ceil_div(nk, SPL);
   const int k0 = sl * per, k1 = min(nk, k0 + per);
   const char* W = (const char*)a.B + ((int64_t)e * a.N + min(n0 + i, a.N - 1)) * ld;
-  const float* sb = F8 ? a.sb + ((int64_t)e * ((a.N + 127) / 128) + min(n0, a.N - 1) / 128) * nk : nullptr;
+  const float* sb = F8 ? a.sb + ((int64_t)e * ceil_div(a.N, 128) + min(n0, a.N - 1) / 128) * nk : nullptr;
   const int last_piece = (int)ld - 16;
 
   for (int row0 = lo; row0 < hi; row0 += 16) {
@@ -946,11 +946,11 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
 template <int FMT>
 int launch_expert_stream(const ExpertArgs& a, hipStream_t s) {
   // slices of at least kStreamDepth blocks of K, so that a wave has as many in flight
-  const int nk = (a.K + 128 / FmtOps<FMT>::ESZ - 1) / (128 / FmtOps<FMT>::ESZ);
+  const int nk = ceil_div(a.K, 128 / FmtOps<FMT>::ESZ);
   int spl = 1;
   while (spl < kStreamWaves && nk > spl * kStreamDepth) spl *= 2;
   const int ct = kStreamWaves / spl;
-  const int64_t blocks = (int64_t)a.E * ((a.N + 16 * ct - 1) / (16 * ct));
+  const int64_t blocks = (int64_t)a.E * ceil_div(a.N, 16 * ct);
   if (blocks >= ((int64_t)1 << 31)) return (int)hipErrorInvalidValue;
   hipLaunchKernelGGL((expert_stream_kernel<FMT>), dim3((uint32_t)blocks), dim3(kStreamWaves * 64), 0, s, a, spl);
   return (int)hipGetLastError();
@@ -972,9 +972,9 @@ constexpr int kCus = 256;
 // average: an expert's last tile is taken to be half full.
 inline double tile_time(const ExpertArgs& a, int esz, const TileCost& t) {
   const double experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1, rows = a.T / experts;
-  double tall = (a.T + t.bm - 1) / t.bm;
+  double tall = ceil_div(a.T, t.bm);
   if (experts > 1) tall = experts * (rows / t.bm + 0.5 > 1 ? rows / t.bm + 0.5 : 1);
-  const double tiles = tall * ((a.N + t.bn - 1) / t.bn), nk = ((int64_t)a.K * esz + 127) / 128;
+  const double tiles = tall * ceil_div(a.N, t.bn), nk = ((int64_t)a.K * esz + 127) / 128;
   const double slots = (double)kCus * t.per;
   const double full = (double)(int64_t)(tiles / slots), rest = tiles - full * slots;
   double time = full * (t.o + t.c * nk);
@@ -998,7 +998,7 @@ inline int best_tile(const ExpertArgs& a, int esz, const TileCost (&t)[N]) {
 // 14.4 us streamed, 12.0 on tiles).
 inline bool stream_pays(const ExpertArgs& a, int esz) {
   const int64_t experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1;
-  return a.T <= 16 * experts && experts * ((a.N + 63) / 64) < kCus && (int64_t)a.K * esz >= 1024;
+  return a.T <= 16 * experts && experts * ceil_div(a.N, 64) < kCus && (int64_t)a.K * esz >= 1024;
 }
 
 // The named variant's place in the table, or -1.
@@ -1015,7 +1015,7 @@ enum Pick : int { PICK_REGS = -2, PICK_REGS_LARGE = -3, PICK_STREAM = -4, PICK_N
 inline int pick_regs(const ExpertArgs& a) {
   const int64_t experts = a.offsets ? (a.E < a.T ? a.E : a.T) : 1;
   const int64_t tall = a.T / 128 > experts ? a.T / 128 : experts;
-  return tall * ((a.N + 127) / 128) >= 2 * kCus && a.T >= 128 * experts ? PICK_REGS_LARGE : PICK_REGS;
+  return tall * ceil_div(a.N, 128) >= 2 * kCus && a.T >= 128 * experts ? PICK_REGS_LARGE : PICK_REGS;
 }
 template <int N>
 inline int pick_variant(ExpertArgs& a, int esz, const TileCost (&t)[N]) {
@@ -1043,8 +1043,8 @@ inline double weights_time(const ExpertArgs& a, int esz) {
 template <int FMT, int BM, int BN, int WM, int WN, int S, int KS, bool DMA, bool KN>
 int launch_expert_tile(const ExpertArgs& a, hipStream_t s) {
   typedef ExpertTileKernel<FMT, BM, BN, WM, WN, S, KS, DMA, KN> TK;
-  const int64_t tall = a.offsets ? expert_tile_bound(a.T, a.E, BM) : ((int64_t)a.T + BM - 1) / BM;
-  const int64_t blocks = tall * ((a.N + BN - 1) / BN);
+  const int64_t tall = a.offsets ? expert_tile_bound(a.T, a.E, BM) : ceil_div(a.T, BM);
+  const int64_t blocks = tall * ceil_div(a.N, BN);
   if (blocks >= ((int64_t)1 << 31)) return (int)hipErrorInvalidValue;
   hipLaunchKernelGGL((expert_gemm_kernel<FMT, BM, BN, WM, WN, S, KS, DMA, KN>), dim3((uint32_t)blocks), dim3(TK::TH),
                      TK::LDS_BYTES, s, a);

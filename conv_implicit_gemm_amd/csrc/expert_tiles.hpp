@@ -10,6 +10,9 @@
 
 namespace ox {
 
+// n / d rounded up, for 0 <= n < 2^31 and a small d: the sum needs the 32nd bit.
+constexpr int ceil_div(int n, int d) { return (int)(((uint32_t)n + (uint32_t)d - 1) / (uint32_t)d); }
+
 struct ExpertTile {
   int e, row0, rows;   // expert, first row of the tile, rows in it (<= BM)
 };

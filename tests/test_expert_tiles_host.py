@@ -28,7 +28,7 @@ static void scan(const int* off, int E, int T, int BM, int base, Round& r) {
       r.lo[l] = clampi(off[base + l], 0, T);
       r.hi[l] = clampi(off[base + l + 1], r.lo[l], T);
     }
-    r.n[l] = (int)(((unsigned)(r.hi[l] - r.lo[l]) + BM - 1) / BM);
+    r.n[l] = ceil_div(r.hi[l] - r.lo[l], BM);
     r.s[l] = (int)(sum += (unsigned)r.n[l]);
   }
 }
@@ -42,6 +42,8 @@ extern "C" long long tile_count(const int* off, int E, int T, int BM) {
   }
   return total;
 }
+
+extern "C" int up(int n, int d) { return ceil_div(n, d); }
 
 extern "C" long long bound(int T, int E, int BM) { return expert_tile_bound(T, E, BM); }
 
@@ -141,3 +143,11 @@ def test_wild_offsets_give_no_tile_outside(tiles, E, T, BM, NT, seed):
     blocks = min(tiles.bound(T, E, BM) * NT, 2 ** 31 - 1)
     for tile in search(tiles, off, T, BM, NT, np.linspace(0, blocks - 1, 300).astype(int)):
         inside(off, T, BM, NT, tile)
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 127, 128, 256, 512])
+def test_blocks_of_sizes_next_to_the_limit(tiles, d):
+    # K, N and T go up to 2^31 - 1 elements; one block too few or a negative
+    # count leaves sums out
+    for n in [0, 1, d - 1, d, d + 1] + [2 ** 31 - i for i in range(1, 2 * d)]:
+        assert tiles.up(n, d) == -(-n // d), (n, d)
