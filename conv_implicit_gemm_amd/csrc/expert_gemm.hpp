@@ -857,8 +857,8 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
       for (int k = k0; k < k1; k += U) {
         u32x4_t wx[U], wy[U], ax[U], ay[U];
         float sa[U], sw[U];
-        // a block past the slice is read again from its last one, with zero
-        // tokens; so is a piece past K
+        // a block past the slice is read again from its last one, a piece past K
+        // from the row's last one
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int kk = min(k + u, k1 - 1), o = kk * 128 + g * 16;
@@ -879,8 +879,11 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
         for (int u = 0; u < U; ++u) {
           const int o = (k + u) * 128 + g * 16;
           const bool in = k + u < k1;
-          const Frag b = Mm::widen(wx[u], wy[u]);
-          const Frag x = Mm::widen(in && o <= last_piece ? ax[u] : zero, in && o + 64 <= last_piece ? ay[u] : zero);
+          // what was read again counts as zeros on both sides: an infinity on
+          // either would make 0 * inf
+          const bool px = in && o <= last_piece, py = in && o + 64 <= last_piece;
+          const Frag b = Mm::widen(px ? wx[u] : zero, py ? wy[u] : zero);
+          const Frag x = Mm::widen(px ? ax[u] : zero, py ? ay[u] : zero);
           if constexpr (F8) {
             const f32x4_t p = Mm::block(b, x);
             const float s = sa[u] * sw[u];

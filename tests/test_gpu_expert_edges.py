@@ -50,3 +50,55 @@ def test_quantize_a_row_next_to_the_limit(ox, K):
     assert (whole[:2048] == 77).all().item() and (whole[-2048:] == 77).all().item()
     assert torch.equal(Q[:, -tail:], q.view(torch.uint8)) and torch.equal(S[-s.shape[0]:], s)
     assert not Q[:, :-tail].any().item()
+
+
+def products64(A, B, off):
+    """A [T, K], B [E, N, K] float64; (Y, sum of magnitudes), infinities and all"""
+    Y, S = np.zeros((A.shape[0], B.shape[1])), np.zeros((A.shape[0], B.shape[1]))
+    with np.errstate(invalid="ignore"):
+        for e in range(B.shape[0]):
+            rows = slice(off[e], off[e + 1])
+            # term by term: a library's product may pad, and 0 * inf is NaN
+            Y[rows] = (A[rows][:, None, :] * B[e][None]).sum(axis=2)
+            S[rows] = np.abs(A[rows][:, None, :] * B[e][None]).sum(axis=2)
+    return Y, S
+
+
+def check_infinities(got, Y, S, K, dtype):
+    """The same infinities and NaN; the finite results within the rounding of K
+    additions in fp32 (2^-23 of the sum of magnitudes each) and of the result."""
+    got = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(Y))
+    inf = np.isinf(Y)
+    assert np.array_equal(np.isinf(got), inf) and np.array_equal(got[inf], Y[inf])
+    fin = np.isfinite(Y)
+    eps = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    assert (np.abs(got[fin] - Y[fin]) <= 1.2 * (K + 8) * 2.0 ** -23 * S[fin] + eps * np.abs(Y[fin])).all()
+
+
+@pytest.mark.parametrize("variant", ["", "stream", "32x64", "64x64x2", "regs"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+# blocks of 128 bytes of K that do not divide into slices of four, and rows that
+# end inside a block
+@pytest.mark.parametrize("blocks,tail", [(24, 0), (9, 0), (17, 16), (33, 112), (3, 48)])
+def test_infinite_operands(ox, monkeypatch, variant, dtype, blocks, tail):
+    say("infinities", variant, dtype, blocks, tail)
+    if variant:
+        monkeypatch.setenv("OX_FORCE_KERNEL", variant)
+    size = 2 if dtype == torch.bfloat16 else 4
+    K, N, off = (blocks * 128 + tail) // size, 48, [0, 1, 1, 4]
+    rng = np.random.default_rng([11, blocks, tail])
+    A = torch.from_numpy(rng.standard_normal((4, K))).to(dtype)
+    B = torch.from_numpy(rng.standard_normal((3, N, K))).to(dtype)
+    for i, k in enumerate([0, 1, K // 2, K - 1, K - 2, K - 16 // size, K - 128 // size, K - 256 // size, K - 512 // size]):
+        B[:, 2 * i, k] = np.inf * (-1) ** i
+    A[2, K - 1] = np.inf
+    Y, S = products64(A.double().numpy(), B.double().numpy(), off)
+    assert np.isinf(Y).sum() > 30
+    dev = [A.cuda(), B.cuda(), torch.tensor(off, dtype=torch.int32, device="cuda")]
+    check_infinities(ox.ox_gemm_grouped(*dev), Y, S, K, dtype)
+    if variant != "stream":                                    # weights stored [K, N] are not streamed
+        Bt = dev[1].transpose(1, 2).contiguous()
+        check_infinities(ox.ox_gemm_grouped(dev[0], Bt, dev[2], transB=False), Y, S, K, dtype)
+    got = ox.ox_gemm_grouped(*dev, act="relu").double().cpu().numpy()
+    assert (got[Y == np.inf] == np.inf).all() and (got[Y == -np.inf] == 0).all()
