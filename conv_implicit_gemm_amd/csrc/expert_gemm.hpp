@@ -655,10 +655,14 @@ struct ExpertTileKernel {
     }
   }
   // The b_scale of stage block k, by a scalar load (a vector load would have to
-  // be waited for with the DMA behind it).
+  // be waited for with the DMA behind it).  A group's block past the last one
+  // has none: its products are zeros, and an infinite scale would make NaN of them.
   __device__ __forceinline__ float scale_of(int k) const {
     typedef const __attribute__((address_space(4))) float* Scalar;
-    if constexpr (F8) return *(Scalar)(uintptr_t)(sb + min(block_of(k), nk - 1));
+    if constexpr (F8) {
+      const float v = *(Scalar)(uintptr_t)(sb + min(block_of(k), nk - 1));
+      return KS == 1 || k < nk ? v : 0.0f;
+    }
     return 1.0f;
   }
   __device__ __forceinline__ void start_loads(int grp) {
@@ -886,7 +890,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
           const Frag x = Mm::widen(px ? ax[u] : zero, py ? ay[u] : zero);
           if constexpr (F8) {
             const f32x4_t p = Mm::block(b, x);
-            const float s = sa[u] * sw[u];
+            const float s = in ? sa[u] * sw[u] : 0.0f;      // (0 * inf again)
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(s, p[r], acc[r]);
           } else {

@@ -102,3 +102,31 @@ def test_infinite_operands(ox, monkeypatch, variant, dtype, blocks, tail):
         check_infinities(ox.ox_gemm_grouped(dev[0], Bt, dev[2], transB=False), Y, S, K, dtype)
     got = ox.ox_gemm_grouped(*dev, act="relu").double().cpu().numpy()
     assert (got[Y == np.inf] == np.inf).all() and (got[Y == -np.inf] == 0).all()
+
+
+@pytest.mark.parametrize("variant", ["", "stream", "32x32x4", "64x64x2", "128x128x2", "64x64", "regs"])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [1152, 1024, 2064, 4224, 368])
+def test_infinite_scales(ox, monkeypatch, variant, out, K):
+    say("infinite scales", variant, out, K)
+    if variant:
+        monkeypatch.setenv("OX_FORCE_KERNEL", variant)
+    M, N, kb = 3, 256, -(-K // 128)
+    rng = np.random.default_rng([12, K])
+    # positive codes: every block's sum is above zero
+    qa, qb = (torch.from_numpy(rng.uniform(0.5, 2.0, (n, K))).float().to(F8) for n in (M, N))
+    sa, sb = rng.uniform(0.5, 2.0, (M, kb)).astype(np.float32), rng.uniform(0.5, 2.0, (2, kb)).astype(np.float32)
+    sa[1, kb - 1] = np.inf
+    sb[1, kb - 1] = -np.inf
+    Y = ox.ox_gemm_fp8(qa.cuda(), torch.from_numpy(sa.T.copy()).cuda(), qb.cuda(), torch.from_numpy(sb).cuda(), out_dtype=out)
+    want = np.zeros((M, N))
+    for b in range(kb):
+        cols = slice(b * 128, min(K, (b + 1) * 128))
+        want += (sa[:, None, b].astype(np.float64) * np.repeat(sb[:, b], 128)[None]
+                 * (qa[:, cols].double().numpy() @ qb[:, cols].double().numpy().T))
+    got = Y.double().cpu().numpy()
+    assert np.isinf(want).sum() == 2 * 128 + 256
+    assert not np.isnan(got).any() and np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+    fin = np.isfinite(want)                 # every product is positive: the sum is the sum of magnitudes
+    tol = 1.2 * ((K + 8) * 2.0 ** -23 + (2.0 ** -15 + 2.0 ** -8 if out == torch.bfloat16 else 2.0 ** -24))
+    assert (np.abs(got[fin] - want[fin]) <= tol * want[fin]).all()
