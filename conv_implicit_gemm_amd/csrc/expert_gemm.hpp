@@ -884,9 +884,10 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
           const int o = (k + u) * 128 + g * 16;
           const bool in = k + u < k1;
           // what was read again counts as zeros on both sides: an infinity on
-          // either would make 0 * inf
+          // either would make 0 * inf (e4m3 codes have none, and a NaN among
+          // the weights has made its column's sum NaN already)
           const bool px = in && o <= last_piece, py = in && o + 64 <= last_piece;
-          const Frag b = Mm::widen(px ? wx[u] : zero, py ? wy[u] : zero);
+          const Frag b = Mm::widen(F8 || px ? wx[u] : zero, F8 || py ? wy[u] : zero);
           const Frag x = Mm::widen(px ? ax[u] : zero, py ? ay[u] : zero);
           if constexpr (F8) {
             const f32x4_t p = Mm::block(b, x);
