@@ -119,16 +119,19 @@ def _torch():
     return torch
 
 
-_DTYPE_CODES = {}
+# Tables of torch's types, made at the first call.  Threads may make theirs at
+# the same time: each is finished before one assignment publishes it.
+_DTYPE_CODES = None
 
 
 def _dtype_code(t):
-    if not _DTYPE_CODES:
+    global _DTYPE_CODES
+    if _DTYPE_CODES is None:
         torch = _torch()
         # uint8 tensors travel as bytes through the int8 calls: the parameter
         # block (ox_int8_prepare(..., x_unsigned / y_unsigned)) says how to read them
-        _DTYPE_CODES.update({torch.float32: OX_F32, torch.bfloat16: OX_BF16, torch.int8: OX_I8,
-                             torch.uint8: OX_I8, torch.int32: OX_I32})
+        _DTYPE_CODES = {torch.float32: OX_F32, torch.bfloat16: OX_BF16, torch.int8: OX_I8,
+                        torch.uint8: OX_I8, torch.int32: OX_I32}
     code = _DTYPE_CODES.get(t.dtype)
     if code is None:
         raise TypeError("unsupported tensor dtype %s" % t.dtype)
@@ -306,14 +309,16 @@ def ox_matmul_nbits(A, B, scales, K, zero_points=None, bias=None, Y=None, stream
 # words for a refusal only made when there is one, and the stream is asked for
 # as a raw handle (0.1 us; a current_stream() object takes 2.8 us).
 
-_F8 = []          # torch's types, looked up once: (float8_e4m3fn, uint8, float32, int32, raw stream function)
+_F8 = None        # torch's types, looked up once: (float8_e4m3fn, uint8, float32, int32, raw stream function)
 
 
 def _types():
-    if not _F8:
+    global _F8
+    if _F8 is None:
         torch = _torch()
-        _F8.extend((torch.float8_e4m3fn, torch.uint8, torch.float32, torch.int32,
-                    getattr(torch._C, "_cuda_getCurrentRawStream", None)))
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _F8 = (torch.float8_e4m3fn, torch.uint8, torch.float32, torch.int32,
+               raw or (lambda device: _stream(None)))
     return _F8
 
 
