@@ -6,8 +6,11 @@
 //
 // bf16 values fall on the halfway points of e4m3 often, and a product with a
 // rounded 448 / m would send them either way: the quotient is corrected by its
-// remainder (three more operations an element), which makes it exact wherever
-// it is representable, halfway points among them.  Sixteen lanes share a row's block, eight elements
+// remainder (three more operations an element).  An fp32 quotient goes to the
+// side of a halfway point that the exact one lies on, or to even where that is
+// the point itself; the few elements near enough to need it are found by a
+// second product (8192 rows of 4096 fp32, 168 MB: 34 us, as without; 24 rows 2.6
+// us, 2.5 without).  Sixteen lanes share a row's block, eight elements
 // each; the maximum crosses them with four DPP steps.  What bounds it is the
 // bytes: each element is read once and its code written once (16384 gathered
 // rows of 4096 bf16, 201 MB: 37 us, 5.4 TB/s; 24 rows: 2.5 us, one trip to HBM).
@@ -84,27 +87,70 @@ __device__ __forceinline__ uint32_t max16(uint32_t m) {
 // m of a block from the bits of its largest finite magnitude
 __device__ __forceinline__ float block_max(uint32_t bits) { return fmaxf(__uint_as_float(bits), kTiny); }
 
-// Eight codes.  v = x * r is off by the rounding of r = 448 / m; the remainder
-// 448 x - v m, taken 2^-9 times (0.875 x and m / 512 are exact and stay in
-// range), over m / 512 is what it lacks.  INF: an infinite x gives +-448
-// (asked for only where the block holds one; finite quotients cannot leave the
-// format, |448 x / m| <= 448 but for roundings that the conversion takes back).
-template <bool INF>
-__device__ __forceinline__ u32x2_t codes8(const float (&x)[8], float m) {
-  const float r = kMax / m, m9 = m * 0.001953125f, r9 = r * 1.142857143f;
-  float v[8];
+__device__ __forceinline__ uint32_t convert4(float a, float b, float c, float d) {
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false), true);
+}
+
+// The codes of N elements, of the exact quotients 448 x / m.  v = x * r is off by the
+// rounding of r = 448 / m; the remainder 448 x - v m, taken 2^-9 times (m / 512
+// is exact and stays in range), over m / 512 is what it lacks, and the corrected
+// v is the quotient rounded to fp32.  For bf16 0.875 x is exact too, and a
+// quotient that is no halfway point h is too far from one to be rounded to it
+// (448 x and h m, of 16 bits, differ by a unit at least).  For fp32 (7/8 of 24
+// bits) the error of 0.875 x, exact in turn, is carried along, and a quotient
+// can be nearer to h than fp32 tells: where v may be a halfway point (5 bits, 19
+// zeros behind them) and its remainder is not zero, v moves one step the
+// remainder's way.  INF: an infinite x gives +-448 (asked for only where the
+// block holds one; finite quotients cannot leave the format, |448 x / m| <= 448
+// but for roundings that the conversion takes back).
+template <bool F32, bool INF, int N>
+__device__ __forceinline__ void exact_codes(const float* x, float m, float r, uint32_t* q) {
+  const float m9 = m * 0.001953125f, r9 = r * 1.142857143f;
+  float v[N];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v0 = x[i] * r;
-    v[i] = __builtin_fmaf(__builtin_fmaf(-v0, m9, x[i] * 0.875f), r9, v0);
+  for (int i = 0; i < N; ++i) {
+    const float v0 = x[i] * r, p = x[i] * 0.875f;
+    if constexpr (F32) {
+      const float e = __builtin_fmaf(x[i], 0.875f, -p);
+      v[i] = __builtin_fmaf(__builtin_fmaf(-v0, m9, p) + e, r9, v0);
+      const uint32_t u = __float_as_uint(v[i]);
+      const float d = __builtin_fmaf(-v[i], m9, p) + e;
+      const uint32_t to = ((__float_as_uint(d) ^ u) >> 31) ? u - 1 : u + 1;
+      if ((u & 0x7ffffu) == 0 && d != 0.0f && (u << 1) != 0) v[i] = __uint_as_float(to);
+    } else {
+      v[i] = __builtin_fmaf(__builtin_fmaf(-v0, m9, p), r9, v0);
+    }
     if (INF && __builtin_isinf(x[i])) v[i] = __builtin_copysignf(kMax, x[i]);
   }
-  int lo = 0, hi = 0;
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], hi, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
-  return u32x2_t{(uint32_t)lo, (uint32_t)hi};
+#pragma unroll
+  for (int i = 0; i < N; i += 4) q[i / 4] = convert4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+
+// Eight codes.  fp32: x * r is within 2^-22 of the quotient, and numbers that far below and
+// above it have the same code but for one in 2^17 or so: only it and its
+// neighbours take the exact form.
+template <bool F32, bool INF>
+__device__ __forceinline__ u32x2_t codes8(const float (&x)[8], float m) {
+  const float r = kMax / m;
+  uint32_t q[2];
+  if constexpr (F32 && !INF) {
+    const float below = r * (1.0f - 0x1p-22f), above = r * (1.0f + 0x1p-22f);
+    float lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo[i] = x[i] * below;
+      hi[i] = x[i] * above;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      q[h] = convert4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
+      if (q[h] != convert4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]))
+        exact_codes<F32, INF, 4>(x + 4 * h, m, r, q + h);
+    }
+  } else {
+    exact_codes<F32, INF, 8>(x, m, r, q);
+  }
+  return u32x2_t{q[0], q[1]};
 }
 
 template <bool VEC>
@@ -157,10 +203,10 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const QuantF8Args 
     u32x2_t q;
     if (bits >= kInfBits) {                                    // (all sixteen lanes agree)
       m = block_max(max16(amax8<true>(x[i])));
-      q = codes8<true>(x[i], m);
+      q = codes8<F32, true>(x[i], m);
     } else {
       m = block_max(bits);
-      q = codes8<false>(x[i], m);
+      q = codes8<F32, false>(x[i], m);
     }
     sc[i] = m / kMax;
     if (k < K && i < rows) store8<VEC>(a, r0 + i, k, q);
@@ -195,7 +241,8 @@ __global__ __launch_bounds__(kThreads) void quant_tiles_kernel(const QuantF8Args
     }
   }
   uint32_t bits = 0;
-  for (int pass = 0; pass < 2; ++pass) {
+  int pass = 0;
+  for (; pass < 2; ++pass) {
     bits = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) bits = max(bits, pass ? amax8<true>(x[i]) : amax8<false>(x[i]));
@@ -209,9 +256,11 @@ __global__ __launch_bounds__(kThreads) void quant_tiles_kernel(const QuantF8Args
   }
   const float m = block_max(bits);
   if (threadIdx.x == 0) a.scales[(int64_t)rb * kb + b] = m / kMax;
+  const bool infinite = !F32 || pass > 0;      // (bf16 takes one form for all: infinities cost it two operations)
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (r0 + 16 * i < R) store8<VEC>(a, r0 + 16 * i, k, codes8<true>(x[i], m));
+    if (r0 + 16 * i < R)
+      store8<VEC>(a, r0 + 16 * i, k, infinite ? codes8<F32, true>(x[i], m) : codes8<F32, false>(x[i], m));
 }
 
 template <bool F32, bool VEC>

@@ -130,3 +130,49 @@ def test_infinite_scales(ox, monkeypatch, variant, out, K):
     fin = np.isfinite(want)                 # every product is positive: the sum is the sum of magnitudes
     tol = 1.2 * ((K + 8) * 2.0 ** -23 + (2.0 ** -15 + 2.0 ** -8 if out == torch.bfloat16 else 2.0 ** -24))
     assert (np.abs(got[fin] - want[fin]) <= tol * want[fin]).all()
+
+
+def e4m3_of(x, m):
+    """The e4m3 value of 448 x / m, of exact rationals, half to even."""
+    from fractions import Fraction
+    q = Fraction(448) * Fraction(float(x)) / Fraction(float(m))
+    a, e = abs(q), -6
+    while a >= Fraction(2) ** (e + 1):
+        e += 1
+    step = Fraction(2) ** (e - 3)
+    return float(round(q / step) * step)            # Fraction rounds half to even
+
+
+def halfway_block(rng, exact, n):
+    """fp32 [n], led by its maximum m: the others make 448 x / m a halfway point
+    of e4m3 exactly, or are the fp32 number nearest to that or next to it,
+    nearer to the halfway point than an fp32 quotient can tell."""
+    m = 7 * 8 * int(rng.integers(2 ** 17, 2 ** 18)) if exact else int(rng.integers(2 ** 23, 2 ** 24))
+    scale = np.float32(2.0 ** int(rng.integers(-60, 60)))
+    half = 2 * rng.integers(0, 16, n) + 1                                  # odd: in halves of a step
+    e = np.where(half < 16, -10, rng.integers(-10, 4, n))                  # (below 2^-6 the step is 2^-9)
+    x = (half * 2.0 ** e * m / 448.0).astype(np.float32)
+    if not exact:
+        x = np.nextafter(x, np.where(rng.random(n) < 0.3, 0, np.where(rng.random(n) < 0.5, x, 1e30)).astype(np.float32))
+    x *= rng.choice([-1, 1], n).astype(np.float32)
+    x[0] = m
+    return x * scale
+
+
+@pytest.mark.parametrize("br", [1, 128])
+@pytest.mark.parametrize("exact", [True, False])
+@pytest.mark.parametrize("inf", [False, True])
+def test_quantize_fp32_halfway_points(ox, br, exact, inf):
+    say("fp32 halfway points", br, exact, inf)
+    rng = np.random.default_rng([13, br, exact, inf])
+    if br == 1:
+        X = np.stack([halfway_block(rng, exact, 128) for _ in range(128)])
+    else:
+        X = halfway_block(rng, exact, 128 * 128).reshape(128, 128)
+    m = np.abs(X).max(axis=1) if br == 1 else np.full(128, np.abs(X).max())
+    want = np.array([[e4m3_of(x, m[r]) for x in X[r]] for r in range(128)])
+    if inf:
+        X[:, 127] = np.inf
+        want[:, 127] = 448.0
+    Q, S = ox.ox_quantize_fp8(torch.from_numpy(X).cuda(), block_rows=br)
+    np.testing.assert_array_equal(Q.float().cpu().numpy().astype(np.float64), want)
