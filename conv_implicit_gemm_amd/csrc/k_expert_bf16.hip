@@ -21,10 +21,11 @@ int launch(ExpertArgs& a, hipStream_t s) {
   // [K, N] weights that take longer to read than to multiply: blocks as wide
   // as 256 bytes of their rows (64 experts of 2048 x 1024, 4003 rows: 60 us,
   // 70 us on 64 x 64 and 68 us on 256 x 256)
-  if (KN && (a.force ? !strcmp(a.force, "64x128") && a.vec : p >= 0 && tile_time(a, 2, kTiles[p]) < weights_time(a, 2))) {
-    a.chosen = "64x128";
-    return launch_expert_tile<FMT_BF16, 64, 128, 2, 4, 3, 1, true, KN>(a, s);
-  }
+  if constexpr (KN)
+    if (a.force ? !strcmp(a.force, "64x128") && a.vec : p >= 0 && tile_time(a, 2, kTiles[p]) < weights_time(a, 2)) {
+      a.chosen = "64x128";
+      return launch_expert_tile<FMT_BF16, 64, 128, 2, 4, 3, 1, true, KN>(a, s);
+    }
   switch (p) {
     case PICK_REGS: return launch_expert_tile<FMT_BF16, 64, 64, 2, 2, 2, 1, false, KN>(a, s);
     case PICK_REGS_LARGE: return launch_expert_tile<FMT_BF16, 128, 128, 2, 4, 2, 1, false, KN>(a, s);
