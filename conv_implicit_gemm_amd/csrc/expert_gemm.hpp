@@ -959,7 +959,7 @@ int launch_expert_stream(const ExpertArgs& a, hipStream_t s) {
   while (spl < kStreamWaves && nk > spl * kStreamDepth) spl *= 2;
   const int ct = kStreamWaves / spl;
   const int64_t blocks = (int64_t)a.E * ceil_div(a.N, 16 * ct);
-  if (blocks >= ((int64_t)1 << 31)) return (int)hipErrorInvalidValue;
+  if (!fits_one_launch(blocks, kStreamWaves * 64)) return kNoGrid;
   hipLaunchKernelGGL((expert_stream_kernel<FMT>), dim3((uint32_t)blocks), dim3(kStreamWaves * 64), 0, s, a, spl);
   return (int)hipGetLastError();
 }
@@ -1053,7 +1053,7 @@ int launch_expert_tile(const ExpertArgs& a, hipStream_t s) {
   typedef ExpertTileKernel<FMT, BM, BN, WM, WN, S, KS, DMA, KN> TK;
   const int64_t tall = a.offsets ? expert_tile_bound(a.T, a.E, BM) : ceil_div(a.T, BM);
   const int64_t blocks = tall * ceil_div(a.N, BN);
-  if (blocks >= ((int64_t)1 << 31)) return (int)hipErrorInvalidValue;
+  if (!fits_one_launch(blocks, TK::TH)) return kNoGrid;
   hipLaunchKernelGGL((expert_gemm_kernel<FMT, BM, BN, WM, WN, S, KS, DMA, KN>), dim3((uint32_t)blocks), dim3(TK::TH),
                      TK::LDS_BYTES, s, a);
   return (int)hipGetLastError();

@@ -270,10 +270,12 @@ int launch(const QuantF8Args& a, hipStream_t s) {
     const int64_t R = a.R, per = ((int64_t)a.K + 511) / 512;
     const int rw = R * per >= 4 * 256 * 16 ? 4 : 1;
     const int64_t blocks = ((R + rw - 1) / rw * per + kThreads / 64 - 1) / (kThreads / 64);
+    if (!fits_one_launch(blocks, kThreads)) return kNoGrid;
     if (rw == 4) hipLaunchKernelGGL((quant_rows_kernel<F32, VEC, 4>), dim3((uint32_t)blocks), dim3(kThreads), 0, s, a);
     else hipLaunchKernelGGL((quant_rows_kernel<F32, VEC, 1>), dim3((uint32_t)blocks), dim3(kThreads), 0, s, a);
   } else {
     const int64_t blocks = ((int64_t)a.R + 127) / 128 * (((int64_t)a.K + 127) / 128);
+    if (!fits_one_launch(blocks, kThreads)) return kNoGrid;
     hipLaunchKernelGGL((quant_tiles_kernel<F32, VEC>), dim3((uint32_t)blocks), dim3(kThreads), 0, s, a);
   }
   return (int)hipGetLastError();

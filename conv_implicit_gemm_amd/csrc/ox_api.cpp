@@ -1037,7 +1037,11 @@ ox_status ox_quantize_fp8(ox_dtype t, int64_t rows, int64_t K, const void* X, in
   a.Q = Q;
   a.scales = scales;
   a.vec = aligned16(X) && aligned_to(Q, 8) && K % 16 == 0;
-  return hip_result(fn, launch_quantize_fp8(a, stream));
+  const int rc = launch_quantize_fp8(a, stream);
+  if (rc == kNoGrid)
+    return fail(OX_ERR_UNSUPPORTED, "%s: %lld rows of %lld are too many blocks for one launch", fn, (long long)R,
+                (long long)K);
+  return hip_result(fn, rc);
 }
 
 namespace {
@@ -1093,6 +1097,9 @@ ox_status expert_call(const char* fn, int dt, ox_dtype y_type, int64_t T, int64_
                                  : launch_expert_f32(a, stream);
   if (rc == kNoVariant)
     return fail(OX_ERR_UNSUPPORTED, "%s: OX_FORCE_KERNEL=%s does not apply to this call", fn, f.variant);
+  if (rc == kNoGrid)
+    return fail(OX_ERR_UNSUPPORTED, "%s: %lld rows x %lld columns over %lld experts are too many tiles for one launch",
+                fn, (long long)T, (long long)N, (long long)E);
   if (log_on())
     fprintf(stderr, "[ox] %s %lldx%lldx%lld experts %lld: %s\n", fn, (long long)T, (long long)N, (long long)K,
             (long long)E, a.chosen);

@@ -298,8 +298,10 @@ struct ExpertArgs {
   const char* force;       // a variant's name (OX_FORCE_KERNEL), or null
   const char* chosen;      // set by the launchers: the variant that runs
 };
-// the launchers' answer to a forced variant that this call cannot take
-constexpr int kNoVariant = -1;
+// the launchers' answers to a forced variant that this call cannot take, and to
+// a call of more blocks than one launch holds (its threads are counted in 32 bits)
+constexpr int kNoVariant = -1, kNoGrid = -2;
+constexpr bool fits_one_launch(int64_t blocks, int threads) { return blocks * threads < (int64_t)1 << 32; }
 int launch_expert_f32(ExpertArgs& a, void* stream);
 int launch_expert_bf16(ExpertArgs& a, void* stream);
 int launch_expert_fp8(ExpertArgs& a, void* stream);

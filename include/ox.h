@@ -396,6 +396,8 @@ ox_status ox_dynamic_quantize_linear(int64_t n, const float* X, uint8_t* Y, floa
  * index: DEVICE int32 [R] or NULL (then R == rows; required for block_rows =
  *   128): row r of Q is row index[r] of X, e.g. the tokens in their experts'
  *   order.  An index outside [0, rows) gives a row of zeros.
+ * A launch's threads are counted in 32 bits: 2^28 rows of up to 512 columns
+ * and 2^24 blocks of 128 x 128 are OX_ERR_UNSUPPORTED.
  * Q: DEVICE uint8 [R, K].  Rows of a multiple of 16 elements in 16-byte
  * aligned X and 8-byte aligned Q take the vector path. */
 ox_status ox_quantize_fp8(ox_dtype t, int64_t rows, int64_t K, const void* X, int64_t R,
@@ -430,7 +432,8 @@ ox_status ox_gemm_fp8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const ui
  * call can be captured.  Rows before offsets[0] and from offsets[E] on (the
  * unused end of a buffer of fixed capacity) are set to zero.  Offsets that
  * decrease or leave [0, T] leave Y undefined, but nothing outside the
- * tensors is touched. */
+ * tensors is touched.  A launch's threads are counted in 32 bits: 2^24 tiles of 64
+ * x 64 (2^30 rows of one column) are OX_ERR_UNSUPPORTED. */
 ox_status ox_gemm_grouped(ox_dtype t, int64_t T, int64_t N, int64_t K, int64_t E, int transB,
                           const void* A, const void* B, const int32_t* offsets, const void* bias,
                           ox_act act, void* Y, void* stream);
