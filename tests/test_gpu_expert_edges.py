@@ -9,6 +9,8 @@ torch = pytest.importorskip("torch")
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
 
+from test_gpu_expert import VARIANTS, check, check_codes, grouped_plain, quantize_plain, wide  # noqa: E402
+
 F8 = torch.float8_e4m3fn
 
 
@@ -176,3 +178,103 @@ def test_quantize_fp32_halfway_points(ox, br, exact, inf):
         want[:, 127] = 448.0
     Q, S = ox.ox_quantize_fp8(torch.from_numpy(X).cuda(), block_rows=br)
     np.testing.assert_array_equal(Q.float().cpu().numpy().astype(np.float64), want)
+
+
+# Sums of n independent terms in fp32, each addition off by a rounding of about
+# 2^-25.3 of the partial sum (0.29 of a step, at a magnitude between powers of
+# two): the error of a chain of n grows as n * 2^-25.3 / sqrt(2) of a term's size.
+# Chains of at most 256 k added up give sqrt(128 + K / 512) * 2^-25.3 of the norm of
+# a random result (2.8e-7 at K = 4096, 2.9e-7 at 10240), one chain over K
+# sqrt(K / 2) * 2^-25.3 (1.1e-6, 1.7e-6).  The bound lies between.
+NORM = 5e-7
+
+
+def off_norm(got, want):
+    return float(((got.double() - want).norm() / want.norm()).item())
+
+
+@pytest.mark.parametrize("variant", [""] + VARIANTS["f32"] + ["kn " + v for v in VARIANTS["f32 kn"]])
+@pytest.mark.parametrize("K", [4096, 10240])
+def test_fp32_sums_stay_short(ox, monkeypatch, variant, K):
+    kn = variant.startswith("kn ")
+    if variant:
+        monkeypatch.setenv("OX_FORCE_KERNEL", variant.split()[-1])
+    say("fp32 sums", variant, K)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    A, B = torch.randn(48, K, device="cuda", generator=g), torch.randn(1, 256, K, device="cuda", generator=g)
+    off = torch.tensor([0, 48], dtype=torch.int32, device="cuda")
+    Y = ox.ox_gemm_grouped(A, B.transpose(1, 2).contiguous() if kn else B, off, transB=not kn)
+    assert off_norm(Y, A.double() @ B[0].double().t().contiguous()) < NORM
+
+
+@pytest.mark.parametrize("variant", [""] + VARIANTS["fp8x"])
+def test_e4m3_to_fp32_keeps_small_products(ox, monkeypatch, variant):
+    # one large product and one 2^-16 of it, side by side in every way that a
+    # matrix instruction might group them: 448 * 448 + 4 * 1 exactly
+    if variant:
+        monkeypatch.setenv("OX_FORCE_KERNEL", variant)
+    say("small products", variant)
+    M, N, K = 96, 64, 256
+    A, B = torch.zeros(M, K), torch.zeros(N, K)
+    B[:, 0] = 448.0
+    B[:, 1:] = 4.0
+    for m in range(M):
+        A[m, 0] = 448.0
+        A[m, 1 + m] = 1.0
+    one = torch.ones(2, M, device="cuda"), torch.ones(1, 2, device="cuda")
+    Y = ox.ox_gemm_fp8(A.to(F8).cuda(), one[0], B.to(F8).cuda(), one[1], out_dtype=torch.float32)
+    assert (Y == 448.0 * 448.0 + 4.0).all().item()
+
+
+@pytest.mark.parametrize("variant", [""] + VARIANTS["fp8x"])
+def test_e4m3_to_fp32_sums(ox, monkeypatch, variant):
+    if variant:
+        monkeypatch.setenv("OX_FORCE_KERNEL", variant)
+    say("e4m3 to fp32 sums", variant)
+    g = torch.Generator(device="cuda").manual_seed(14)
+    K = 4096
+    A, B = (torch.randn(n, K, device="cuda", generator=g).mul_(60).clamp_(-448, 448).to(F8) for n in (48, 256))
+    sa, sb = torch.rand(K // 128, 48, device="cuda", generator=g) + 0.5, torch.rand(2, K // 128, device="cuda", generator=g) + 0.5
+    Y = ox.ox_gemm_fp8(A, sa, B, sb, out_dtype=torch.float32)
+    a = A.double() * sa.double().t().repeat_interleave(128, dim=1)
+    b = B.double() * sb.double().repeat_interleave(128, dim=0).repeat_interleave(128, dim=1)
+    assert off_norm(Y, a @ b.t().contiguous()) < NORM
+
+
+@pytest.mark.parametrize("tokens,experts,width,hidden", [(5, 8, 256, 512), (100, 4, 384, 640)])
+def test_example_layer_step_by_step(ox, tokens, experts, width, hidden):
+    """Every step of the layer against 64 bits, from the buffers that it ran on."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "expert_layer.py")
+    spec = importlib.util.spec_from_file_location("expert_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    say("example layer", tokens, experts, width, hidden)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    layer = mod.ExpertLayer(tokens, experts, width, hidden, g)
+    X = torch.randn(tokens, width, generator=g, device="cuda").bfloat16()
+    out = layer(X)
+    weight, token, place, offsets = layer.route(X)
+    off = offsets.tolist()
+    bf16 = torch.bfloat16
+
+    def wide64(t):
+        return t.float().cpu().double().numpy()
+    for e in range(experts):
+        for W, q, s in ((layer.W1, layer.q1, layer.s1), (layer.W2, layer.q2, layer.s2)):
+            Q, S, V = quantize_plain(wide64(W[e]), 128)
+            check_codes(q[e], Q, V, bf16)
+            np.testing.assert_array_equal(wide64(s[e]), S)
+    for x, q, s in ((X[token.long()], layer.xq, layer.xs), (layer.h, layer.hq, layer.hs)):
+        Q, S, V = quantize_plain(wide64(x), 1)
+        check_codes(q, Q, V, bf16)
+        np.testing.assert_array_equal(wide64(s), S.T)
+    for a, sa, q, s, bias, act, y in ((layer.xq, layer.xs, layer.q1, layer.s1, wide64(layer.b1), "gelu", layer.h),
+                                      (layer.hq, layer.hs, layer.q2, layer.s2, None, "none", layer.y)):
+        ref, S = grouped_plain(wide(wide64(a), wide64(sa).T, 1), wide(wide64(q), wide64(s), 128), off, bias, act)
+        check(y, ref, S, a.shape[1], bf16, act, "layer", e4m3=True)
+    rows = wide64(layer.y)[place.cpu().numpy()].reshape(tokens, mod.TOP, -1) * wide64(weight)[:, :, None]
+    # two products and a sum in fp32, rounded once to bf16
+    tol = 2.0 ** -8 * np.abs(rows.sum(axis=1)) + 4 * 2.0 ** -24 * np.abs(rows).sum(axis=1)
+    assert (np.abs(wide64(out) - rows.sum(axis=1)) <= tol).all()
