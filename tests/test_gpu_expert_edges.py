@@ -278,3 +278,43 @@ def test_example_layer_step_by_step(ox, tokens, experts, width, hidden):
     # two products and a sum in fp32, rounded once to bf16
     tol = 2.0 ** -8 * np.abs(rows.sum(axis=1)) + 4 * 2.0 ** -24 * np.abs(rows).sum(axis=1)
     assert (np.abs(wide64(out) - rows.sum(axis=1)) <= tol).all()
+
+
+@pytest.mark.parametrize("variant", [""] + VARIANTS["fp8"])
+@pytest.mark.parametrize("kind", ["normal", "positive", "seven"])
+def test_e4m3_to_bf16_loses_what_the_header_says(ox, monkeypatch, variant, kind):
+    """A second block of K holds the negative of each eight's largest product, so
+    that the small products, and what they lose beside it, are the result."""
+    if variant:
+        monkeypatch.setenv("OX_FORCE_KERNEL", variant)
+    say("e4m3 to bf16", variant, kind)
+    M, N = 40, 64
+    rng = np.random.default_rng([15, len(kind)])
+    if kind == "seven":                     # seven products just below the cut: all of them are lost
+        a, b = np.full((M, 128), 1.875), np.full((N, 128), 3.75)
+        a[:, ::8], b[:, ::8] = 256.0, 256.0
+    else:
+        a, b = (np.exp2(rng.integers(-2, 5, (n, 128))) * (1 + rng.integers(0, 8, (n, 128)) / 8) for n in (M, N))
+        if kind == "normal":
+            a *= rng.choice([-1, 1], a.shape)
+        a[:, ::8] *= 8.0
+        b[:, ::8] *= 8.0
+    A, B = np.concatenate([a, np.zeros((M, 128))], axis=1), np.concatenate([b, np.zeros((N, 128))], axis=1)
+    A[:, 128::8], B[:, 128::8] = -a[:, ::8], b[:, ::8]
+    ta, tb = torch.from_numpy(A).float().to(F8), torch.from_numpy(B).float().to(F8)
+    assert (ta.double().numpy() == A).all() and (tb.double().numpy() == B).all()
+
+    def power(x):
+        return np.exp2(np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -30))))
+    P = A[:, None] * B[None]                                                   # [M, N, 256]
+    tops = (power(A)[:, None] * power(B)[None] * (P != 0)).reshape(M, N, 32, 8).max(axis=3, keepdims=True)
+    cut = 2.0 ** -13 * np.maximum(tops, 2.0 ** -60)
+    P8 = P.reshape(M, N, 32, 8)
+    want, exact = (np.trunc(P8 / cut) * cut).sum(axis=(2, 3)), P.sum(axis=2)
+    lost = np.abs(want - exact)
+    assert (lost <= 7 * 2.0 ** -13 * np.abs(P8).max(axis=3).sum(axis=2)).all() and lost.max() > 0
+    Y = ox.ox_gemm_fp8(ta.cuda(), torch.ones(2, M, device="cuda"), tb.cuda(), torch.ones(1, 2, device="cuda"))
+    got = Y.double().cpu().numpy()
+    # the additions between the eights (fp32, and exact up to 2^-23 of the sums) and the rounding to bf16
+    tol = 2.0 ** -8 * np.abs(want) + 64 * 2.0 ** -23 * np.abs(P).sum(axis=2)
+    assert (np.abs(got - want) <= tol).all()
