@@ -232,7 +232,7 @@ __device__ __forceinline__ bool find_tile(const ExpertArgs& a, int NT, ExpertTil
 // back with transposing LDS reads.
 //
 // What bounds it: at 8192^3 e4m3 (256 x 256, two waves a SIMD, 128 accumulator
-// registers each) 478 us, 2.3 PFLOP/s: the matrix units are busy 54% of the
+// registers each) 468 to 492 us on different cards, 2.2 to 2.35 PFLOP/s: the matrix units are busy 54% of the
 // cycles, LDS reads take 75% of what it delivers in a step (24 KB a wave and
 // block of K, the reason for the tall wave tiles), and each tile adds 11 us,
 // 6 of them the stores of all CUs at once.  bf16 at 8192^3: 1.3 PFLOP/s.

@@ -19,8 +19,10 @@ template <bool KN>
 int launch(ExpertArgs& a, hipStream_t s) {
   const int p = pick_variant(a, 2, kTiles);
   // [K, N] weights that take longer to read than to multiply: blocks as wide
-  // as 256 bytes of their rows (64 experts of 2048 x 1024, 4003 rows: 60 us,
-  // 70 us on 64 x 64 and 68 us on 256 x 256)
+  // as 256 bytes of their rows (64 experts of 2048 x 1024, 4003 rows: 62 us, 71
+  // on 64 x 64; 300 rows over 16 of 2048 x 2000: 24.1 us, 24.9 on 64 x 64; 1000
+  // over 16 of 4096 x 4096: 125 us, 119 on 256 x 256; 64 over 4 of 4096 x 4096,
+  // the worst found: 30.1 us, 25.7 on 32 x 64)
   if constexpr (KN)
     if (a.force ? !strcmp(a.force, "64x128") && a.vec : p >= 0 && tile_time(a, 2, kTiles[p]) < weights_time(a, 2)) {
       a.chosen = "64x128";
