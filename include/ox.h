@@ -421,7 +421,8 @@ ox_status ox_quantize_fp8(ox_dtype t, int64_t rows, int64_t K, const void* X, in
  * bias: DEVICE [N] of y_type, or NULL.  NaN codes give NaN sums (which ReLU
  * and ReLU6 take to 0, as everywhere in this library).  With few rows the
  * weights are streamed once and K is divided over the waves of a block; the
- * order of every sum depends on the sizes alone. */
+ * order of every sum depends on the sizes, and on whether the rows start on 16
+ * bytes, alone. */
 ox_status ox_gemm_fp8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const uint8_t* A,
                       const float* a_scales, const uint8_t* B, const float* b_scales, const void* bias,
                       ox_act act, void* Y, void* stream);
@@ -437,8 +438,8 @@ ox_status ox_gemm_fp8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const ui
  * call can be captured.  Rows before offsets[0] and from offsets[E] on (the
  * unused end of a buffer of fixed capacity) are set to zero.  Offsets that
  * decrease or leave [0, T] leave Y undefined, but nothing outside the
- * tensors is touched.  A launch's threads are counted in 32 bits: 2^24 tiles of 64
- * x 64 (2^30 rows of one column) are OX_ERR_UNSUPPORTED. */
+ * tensors is touched.  A launch's threads are counted in 32 bits: 2^24 tiles
+ * of 64 x 64 (2^30 rows of one column) are OX_ERR_UNSUPPORTED. */
 ox_status ox_gemm_grouped(ox_dtype t, int64_t T, int64_t N, int64_t K, int64_t E, int transB,
                           const void* A, const void* B, const int32_t* offsets, const void* bias,
                           ox_act act, void* Y, void* stream);
