@@ -31,7 +31,7 @@ EXPORTS = ("ox_matmul_batched", "ox_gemm_fused", "ox_conv2d_fused", "ox_conv2d_i
            "ox_int8_prepare_ex", "ox_dynamic_quantize_workspace_bytes", "ox_dynamic_quantize_linear",
            "ox_matmul_nbits", "ox_gemm_workspace_bytes", "ox_gemm_fused_ws",
            "ox_static_scratch_bytes", "ox_conv2d_fused_static", "ox_quantize_fp8", "ox_gemm_fp8",
-           "ox_gemm_grouped", "ox_gemm_grouped_fp8")
+           "ox_gemm_grouped", "ox_gemm_grouped_fp8", "ox_quantize_i8", "ox_gemm_i8", "ox_rmsnorm")
 
 
 class OxError(RuntimeError):
@@ -86,6 +86,9 @@ def _load():
         "ox_gemm_fp8": (I, [I, I64, I64, I64, P, P, P, P, P, I, P, P]),
         "ox_gemm_grouped": (I, [I, I64, I64, I64, I64, I, P, P, P, P, I, P, P]),
         "ox_gemm_grouped_fp8": (I, [I, I64, I64, I64, I64, P, P, P, P, P, P, I, P, P]),
+        "ox_quantize_i8": (I, [I, I64, I64, P, P, P, P]),
+        "ox_gemm_i8": (I, [I, I64, I64, I64, P, P, P, P, P, I, P, P]),
+        "ox_rmsnorm": (I, [I, I64, I64, P, P, P, F, P, I, P, P, P]),
         "ox_last_error": (C.c_char_p, []),
         "ox_version": (C.c_char_p, []),
     }
@@ -310,6 +313,7 @@ def ox_matmul_nbits(A, B, scales, K, zero_points=None, bias=None, Y=None, stream
 # as a raw handle (0.1 us; a current_stream() object takes 2.8 us).
 
 _F8 = None        # torch's types, looked up once: (float8_e4m3fn, uint8, float32, int32, raw stream function)
+_I8 = None        # int8 and bfloat16, likewise
 
 
 def _types():
@@ -514,6 +518,143 @@ def ox_gemm_grouped_fp8(A, a_scales, B, b_scales, offsets, bias=None, act="none"
     if st:
         _check(st)
     return Y
+
+
+def _small_types():
+    global _I8
+    if _I8 is None:
+        torch = _torch()
+        _I8 = (torch.int8, torch.bfloat16)
+    return _I8
+
+
+def ox_quantize_i8(X, Q=None, scales=None, stream=None):
+    """int8 codes and one fp32 scale per row of a dense device matrix X (float32
+    or bfloat16) [rows, K], K up to 65536.  Returns (Q int8 [rows, K], scales
+    float32 [rows])."""
+    f8, u8, f32, i32, raw = _F8 or _types()
+    i8 = (_I8 or _small_types())[0]
+    rows, K = X.shape
+    if Q is None:
+        Q = _new_result((rows, K), i8, X.device)
+    elif Q.shape != (rows, K):
+        raise _shape_error("Q", Q, (rows, K))
+    elif Q.dtype != i8:
+        raise TypeError("Q must be int8")
+    if scales is None:
+        scales = _new_result((rows,), f32, X.device)
+    elif scales.shape != (rows,):
+        raise _shape_error("scales", scales, (rows,))
+    elif scales.dtype != f32:
+        raise TypeError("scales must be float32")
+    code = _dtype_code(X)
+    dev = X.get_device()
+    if not (dev >= 0 and Q.get_device() == dev and scales.get_device() == dev and X.is_contiguous()
+            and Q.is_contiguous() and scales.is_contiguous()):
+        raise _refuse_memory(("X", "Q", "scales"), X, Q, scales)
+    st = lib.ox_quantize_i8(code, rows, K, X.data_ptr(), Q.data_ptr(), scales.data_ptr(),
+                            raw(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
+    return Q, scales
+
+
+def ox_gemm_i8(A, a_scales, B, b_scales, bias=None, act="none", Y=None, out_dtype=None, stream=None):
+    """Y [M, N] = act(a_scales[m] b_scales[n] (A B^T)[m, n] + bias[n]) for int8 A
+    [M, K] and B [N, K] with float32 scales [M] and [N] (as ox_quantize_i8 makes
+    them).  Y's type (out_dtype, default bfloat16, or float32) is the bias's too."""
+    f8, u8, f32, i32, raw = _F8 or _types()
+    i8 = (_I8 or _small_types())[0]
+    M, K = A.shape
+    N, Kb = B.shape
+    if Kb != K:
+        raise ValueError("B has %d columns, A %d" % (Kb, K))
+    if A.dtype != i8 or B.dtype != i8:
+        raise TypeError("A and B must be int8, not %s and %s" % (A.dtype, B.dtype))
+    if a_scales.dtype != f32 or b_scales.dtype != f32:
+        raise TypeError("a_scales and b_scales must be float32")
+    if a_scales.shape != (M,):
+        raise _shape_error("a_scales", a_scales, (M,))
+    if b_scales.shape != (N,):
+        raise _shape_error("b_scales", b_scales, (N,))
+    if Y is None:
+        Y = _new_result((M, N), out_dtype, A.device)
+    elif Y.shape != (M, N):
+        raise _shape_error("Y", Y, (M, N))
+    if bias is not None:
+        _check_bias(bias, (N,), Y)
+    code = _dtype_code(Y)
+    dev = A.get_device()
+    if not (dev >= 0 and a_scales.get_device() == dev and B.get_device() == dev and b_scales.get_device() == dev
+            and Y.get_device() == dev and A.is_contiguous() and a_scales.is_contiguous() and B.is_contiguous()
+            and b_scales.is_contiguous() and Y.is_contiguous()
+            and (bias is None or (bias.get_device() == dev and bias.is_contiguous()))):
+        raise _refuse_memory(("A", "a_scales", "B", "b_scales", "Y", "bias"), A, a_scales, B, b_scales, Y, bias)
+    st = lib.ox_gemm_i8(code, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(), b_scales.data_ptr(),
+                        None if bias is None else bias.data_ptr(), ACT[act], Y.data_ptr(),
+                        raw(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
+    return Y
+
+
+def ox_rmsnorm(X, gamma=None, residual=None, eps=1e-6, out="same", Y=None, scales=None, S=None, stream=None):
+    """y = s / sqrt(mean(s^2) + eps) * gamma over the rows of s = X + residual,
+    X [rows, K] float32 or bfloat16, K up to 65536.  out: "same" (y in X's type),
+    "fp8" (float8_e4m3fn codes, scales [ceil(K/128), rows] as ox_gemm_fp8 takes
+    them) or "i8" (int8 codes, scales [rows] as ox_gemm_i8 takes them).  With a
+    residual, s itself goes to S (X or residual for in place; made if None).
+    Returns (Y, scales or None, S or None)."""
+    f8, u8, f32, i32, raw = _F8 or _types()
+    i8 = (_I8 or _small_types())[0]
+    rows, K = X.shape
+    dtype = X.dtype
+    if out == "same":
+        code, shape, want = _dtype_code(X), None, dtype
+    elif out == "fp8":
+        code, shape, want = OX_F8E4M3, ((K + 127) >> 7, rows), f8
+    elif out == "i8":
+        code, shape, want = OX_I8, (rows,), i8
+    else:
+        raise ValueError("out must be 'same', 'fp8' or 'i8'")
+    if Y is None:
+        Y = _new_result((rows, K), want, X.device)
+    elif Y.shape != (rows, K):
+        raise _shape_error("Y", Y, (rows, K))
+    elif Y.dtype != want and not (want is f8 and Y.dtype == u8):
+        raise TypeError("Y is %s, not %s" % (Y.dtype, want))
+    if shape is None:
+        if scales is not None:
+            raise ValueError("scales go with out='fp8' or 'i8'")
+    elif scales is None:
+        scales = _new_result(shape, f32, X.device)
+    elif scales.shape != shape:
+        raise _shape_error("scales", scales, shape)
+    elif scales.dtype != f32:
+        raise TypeError("scales must be float32")
+    if gamma is not None and (gamma.shape != (K,) or gamma.dtype != dtype):
+        raise _shape_error("gamma", gamma, (K,)) if gamma.shape != (K,) else TypeError("gamma is %s, X %s" % (gamma.dtype, dtype))
+    if residual is not None:
+        if S is None:
+            S = _new_result((rows, K), dtype, X.device)
+        for name, t in (("residual", residual), ("S", S)):
+            if t.shape != (rows, K):
+                raise _shape_error(name, t, (rows, K))
+            if t.dtype != dtype:
+                raise TypeError("%s is %s, X %s" % (name, t.dtype, dtype))
+    elif S is not None:
+        raise ValueError("S needs a residual")
+    dev = X.get_device()
+    for t in (X, Y, scales, gamma, residual, S):
+        if t is not None and (dev < 0 or t.get_device() != dev or not t.is_contiguous()):
+            raise _refuse_memory(("X", "Y", "scales", "gamma", "residual", "S"), X, Y, scales, gamma, residual, S)
+    st = lib.ox_rmsnorm(_dtype_code(X), rows, K, X.data_ptr(), None if residual is None else residual.data_ptr(),
+                        None if gamma is None else gamma.data_ptr(), eps, None if S is None else S.data_ptr(), code,
+                        Y.data_ptr(), None if scales is None else scales.data_ptr(),
+                        raw(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
+    return Y, scales, S
 
 
 def ox_dynamic_quantize_linear(X, Y=None, y_scale=None, y_zp=None, workspace=None, stream=None):

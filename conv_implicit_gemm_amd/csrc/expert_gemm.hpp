@@ -50,12 +50,31 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 // from zero again (one chain over K = 2800 is 9e-7 of the norm off, this 3e-7
 // for any K; adding every block costs 10% of the time, as the fp32 instruction
 // leaves the vector unit no room beside it).
-enum Fmt : int { FMT_BF16 = 0, FMT_FP8 = 1, FMT_FP8X = 2, FMT_F32 = 3 };
+// int8 operands take the K = 64 int8 instruction; their sums are int32, exact,
+// kept in the same registers as the others' (only the bits travel as floats),
+// and meet the scales (one per row of A, one per row of B) with the bias.
+enum Fmt : int { FMT_BF16 = 0, FMT_FP8 = 1, FMT_FP8X = 2, FMT_F32 = 3, FMT_I8 = 4 };
 
 template <int FMT>
 struct FmtOps {
   static constexpr bool F8 = FMT == FMT_FP8 || FMT == FMT_FP8X;
-  static constexpr int ESZ = F8 ? 1 : FMT == FMT_F32 ? 4 : 2;
+  static constexpr bool INT = FMT == FMT_I8;
+  static constexpr int ESZ = F8 || INT ? 1 : FMT == FMT_F32 ? 4 : 2;
+  // c + o: sums of products, or what the integers behind them add up to
+  static __device__ __forceinline__ f32x4_t add(f32x4_t c, f32x4_t o) {
+    if constexpr (INT) {
+      return __builtin_bit_cast(f32x4_t, __builtin_bit_cast(i32x4_t, c) + __builtin_bit_cast(i32x4_t, o));
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) c[r] += o[r];
+      return c;
+    }
+  }
+  // the sum that v holds, under its scales (int8)
+  static __device__ __forceinline__ float value(float v, float sa, float sb) {
+    if constexpr (INT) return (float)__float_as_int(v) * sa * sb;
+    return v;
+  }
   // a fragment's 128 bytes of K as the matrix instructions take them
   struct Frag { u32x4_t v[FMT == FMT_FP8X ? 4 : 2]; };
   static __device__ __forceinline__ Frag widen(u32x4_t x, u32x4_t y) {
@@ -84,6 +103,9 @@ struct FmtOps {
       for (int i = 0; i < 4; ++i)
         c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b.v[H][i]), __uint_as_float(a.v[H][i]), c, 0, 0, 0);
       return c;
+    } else if constexpr (INT) {
+      return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_mfma_i32_16x16x64_i8(
+          __builtin_bit_cast(i32x4_t, b.v[H]), __builtin_bit_cast(i32x4_t, a.v[H]), __builtin_bit_cast(i32x4_t, c), 0, 0, 0));
     } else {
       return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b.v[H]),
                                                      __builtin_bit_cast(bf16x8_t, a.v[H]), c, 0, 0, 0);
@@ -260,7 +282,7 @@ struct ExpertTileKernel {
   static_assert(DMA || KS == 1, "one block per stage through registers");
   static_assert(MF % 2 == 0, "row fragments alternate between two sets of block sums");
   static_assert(!KN || (NF & (NF - 1)) == 0, "fragments are bits of the column");
-  static_assert(!KN || !F8, "e4m3 weights are [N, K]");
+  static_assert(!KN || ESZ > 1, "8-bit weights are [N, K]");
   static_assert(!KN || FMT != FMT_F32 || BN % 64 == 0, "the swizzle of fp32 rows spans 64 columns");
   static_assert(!F8 || TN <= 128, "a wave's columns share a scale block");
 
@@ -586,9 +608,19 @@ struct ExpertTileKernel {
         }
       }
   }
+  // int8: the columns' scales, as the biases
+  __device__ __forceinline__ void load_scales(const Where& t, int wn, float (&sv)[NF][4]) const {
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int n = col_of(wn, j, r);
+        sv[j][r] = Mm::INT && n < t.cols ? a.sb[(int64_t)t.e * a.N + t.n0 + n] : 0.0f;
+      }
+  }
   template <int ACT>
   __device__ __forceinline__ void store(const Where& t, int wm, int wn, const f32x4_t (&acc)[MF][NF],
-                                        const float (&bv)[NF][4]) const {
+                                        const float (&bv)[NF][4], const float (&sv)[NF][4], const float (&sm)[MF]) const {
     const int lane = threadIdx.x & 63, cols = t.cols;
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
@@ -598,7 +630,7 @@ struct ExpertTileKernel {
 #pragma unroll
       for (int j = 0; j < NF; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[j][r] = act_c<ACT>(acc[f][j][r] + bv[j][r]);
+        for (int r = 0; r < 4; ++r) v[j][r] = act_c<ACT>(Mm::value(acc[f][j][r], sm[f], sv[j][r]) + bv[j][r]);
       const int64_t at = (int64_t)(t.row0 + m) * a.N + t.n0;
       if (a.out_dt == DT_F32) {
         float* y = (float*)a.Y + at;
@@ -790,14 +822,17 @@ struct ExpertTileKernel {
 #pragma unroll
           for (int j = 0; j < NF; ++j) {
             const f32x4_t o = part[(q * NW * MF * NF + f * NF + j) * 64];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[f][j][r] += o[r];
+            acc[f][j] = Mm::add(acc[f][j], o);
           }
     }
-    float bv[NF][4];
+    float bv[NF][4], sv[NF][4], sm[MF];
     load_bias(t, wn, bv);
+    load_scales(t, wn, sv);
+#pragma unroll
+    for (int f = 0; f < MF; ++f)
+      sm[f] = Mm::INT ? a.sa[t.row0 + min(wm * TM + f * 16 + (int)(threadIdx.x & 15), t.rows - 1)] : 0.0f;
     wait_vmem();
-    with_act(a.act, [&](auto act) { store<decltype(act)::value>(t, wm, wn, acc, bv); });
+    with_act(a.act, [&](auto act) { store<decltype(act)::value>(t, wm, wn, acc, bv, sv, sm); });
   }
 };
 
@@ -887,10 +922,10 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
           const int o = (k + u) * 128 + g * 16;
           const bool in = k + u < k1;
           // what was read again counts as zeros on both sides: an infinity on
-          // either would make 0 * inf (e4m3 codes have none, and a NaN among
+          // either would make 0 * inf (8-bit codes have none, and a NaN among
           // the weights has made its column's sum NaN already)
           const bool px = in && o <= last_piece, py = in && o + 64 <= last_piece;
-          const Frag b = Mm::widen(F8 || px ? wx[u] : zero, F8 || py ? wy[u] : zero);
+          const Frag b = Mm::widen(ESZ == 1 || px ? wx[u] : zero, ESZ == 1 || py ? wy[u] : zero);
           const Frag x = Mm::widen(px ? ax[u] : zero, py ? ay[u] : zero);
           if constexpr (F8) {
             const f32x4_t p = Mm::block(b, x);
@@ -902,10 +937,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
             chain = Mm::template half<1>(b, x, chain);
           }
         }
-        if constexpr (!F8) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r] += chain[r];
-        }
+        if constexpr (!F8) acc = Mm::add(acc, chain);
       }
     }
     if (SPL > 1) {
@@ -915,20 +947,22 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
       __syncthreads();
       if (sl != 0) continue;
       for (int q = 1; q < SPL; ++q)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] += part[wave + q][r][lane];
+        acc = Mm::add(acc, f32x4_t{part[wave + q][0][lane], part[wave + q][1][lane], part[wave + q][2][lane],
+                                   part[wave + q][3][lane]});
     }
     const int n = n0 + g * 4;
     if (!live || m >= hi || n >= a.N) continue;
     float v[4];
+    const float sm = Mm::INT ? a.sa[m] : 0.0f;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float bv = 0.0f;
+      const float sv = Mm::INT && n + r < a.N ? a.sb[(int64_t)e * a.N + n + r] : 0.0f;
       if (a.bias && n + r < a.N) {
         const int64_t at = (int64_t)e * a.N + n + r;
         bv = a.out_dt == DT_F32 ? ((const float*)a.bias)[at] : bf16_to_f32(((const uint16_t*)a.bias)[at]);
       }
-      v[r] = apply_act(a.act, acc[r] + bv);
+      v[r] = apply_act(a.act, Mm::value(acc[r], sm, sv) + bv);
     }
     const int64_t at = (int64_t)m * a.N + n;
     if (a.out_dt == DT_F32) {

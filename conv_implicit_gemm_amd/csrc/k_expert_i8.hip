@@ -1,0 +1,37 @@
+// k_expert_i8.hip -- int8 products with a scale for each row of both operands
+// (expert_gemm.hpp).
+#include "expert_gemm.hpp"
+
+namespace ox {
+
+namespace {
+
+// (xN: K divided over N groups of waves)
+constexpr TileCost kTiles[] = {{"32x64", 32, 64, 4, 2.5, 0.30, 0.60},
+                               {"64x64", 64, 64, 3, 2.5, 0.42, 0.57},
+                               {"128x128", 128, 128, 2, 5.3, 0.69, 1.07},
+                               {"256x256", 256, 256, 1, 11.3, 1.68, 1.68},
+                               {"32x32x4", 32, 32, 2, 3.0, 0.19, 0.22},
+                               {"64x64x2", 64, 64, 1, 3.0, 0.285, 0.285},
+                               {"128x128x2", 128, 128, 1, 5.5, 0.60, 0.60}};
+
+}  // namespace
+
+int launch_expert_i8(ExpertArgs& a, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  switch (pick_variant(a, 1, kTiles)) {
+    case PICK_REGS: return launch_expert_tile<FMT_I8, 64, 64, 2, 2, 2, 1, false, false>(a, s);
+    case PICK_REGS_LARGE: return launch_expert_tile<FMT_I8, 128, 128, 2, 4, 2, 1, false, false>(a, s);
+    case PICK_STREAM: return launch_expert_stream<FMT_I8>(a, s);
+    case 0: return launch_expert_tile<FMT_I8, 32, 64, 1, 4, 3, 1, true, false>(a, s);
+    case 1: return launch_expert_tile<FMT_I8, 64, 64, 2, 2, 3, 1, true, false>(a, s);
+    case 2: return launch_expert_tile<FMT_I8, 128, 128, 2, 4, 2, 1, true, false>(a, s);
+    case 3: return launch_expert_tile<FMT_I8, 256, 256, 2, 4, 2, 1, true, false>(a, s);
+    case 4: return launch_expert_tile<FMT_I8, 32, 32, 1, 2, 2, 4, true, false>(a, s);
+    case 5: return launch_expert_tile<FMT_I8, 64, 64, 2, 2, 3, 2, true, false>(a, s);
+    case 6: return launch_expert_tile<FMT_I8, 128, 128, 2, 4, 2, 2, true, false>(a, s);
+    default: return kNoVariant;
+  }
+}
+
+}  // namespace ox

@@ -1,0 +1,282 @@
+// k_norm.hip -- kernels that hold a row in registers: the RMS norm with the
+// residual's addition and results of 8 bits with scales, and the quantisation
+// to int8 with a scale per row.
+//
+//   s = x + r,  z = s * gamma,  y = z / sqrt(mean(s^2) + eps)
+//   same type:  y, rounded once
+//   e4m3:       per block of 128, m = max|y|: scale m / 448, code 448 y / m
+//   int8:       per row, m = max|y|: scale m / 127, code rint(127 y / m)
+//
+// A code does not need the norm: 448 y / m = 448 z / max|z|.  So the sum of
+// squares and the largest |z| are found in one pass and cross the row's threads
+// together, behind one barrier, and the codes are those of exact quotients of z.
+// Where that shortcut does not hold (infinities or NaN in the row, magnitudes
+// next to the ends of fp32) the codes are taken of y itself.
+//
+// A row's TPR threads hold eight neighbouring elements C times over; a wave
+// has a row of up to 1024 for itself, longer rows have a block of threads.  What
+// bounds it is the bytes, each read or written once.
+#include "quant_codes.hpp"
+
+namespace ox {
+
+namespace {
+
+enum Out : int { OUT_SAME = 0, OUT_F8 = 1, OUT_I8 = 2 };
+
+struct __attribute__((packed, aligned(1))) Bytes16 { u32x4_t v; };
+struct __attribute__((packed, aligned(1))) Bytes8 { u32x2_t v; };
+
+// Eight elements at p; `n` of them lie in the row (others: zeros).  Whole pieces
+// take vector accesses from any address; a row's last piece is taken apart.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&x)[8]) {
+  if (n >= 8) {
+    if constexpr (F32) {
+      const float* p = (const float*)base + at;
+      const u32x4_t u = ((const Bytes16*)p)->v, v = ((const Bytes16*)(p + 4))->v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = __uint_as_float(u[i]);
+        x[i + 4] = __uint_as_float(v[i]);
+      }
+    } else {
+      const u32x4_t u = ((const Bytes16*)((const uint16_t*)base + at))->v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = 0.0f;
+      if (i < n) x[i] = F32 ? ((const float*)base)[at + i] : bf16_to_f32(((const uint16_t*)base)[at + i]);
+    }
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void store8(void* base, int64_t at, int n, const float (&x)[8]) {
+  if (n >= 8) {
+    if constexpr (F32) {
+      float* p = (float*)base + at;
+      ((Bytes16*)p)->v = u32x4_t{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+      ((Bytes16*)(p + 4))->v = u32x4_t{__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7])};
+    } else {
+      ((Bytes16*)((uint16_t*)base + at))->v =
+          u32x4_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        if constexpr (F32) ((float*)base)[at + i] = x[i];
+        else ((uint16_t*)base)[at + i] = (uint16_t)pack_bf16x2(x[i], 0.0f);
+      }
+  }
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* y, int n, u32x2_t q) {
+  if (n >= 8) {
+    ((Bytes8*)y)->v = q;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) y[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+  }
+}
+
+// over the 64 lanes of a wave, in every lane
+__device__ __forceinline__ uint32_t wave_max(uint32_t m) {
+  m = max16(m);
+  m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+  return max(m, (uint32_t)__shfl_xor((int)m, 32));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+  return v;
+}
+
+// The largest `m` and the sum of `v` over a row's threads (the waves' parts are
+// added in their order).
+template <int TPR>
+__device__ __forceinline__ void row_reduce(float& v, uint32_t& m, float* sums, uint32_t* tops) {
+  v = wave_sum(v);
+  m = wave_max(m);
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    if ((threadIdx.x & 63) == 0) {
+      sums[threadIdx.x >> 6] = v;
+      tops[threadIdx.x >> 6] = m;
+    }
+    __syncthreads();
+    v = 0.0f;
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      v += sums[i];
+      m = max(m, tops[i]);
+    }
+  }
+}
+
+constexpr int row_threads(int TPR) { return TPR > kThreads ? TPR : kThreads; }
+
+template <bool F32, int OUT, bool NORM, int TPR, int C>
+__global__ __launch_bounds__(row_threads(TPR)) void row_kernel(const NormArgs a) {
+  constexpr int RPB = row_threads(TPR) / TPR;      // rows of a block
+  __shared__ float sums[2][TPR / 64];
+  __shared__ uint32_t tops[2][TPR / 64];
+  const int t = threadIdx.x % TPR;
+  // (blocks of an XCD take neighbouring rows: their scales share lines of its L2)
+  const uint32_t row = (uint32_t)xcd_tile(blockIdx.x, gridDim.x) * RPB + threadIdx.x / TPR;
+  if (row >= (uint32_t)a.rows) return;             // (whole waves; rows of a block share no barrier)
+  const int64_t at = (int64_t)row * a.K;
+  float z[C][8];
+  int n[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int k = (c * TPR + t) * 8;
+    n[c] = a.K - k;
+    load8<F32>(a.X, at + k, n[c], z[c]);
+  }
+  float ss = 0.0f;
+  if constexpr (NORM) {
+    if (a.residual) {
+      float r[C][8];
+#pragma unroll
+      for (int c = 0; c < C; ++c) load8<F32>(a.residual, at + (c * TPR + t) * 8, n[c], r[c]);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[c][i] += r[c][i];
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(z[c][i], z[c][i], ss);
+    if (a.sum_out) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) store8<F32>(a.sum_out, at + (c * TPR + t) * 8, n[c], z[c]);
+    }
+    if (a.gamma) {
+      float g[8];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        load8<F32>(a.gamma, (c * TPR + t) * 8, n[c], g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[c][i] *= g[i];
+      }
+    }
+  }
+  uint32_t top = 0, block_top[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    block_top[c] = OUT == OUT_SAME ? 0u : amax8<false>(z[c]);
+    top = max(top, block_top[c]);
+  }
+  if constexpr (NORM || OUT == OUT_I8) row_reduce<TPR>(ss, top, sums[0], tops[0]);
+  const float rs = NORM ? 1.0f / sqrtf(ss / (float)a.K + a.eps) : 1.0f;
+
+  if constexpr (OUT == OUT_SAME) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[c][i] *= rs;
+      store8<F32>(a.Y, at + (c * TPR + t) * 8, n[c], z[c]);
+    }
+  } else if constexpr (OUT == OUT_I8) {
+    const float zm = __uint_as_float(top);
+    const bool plain = top < kInfBits && ss < __uint_as_float(kInfBits) && zm >= kTiny && zm * rs >= kTiny &&
+                       zm * rs < __uint_as_float(kInfBits);      // (the same in all the row's threads)
+    float m = zm;
+    uint32_t any = 0;
+    if (!plain) {
+      uint32_t fin = 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[c][i] *= rs;
+        any = max(any, amax8<false>(z[c]));
+        fin = max(fin, amax8<true>(z[c]));
+      }
+      float all = __uint_as_float(0);
+      uint32_t both = fin;
+      row_reduce<TPR>(all, both, sums[1], tops[1]);
+      fin = both;
+      // a NaN in the row: its scale is NaN too, as no int8 code can say it
+      if constexpr (TPR > 64) any = (uint32_t)__syncthreads_or(any > kInfBits);
+      else any = __any(any > kInfBits) ? 1u : 0u;
+      m = block_max(fin);
+    }
+    if (t == 0) a.scales[row] = any ? __uint_as_float(0x7fc00000u) : (plain ? m * rs : m) / 127.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const u32x2_t q = plain ? codes8_i8<false>(z[c], m) : codes8_i8<true>(z[c], m);
+      store_codes((uint8_t*)a.Y + at + (c * TPR + t) * 8, n[c], q);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t bits = max16(block_top[c]);
+      const float zm = __uint_as_float(bits);
+      const bool plain = bits < kInfBits && ss < __uint_as_float(kInfBits) && zm >= kTiny && zm * rs >= kTiny &&
+                         zm * rs < __uint_as_float(kInfBits);    // (the same in a block's sixteen lanes)
+      float m = zm, scale = zm * rs / kMax;
+      u32x2_t q;
+      if (plain) {
+        q = codes8<true, false>(z[c], m);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[c][i] *= rs;
+        m = block_max(max16(amax8<true>(z[c])));
+        scale = m / kMax;
+        q = codes8<true, true>(z[c], m);
+      }
+      const int k = (c * TPR + t) * 8;
+      store_codes((uint8_t*)a.Y + at + k, n[c], q);
+      if (n[c] > 0 && (t & 15) == 0) a.scales[(int64_t)(k >> 7) * a.rows + row] = scale;
+    }
+  }
+}
+
+template <bool F32, int OUT, bool NORM, int TPR, int C>
+int launch(const NormArgs& a, hipStream_t s) {
+  constexpr int TH = row_threads(TPR), RPB = TH / TPR;
+  const int64_t blocks = ((int64_t)a.rows + RPB - 1) / RPB;
+  if (!fits_one_launch(blocks, TH)) return kNoGrid;
+  hipLaunchKernelGGL((row_kernel<F32, OUT, NORM, TPR, C>), dim3((uint32_t)blocks), dim3(TH), 0, s, a);
+  return (int)hipGetLastError();
+}
+
+template <bool F32, int OUT, bool NORM>
+int pick(const NormArgs& a, hipStream_t s) {
+  if (a.K <= 512) return launch<F32, OUT, NORM, 64, 1>(a, s);
+  if (a.K <= 1024) return launch<F32, OUT, NORM, 64, 2>(a, s);
+  if (a.K <= 2048) return launch<F32, OUT, NORM, 256, 1>(a, s);
+  if (a.K <= 4096) return launch<F32, OUT, NORM, 256, 2>(a, s);
+  if (a.K <= 8192) return launch<F32, OUT, NORM, 512, 2>(a, s);
+  if (a.K <= 16384) return launch<F32, OUT, NORM, 1024, 2>(a, s);
+  if (a.K <= 32768) return launch<F32, OUT, NORM, 1024, 4>(a, s);
+  return launch<F32, OUT, NORM, 1024, 8>(a, s);
+}
+
+}  // namespace
+
+int launch_rmsnorm(const NormArgs& a, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  const bool f32 = a.dt == DT_F32;
+  if (a.out_dt == DT_F8) return f32 ? pick<true, OUT_F8, true>(a, s) : pick<false, OUT_F8, true>(a, s);
+  if (a.out_dt == DT_I8) return f32 ? pick<true, OUT_I8, true>(a, s) : pick<false, OUT_I8, true>(a, s);
+  return f32 ? pick<true, OUT_SAME, true>(a, s) : pick<false, OUT_SAME, true>(a, s);
+}
+
+int launch_quantize_i8(const NormArgs& a, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  return a.dt == DT_F32 ? pick<true, OUT_I8, false>(a, s) : pick<false, OUT_I8, false>(a, s);
+}
+
+}  // namespace ox

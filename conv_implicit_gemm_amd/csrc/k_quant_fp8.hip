@@ -14,14 +14,11 @@
 // each; the maximum crosses them with four DPP steps.  What bounds it is the
 // bytes: each element is read once and its code written once (16384 gathered
 // rows of 4096 bf16, 201 MB: 37 us, 5.4 TB/s; 24 rows: 2.5 us, one trip to HBM).
-#include "engine.hpp"
+#include "quant_codes.hpp"
 
 namespace ox {
 
 namespace {
-
-constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100: below it 448 / m would leave fp32
-constexpr float kMax = 448.0f;
 
 // Columns and rows of a last block run past K and R, which end below 2^31: they
 // are counted in 32 bits without a sign.
@@ -57,100 +54,6 @@ __device__ __forceinline__ void load8(const QuantF8Args& a, int64_t row, uint32_
       if (k + i < K) x[i] = F32 ? ((const float*)a.X)[at + i] : bf16_to_f32(((const uint16_t*)a.X)[at + i]);
     }
   }
-}
-
-// Largest magnitude, as the bits of a float: magnitudes order as their bits
-// do, with infinities and NaN above every number.  FINITE: those are passed
-// over.
-constexpr uint32_t kInfBits = 0x7f800000u;
-template <bool FINITE>
-__device__ __forceinline__ uint32_t amax8(const float (&x)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t v = __float_as_uint(x[i]) & 0x7fffffffu;
-    m = max(m, FINITE && v >= kInfBits ? 0u : v);
-  }
-  return m;
-}
-
-// the maximum over the sixteen lanes of a row's block
-__device__ __forceinline__ uint32_t max16(uint32_t m) {
-  // lane ^ 1, ^ 2 within quads, then the mirrored half row and row (every
-  // lane of a quad, of a half row, already agrees)
-  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xf, 0xf, true));    // quad_perm 1,0,3,2
-  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xf, 0xf, true));    // quad_perm 2,3,0,1
-  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xf, 0xf, true));   // row_half_mirror
-  return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xf, 0xf, true));   // row_mirror
-}
-
-// m of a block from the bits of its largest finite magnitude
-__device__ __forceinline__ float block_max(uint32_t bits) { return fmaxf(__uint_as_float(bits), kTiny); }
-
-__device__ __forceinline__ uint32_t convert4(float a, float b, float c, float d) {
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false), true);
-}
-
-// The codes of N elements, of the exact quotients 448 x / m.  v = x * r is off by the
-// rounding of r = 448 / m; the remainder 448 x - v m, taken 2^-9 times (m / 512
-// is exact and stays in range), over m / 512 is what it lacks, and the corrected
-// v is the quotient rounded to fp32.  For bf16 0.875 x is exact too, and a
-// quotient that is no halfway point h is too far from one to be rounded to it
-// (448 x and h m, of 16 bits, differ by a unit at least).  For fp32 (7/8 of 24
-// bits) the error of 0.875 x, exact in turn, is carried along, and a quotient
-// can be nearer to h than fp32 tells: where v may be a halfway point (5 bits, 19
-// zeros behind them) and its remainder is not zero, v moves one step the
-// remainder's way.  INF: an infinite x gives +-448 (asked for only where the
-// block holds one; finite quotients cannot leave the format, |448 x / m| <= 448
-// but for roundings that the conversion takes back).
-template <bool F32, bool INF, int N>
-__device__ __forceinline__ void exact_codes(const float* x, float m, float r, uint32_t* q) {
-  const float m9 = m * 0.001953125f, r9 = r * 1.142857143f;
-  float v[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float v0 = x[i] * r, p = x[i] * 0.875f;
-    if constexpr (F32) {
-      const float e = __builtin_fmaf(x[i], 0.875f, -p);
-      v[i] = __builtin_fmaf(__builtin_fmaf(-v0, m9, p) + e, r9, v0);
-      const uint32_t u = __float_as_uint(v[i]);
-      const float d = __builtin_fmaf(-v[i], m9, p) + e;
-      const uint32_t to = ((__float_as_uint(d) ^ u) >> 31) ? u - 1 : u + 1;
-      if ((u & 0x7ffffu) == 0 && d != 0.0f && (u << 1) != 0) v[i] = __uint_as_float(to);
-    } else {
-      v[i] = __builtin_fmaf(__builtin_fmaf(-v0, m9, p), r9, v0);
-    }
-    if (INF && __builtin_isinf(x[i])) v[i] = __builtin_copysignf(kMax, x[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < N; i += 4) q[i / 4] = convert4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-}
-
-// Eight codes.  fp32: x * r is within 2^-22 of the quotient, and numbers that far below and
-// above it have the same code but for one in 2^17 or so: only it and its
-// neighbours take the exact form.
-template <bool F32, bool INF>
-__device__ __forceinline__ u32x2_t codes8(const float (&x)[8], float m) {
-  const float r = kMax / m;
-  uint32_t q[2];
-  if constexpr (F32 && !INF) {
-    const float below = r * (1.0f - 0x1p-22f), above = r * (1.0f + 0x1p-22f);
-    float lo[8], hi[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo[i] = x[i] * below;
-      hi[i] = x[i] * above;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      q[h] = convert4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
-      if (q[h] != convert4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]))
-        exact_codes<F32, INF, 4>(x + 4 * h, m, r, q + h);
-    }
-  } else {
-    exact_codes<F32, INF, 8>(x, m, r, q);
-  }
-  return u32x2_t{q[0], q[1]};
 }
 
 template <bool VEC>

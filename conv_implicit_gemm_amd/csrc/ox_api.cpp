@@ -1046,7 +1046,24 @@ ox_status ox_quantize_fp8(ox_dtype t, int64_t rows, int64_t K, const void* X, in
 
 namespace {
 
-// The shared half of the three products below: sizes, pointers, alignment.
+// The sizes of the calls that hold a row in registers.
+ox_status check_rows(const char* fn, int64_t rows, int64_t K) {
+  if (rows < 0 || K < 0)
+    return fail(OX_ERR_SHAPE, "%s: rows=%lld or K=%lld is negative", fn, (long long)rows, (long long)K);
+  if (too_big(rows, K)) return fail(OX_ERR_UNSUPPORTED, "%s: a tensor holds 2^31 elements or more", fn);
+  if (rows > 0 && K > kMaxNormRow)
+    return fail(OX_ERR_UNSUPPORTED, "%s: K=%lld, rows hold up to %d elements", fn, (long long)K, kMaxNormRow);
+  return OX_OK;
+}
+
+ox_status norm_result(const char* fn, int64_t rows, int64_t K, int rc) {
+  if (rc == kNoGrid)
+    return fail(OX_ERR_UNSUPPORTED, "%s: %lld rows of %lld are too many blocks for one launch", fn, (long long)rows,
+                (long long)K);
+  return hip_result(fn, rc);
+}
+
+// The shared half of the four products below: sizes, pointers, alignment.
 ox_status expert_call(const char* fn, int dt, ox_dtype y_type, int64_t T, int64_t N, int64_t K, int64_t E,
                       int transB, const void* A, const float* a_scales, const void* B, const float* b_scales,
                       const int32_t* offsets, const void* bias, ox_act act, void* Y, void* stream) {
@@ -1063,7 +1080,7 @@ ox_status expert_call(const char* fn, int dt, ox_dtype y_type, int64_t T, int64_
   if (T == 0 || N == 0) return ok();
   if (!Y) return fail(OX_ERR_INVALID_ARG, "%s: Y is NULL", fn);
   if (K > 0 && (!A || !B)) return fail(OX_ERR_INVALID_ARG, "%s: A or B is NULL", fn);
-  if (dt == DT_F8 && K > 0 && (!a_scales || !b_scales))
+  if ((dt == DT_F8 && K > 0 && (!a_scales || !b_scales)) || (dt == DT_I8 && (!a_scales || !b_scales)))
     return fail(OX_ERR_INVALID_ARG, "%s: a_scales or b_scales is NULL", fn);
   if (!aligned_to(A, esize(dt)) || !aligned_to(B, esize(dt)) || !aligned_to(bias, esize(y_type)) ||
       !aligned_to(Y, esize(y_type)) || !aligned_to(a_scales, 4) || !aligned_to(b_scales, 4) || !aligned_to(offsets, 4))
@@ -1093,6 +1110,7 @@ ox_status expert_call(const char* fn, int dt, ox_dtype y_type, int64_t T, int64_
   a.force = f.variant;
   a.chosen = "";
   const int rc = dt == DT_F8 ? launch_expert_fp8(a, stream)
+                 : dt == DT_I8 ? launch_expert_i8(a, stream)
                  : dt == DT_BF16 ? launch_expert_bf16(a, stream)
                                  : launch_expert_f32(a, stream);
   if (rc == kNoVariant)
@@ -1115,6 +1133,14 @@ ox_status ox_gemm_fp8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const ui
                      stream);
 }
 
+ox_status ox_gemm_i8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const int8_t* A, const float* a_scales,
+                     const int8_t* B, const float* b_scales, const void* bias, ox_act act, void* Y, void* stream) {
+  const char* fn = "ox_gemm_i8";
+  // (K products of up to 2^14 in magnitude stay below 2^31)
+  if (K >= (1 << 17)) return fail(OX_ERR_UNSUPPORTED, "%s: K=%lld, int32 sums hold up to 131071", fn, (long long)K);
+  return expert_call(fn, DT_I8, y_type, M, N, K, 1, 1, A, a_scales, B, b_scales, nullptr, bias, act, Y, stream);
+}
+
 ox_status ox_gemm_grouped(ox_dtype t, int64_t T, int64_t N, int64_t K, int64_t E, int transB,
                           const void* A, const void* B, const int32_t* offsets, const void* bias,
                           ox_act act, void* Y, void* stream) {
@@ -1130,6 +1156,60 @@ ox_status ox_gemm_grouped_fp8(ox_dtype y_type, int64_t T, int64_t N, int64_t K, 
   const char* fn = "ox_gemm_grouped_fp8";
   if (T > 0 && N > 0 && !offsets) return fail(OX_ERR_INVALID_ARG, "%s: offsets is NULL", fn);
   return expert_call(fn, DT_F8, y_type, T, N, K, E, 1, A, a_scales, B, b_scales, offsets, bias, act, Y, stream);
+}
+
+ox_status ox_rmsnorm(ox_dtype t, int64_t rows, int64_t K, const void* X, const void* residual, const void* gamma,
+                     float eps, void* sum_out, ox_dtype y_type, void* Y, float* scales, void* stream) {
+  const char* fn = "ox_rmsnorm";
+  ox_status st = check_float_dt(fn, t);
+  if (st) return st;
+  if (y_type != t && y_type != OX_F8E4M3 && y_type != OX_I8)
+    return fail(OX_ERR_UNSUPPORTED, "%s: y_type %d is not t, OX_F8E4M3 or OX_I8", fn, (int)y_type);
+  if (!(eps > 0.0f) || !isfinite(eps)) return fail(OX_ERR_INVALID_ARG, "%s: eps must be finite and > 0", fn);
+  st = check_rows(fn, rows, K);
+  if (st) return st;
+  if (rows == 0 || K == 0) return ok();
+  const bool codes = y_type != t;
+  if (!X || !Y || (codes && !scales)) return fail(OX_ERR_INVALID_ARG, "%s: X, Y or scales is NULL", fn);
+  if (sum_out && !residual) return fail(OX_ERR_INVALID_ARG, "%s: sum_out without a residual", fn);
+  if (sum_out == Y) return fail(OX_ERR_INVALID_ARG, "%s: sum_out and Y are the same memory", fn);
+  if (!aligned_to(X, esize(t)) || !aligned_to(residual, esize(t)) || !aligned_to(gamma, esize(t)) ||
+      !aligned_to(sum_out, esize(t)) || (!codes && !aligned_to(Y, esize(t))) || (codes && !aligned_to(scales, 4)))
+    return fail(OX_ERR_INVALID_ARG, "%s: a pointer is not aligned to its element size", fn);
+  NormArgs a;
+  a.rows = (int)rows;
+  a.K = (int)K;
+  a.dt = t;
+  a.out_dt = y_type == OX_I8 ? DT_I8 : y_type == OX_F8E4M3 ? DT_F8 : (int)t;
+  a.X = X;
+  a.residual = residual;
+  a.gamma = gamma;
+  a.eps = eps;
+  a.sum_out = sum_out;
+  a.Y = Y;
+  a.scales = codes ? scales : nullptr;
+  return norm_result(fn, rows, K, launch_rmsnorm(a, stream));
+}
+
+ox_status ox_quantize_i8(ox_dtype t, int64_t rows, int64_t K, const void* X, int8_t* Q, float* scales, void* stream) {
+  const char* fn = "ox_quantize_i8";
+  ox_status st = check_float_dt(fn, t);
+  if (st) return st;
+  st = check_rows(fn, rows, K);
+  if (st) return st;
+  if (rows == 0 || K == 0) return ok();
+  if (!X || !Q || !scales) return fail(OX_ERR_INVALID_ARG, "%s: X, Q or scales is NULL", fn);
+  if (!aligned_to(X, esize(t)) || !aligned_to(scales, 4))
+    return fail(OX_ERR_INVALID_ARG, "%s: X or scales is not aligned to its element size", fn);
+  NormArgs a = {};
+  a.rows = (int)rows;
+  a.K = (int)K;
+  a.dt = t;
+  a.out_dt = DT_I8;
+  a.X = X;
+  a.Y = Q;
+  a.scales = scales;
+  return norm_result(fn, rows, K, launch_quantize_i8(a, stream));
 }
 
 size_t ox_dynamic_quantize_workspace_bytes(void) { return dynq_workspace_bytes(); }

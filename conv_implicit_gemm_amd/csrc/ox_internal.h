@@ -283,13 +283,13 @@ int launch_matmul_nbits(const NBitsArgs& a, void* stream);
 struct ExpertArgs {
   int T, N, K, E;          // rows, columns of Y, reduction, experts
   const void* A;           // [T, K]
-  const float* sa;         // e4m3: scales [ceil(K/128)][T]
+  const float* sa;         // e4m3: scales [ceil(K/128)][T]; int8: [T]
   const void* B;           // [E][N, K], or [E][K, N] when kn
-  const float* sb;         // e4m3: scales [E][ceil(N/128)][ceil(K/128)]
+  const float* sb;         // e4m3: scales [E][ceil(N/128)][ceil(K/128)]; int8: [E][N]
   const int32_t* offsets;  // DEVICE [E + 1], or null
   const void* bias;        // [E][N] of Y's type, or null
   void* Y;                 // [T, N]
-  int dt;                  // DT_F32, DT_BF16 or DT_F8
+  int dt;                  // DT_F32, DT_BF16, DT_F8 or DT_I8
   int out_dt;              // DT_F32 or DT_BF16
   int act;
   int kn;                  // weights are [K, N]
@@ -305,6 +305,7 @@ constexpr bool fits_one_launch(int64_t blocks, int threads) { return blocks * th
 int launch_expert_f32(ExpertArgs& a, void* stream);
 int launch_expert_bf16(ExpertArgs& a, void* stream);
 int launch_expert_fp8(ExpertArgs& a, void* stream);
+int launch_expert_i8(ExpertArgs& a, void* stream);
 
 // Quantisation to e4m3 with one fp32 scale per 1 x 128 or 128 x 128 block.
 struct QuantF8Args {
@@ -318,6 +319,25 @@ struct QuantF8Args {
   int vec;                 // rows of X and Q take 16- and 8-byte accesses
 };
 int launch_quantize_fp8(const QuantF8Args& a, void* stream);
+
+// RMS norm of X (+ residual) with results of X's type, e4m3 codes (a scale per
+// 1 x 128 block) or int8 codes (a scale per row), and the int8 quantisation of
+// X's rows (X, Y and scales alone).
+constexpr int kMaxNormRow = 65536;   // a row lies in the registers of 1024 threads
+struct NormArgs {
+  int rows, K;
+  int dt;                  // X, residual, gamma, sum_out: DT_F32 or DT_BF16
+  int out_dt;              // dt, DT_F8 or DT_I8
+  const void* X;           // [rows, K]
+  const void* residual;    // [rows, K] or null
+  const void* gamma;       // [K] or null (ones)
+  float eps;
+  void* sum_out;           // [rows, K] or null
+  void* Y;                 // [rows, K]
+  float* scales;           // [ceil(K/128)][rows] (e4m3) or [rows] (int8)
+};
+int launch_rmsnorm(const NormArgs& a, void* stream);
+int launch_quantize_i8(const NormArgs& a, void* stream);
 
 size_t dynq_workspace_bytes();
 int launch_dynamic_quantize(int64_t n, const float* X, uint8_t* Y, float* y_scale, uint8_t* y_zp,

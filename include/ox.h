@@ -377,7 +377,7 @@ ox_status ox_dynamic_quantize_linear(int64_t n, const float* X, uint8_t* Y, floa
                                      uint8_t* y_zp, void* workspace, size_t workspace_bytes,
                                      void* stream);
 
-/* ------------- 8-bit floating point with block scales, experts' products */
+/* --------- 8-bit operands with scales found at run time, experts' products */
 
 /* Quantise X to e4m3 (ONNX FLOAT8E4M3FN codes: 4 exponent and 3 mantissa
  * bits, largest value 448, no infinity) with one fp32 scale per block of 128
@@ -426,6 +426,52 @@ ox_status ox_quantize_fp8(ox_dtype t, int64_t rows, int64_t K, const void* X, in
 ox_status ox_gemm_fp8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const uint8_t* A,
                       const float* a_scales, const uint8_t* B, const float* b_scales, const void* bias,
                       ox_act act, void* Y, void* stream);
+
+/* Quantise the rows of X to int8 with one fp32 scale per row:
+ *   m = max(|x| over the row's finite values, 2^-100)
+ *   scales[r] = m / 127,  Q = rint(127 * x / m), half to even
+ * of the exact quotient: activations get a scale per token, weights [N, K] one
+ * per output channel.  An infinity gives +-127 and does not move the scale; a
+ * row that holds a NaN gets a scale of NaN (no int8 code can say it, so what is
+ * multiplied by the scale does) and the code 0 in its place.
+ * t: the type of X, OX_F32 or OX_BF16; X: DEVICE [rows, K], K <= 65536 (a row
+ * lies in registers; OX_ERR_UNSUPPORTED above); Q: DEVICE int8 [rows, K];
+ * scales: DEVICE fp32 [rows].  2^26 rows or more, if short, can be too many
+ * blocks for one launch (OX_ERR_UNSUPPORTED). */
+ox_status ox_quantize_i8(ox_dtype t, int64_t rows, int64_t K, const void* X, int8_t* Q, float* scales,
+                         void* stream);
+
+/* Product of int8 matrices with scales found at run time (MatMulInteger with
+ * its dequantisation and epilogue fused):
+ *   Y[m,n] = act( a_scales[m] * b_scales[n] * sum_k A[m,k] * B[n,k] + bias[n] )
+ * A: DEVICE int8 [M, K], a_scales DEVICE fp32 [M]; B: DEVICE int8 [N, K],
+ * b_scales DEVICE fp32 [N] (both as ox_quantize_i8 writes them).  The sums are
+ * int32 and exact: K <= 131071 (OX_ERR_UNSUPPORTED above).  They are turned to
+ * fp32, scaled and biased there and rounded once to y_type (OX_F32 or OX_BF16),
+ * the type of Y DEVICE [M, N] and of bias DEVICE [N] or NULL. */
+ox_status ox_gemm_i8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const int8_t* A, const float* a_scales,
+                     const int8_t* B, const float* b_scales, const void* bias, ox_act act, void* Y, void* stream);
+
+/* RMS norm of rows, with the residual's addition in front and 8-bit results
+ * with scales behind, for the products above:
+ *   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * gamma
+ * in fp32; the norm is that of the fp32 sum.
+ * t: OX_F32 or OX_BF16, the type of X, residual, sum_out DEVICE [rows, K] and
+ * gamma DEVICE [K].  residual NULL: s = x; gamma NULL: ones.  sum_out: s,
+ * rounded once, for the next residual (NULL: not written; needs a residual).
+ * y_type = t: Y DEVICE [rows, K] of t, scales ignored;
+ * y_type = OX_F8E4M3: e4m3 codes and a scale per 1 x 128 block, scales DEVICE
+ *   fp32 [ceil(K/128)][rows], as ox_quantize_fp8 makes them of y;
+ * y_type = OX_I8: int8 codes and a scale per row, scales DEVICE fp32 [rows], as
+ *   ox_quantize_i8 makes them of y.
+ * sum_out may be X or residual (in place), and so may a Y of type t where
+ * sum_out is not; any other overlap of an output is undefined.  The sum of
+ * squares is an fp32 sum: it overflows from |s| = 2^64 / sqrt(K) on, and then
+ * finite s give 0 and infinite ones NaN; a NaN makes the whole row NaN.
+ * K <= 65536; eps > 0. */
+ox_status ox_rmsnorm(ox_dtype t, int64_t rows, int64_t K, const void* X, const void* residual,
+                     const void* gamma, float eps, void* sum_out, ox_dtype y_type, void* Y, float* scales,
+                     void* stream);
 
 /* Products grouped by expert: rows offsets[e] .. offsets[e+1]-1 of A belong
  * to expert e (none, when the two are equal), and
