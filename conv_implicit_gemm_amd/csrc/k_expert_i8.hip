@@ -7,13 +7,13 @@ namespace ox {
 namespace {
 
 // (xN: K divided over N groups of waves)
-constexpr TileCost kTiles[] = {{"32x64", 32, 64, 4, 2.5, 0.30, 0.60},
-                               {"64x64", 64, 64, 3, 2.5, 0.42, 0.57},
-                               {"128x128", 128, 128, 2, 5.3, 0.69, 1.07},
-                               {"256x256", 256, 256, 1, 11.3, 1.68, 1.68},
-                               {"32x32x4", 32, 32, 2, 3.0, 0.19, 0.22},
-                               {"64x64x2", 64, 64, 1, 3.0, 0.285, 0.285},
-                               {"128x128x2", 128, 128, 1, 5.5, 0.60, 0.60}};
+constexpr TileCost kTiles[] = {{"32x64", 32, 64, 4, 2.5, 0.31, 0.53},
+                               {"64x64", 64, 64, 3, 2.5, 0.39, 0.59},
+                               {"128x128", 128, 128, 2, 5.3, 0.71, 0.98},
+                               {"256x256", 256, 256, 1, 11.3, 1.55, 1.55},
+                               {"32x32x4", 32, 32, 2, 3.0, 0.19, 0.19},
+                               {"64x64x2", 64, 64, 1, 3.0, 0.23, 0.23},
+                               {"128x128x2", 128, 128, 1, 5.5, 0.57, 0.57}};
 
 }  // namespace
 

@@ -13,9 +13,13 @@
 // Where that shortcut does not hold (infinities or NaN in the row, magnitudes
 // next to the ends of fp32) the codes are taken of y itself.
 //
-// A row's TPR threads hold eight neighbouring elements C times over; a wave
-// has a row of up to 1024 for itself, longer rows have a block of threads.  What
-// bounds it is the bytes, each read or written once.
+// A row's TPR threads hold eight neighbouring elements C times over; short rows
+// have a wave each, longer ones a block of threads.  What bounds it is the bytes,
+// each read or written once: 8192 rows of 4096 bf16, residual, norm and e4m3
+// codes (236 MB) 45 us, 5.2 TB/s; int8 codes of 8192 rows of 8192 bf16 (201 MB)
+// 38.9 us, 5.2 TB/s, what a large copy reaches.  24 rows are one trip to HBM, a
+// barrier and a store: 3.2 and 2.7 us.  Blocks that stay and load the next row
+// ahead were no faster (47.7 us).
 #include "quant_codes.hpp"
 
 namespace ox {
@@ -27,33 +31,40 @@ enum Out : int { OUT_SAME = 0, OUT_F8 = 1, OUT_I8 = 2 };
 struct __attribute__((packed, aligned(1))) Bytes16 { u32x4_t v; };
 struct __attribute__((packed, aligned(1))) Bytes8 { u32x2_t v; };
 
-// Eight elements at p; `n` of them lie in the row (others: zeros).  Whole pieces
-// take vector accesses from any address; a row's last piece is taken apart.
+// Eight elements of a row as they lie in memory, and as floats.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&x)[8]) {
-  if (n >= 8) {
-    if constexpr (F32) {
-      const float* p = (const float*)base + at;
-      const u32x4_t u = ((const Bytes16*)p)->v, v = ((const Bytes16*)(p + 4))->v;
+struct Raw {
+  u32x4_t v[F32 ? 2 : 1];
+
+  // The piece at column k, or the row's last eight elements where it ends
+  // before k + 8 (K >= 8): no branch, so that a row's loads go out together
+  // (8192 rows of 4096: 50.6 us, 56.6 with a branch around each piece).
+  __device__ __forceinline__ void load(const void* row, int k, int K) {
+    const int64_t at = min(k, K - 8);
+    const char* p = (const char*)row + at * (F32 ? 4 : 2);
+    v[0] = ((const Bytes16*)p)->v;
+    if constexpr (F32) v[1] = ((const Bytes16*)(p + 16))->v;
+  }
+  __device__ __forceinline__ void widen(float (&x)[8]) const {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = __uint_as_float(u[i]);
-        x[i + 4] = __uint_as_float(v[i]);
-      }
-    } else {
-      const u32x4_t u = ((const Bytes16*)((const uint16_t*)base + at))->v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (F32) {
+        x[i] = __uint_as_float(v[0][i]);
+        x[i + 4] = __uint_as_float(v[F32][i]);
+      } else {
+        x[2 * i] = __uint_as_float(v[0][i] << 16);
+        x[2 * i + 1] = __uint_as_float(v[0][i] & 0xffff0000u);
       }
     }
-  } else {
+  }
+};
+// A piece that the row ends inside of, from n of its elements (zeros behind them).
+template <bool F32>
+__device__ __forceinline__ void load_part(const void* row, int k, int n, float (&x)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = 0.0f;
-      if (i < n) x[i] = F32 ? ((const float*)base)[at + i] : bf16_to_f32(((const uint16_t*)base)[at + i]);
-    }
+  for (int i = 0; i < 8; ++i) {
+    x[i] = 0.0f;
+    if (i < n) x[i] = F32 ? ((const float*)row)[k + i] : bf16_to_f32(((const uint16_t*)row)[k + i]);
   }
 }
 
@@ -88,16 +99,27 @@ __device__ __forceinline__ void store_codes(uint8_t* y, int n, u32x2_t q) {
   }
 }
 
-// over the 64 lanes of a wave, in every lane
+// over the 64 lanes of a wave, in every lane: within rows of sixteen lanes by
+// DPP, then the rows' values by scalar reads
 __device__ __forceinline__ uint32_t wave_max(uint32_t m) {
   m = max16(m);
-  m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-  return max(m, (uint32_t)__shfl_xor((int)m, 32));
+  const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)m, 0), (uint32_t)__builtin_amdgcn_readlane((int)m, 16));
+  const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)m, 32), (uint32_t)__builtin_amdgcn_readlane((int)m, 48));
+  return max(a, b);
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
 }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-  return v;
+  v += dpp<0xB1>(v);    // quad_perm 1,0,3,2
+  v += dpp<0x4E>(v);    // quad_perm 2,3,0,1
+  v += dpp<0x141>(v);   // row_half_mirror
+  v += dpp<0x140>(v);   // row_mirror
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
 
 // The largest `m` and the sum of `v` over a row's threads (the waves' parts are
@@ -123,7 +145,7 @@ __device__ __forceinline__ void row_reduce(float& v, uint32_t& m, float* sums, u
   }
 }
 
-constexpr int row_threads(int TPR) { return TPR > kThreads ? TPR : kThreads; }
+constexpr int row_threads(int TPR) { return TPR > 64 ? TPR : kThreads; }      // threads of a block
 
 template <bool F32, int OUT, bool NORM, int TPR, int C>
 __global__ __launch_bounds__(row_threads(TPR)) void row_kernel(const NormArgs a) {
@@ -131,28 +153,52 @@ __global__ __launch_bounds__(row_threads(TPR)) void row_kernel(const NormArgs a)
   __shared__ float sums[2][TPR / 64];
   __shared__ uint32_t tops[2][TPR / 64];
   const int t = threadIdx.x % TPR;
-  // (blocks of an XCD take neighbouring rows: their scales share lines of its L2)
-  const uint32_t row = (uint32_t)xcd_tile(blockIdx.x, gridDim.x) * RPB + threadIdx.x / TPR;
+  static_assert(TPR == 64 || RPB == 1, "a barrier is for one row");
+  // (rows in the order of the blocks: a range of rows for each XCD, powers of two
+  // apart, measured 5 to 15% slower)
+  const uint32_t row = blockIdx.x * RPB + threadIdx.x / TPR;
   if (row >= (uint32_t)a.rows) return;             // (whole waves; rows of a block share no barrier)
   const int64_t at = (int64_t)row * a.K;
+  const int64_t size = F32 ? 4 : 2;
+  const char* xr = (const char*)a.X + at * size;
+  const char* rr = (const char*)a.residual + at * size;
+  const bool whole = a.K >= 8;                     // (else the row is part of one piece)
   float z[C][8];
-  int n[C];
+  int n[C];                                        // elements of the row from this piece's first on
+  Raw<F32> x[C], r[NORM ? C : 1], g[NORM ? C : 1];
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int k = (c * TPR + t) * 8;
-    n[c] = a.K - k;
-    load8<F32>(a.X, at + k, n[c], z[c]);
+  for (int c = 0; c < C; ++c) n[c] = a.K - (c * TPR + t) * 8;
+  if (whole) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) x[c].load(xr, (c * TPR + t) * 8, a.K);
+    if constexpr (NORM) {
+      if (a.residual) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) r[c].load(rr, (c * TPR + t) * 8, a.K);
+      }
+      if (a.gamma) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) g[c].load(a.gamma, (c * TPR + t) * 8, a.K);
+      }
+    }
   }
+  // a piece's eight floats: zeros past the row's end
+  auto floats = [&](const Raw<F32>& raw, const void* from, int c, float (&v)[8]) {
+    if (n[c] >= 8) raw.widen(v);
+    else load_part<F32>(from, (c * TPR + t) * 8, n[c], v);
+  };
+#pragma unroll
+  for (int c = 0; c < C; ++c) floats(x[c], xr, c, z[c]);
   float ss = 0.0f;
   if constexpr (NORM) {
+    float v[8];
     if (a.residual) {
-      float r[C][8];
 #pragma unroll
-      for (int c = 0; c < C; ++c) load8<F32>(a.residual, at + (c * TPR + t) * 8, n[c], r[c]);
+      for (int c = 0; c < C; ++c) {
+        floats(r[c], rr, c, v);
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[c][i] += r[c][i];
+        for (int i = 0; i < 8; ++i) z[c][i] += v[i];
+      }
     }
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -163,12 +209,11 @@ __global__ __launch_bounds__(row_threads(TPR)) void row_kernel(const NormArgs a)
       for (int c = 0; c < C; ++c) store8<F32>(a.sum_out, at + (c * TPR + t) * 8, n[c], z[c]);
     }
     if (a.gamma) {
-      float g[8];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        load8<F32>(a.gamma, (c * TPR + t) * 8, n[c], g);
+        floats(g[c], a.gamma, c, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[c][i] *= g[i];
+        for (int i = 0; i < 8; ++i) z[c][i] *= v[i];
       }
     }
   }
@@ -203,10 +248,8 @@ __global__ __launch_bounds__(row_threads(TPR)) void row_kernel(const NormArgs a)
         any = max(any, amax8<false>(z[c]));
         fin = max(fin, amax8<true>(z[c]));
       }
-      float all = __uint_as_float(0);
-      uint32_t both = fin;
-      row_reduce<TPR>(all, both, sums[1], tops[1]);
-      fin = both;
+      float none = 0.0f;
+      row_reduce<TPR>(none, fin, sums[1], tops[1]);
       // a NaN in the row: its scale is NaN too, as no int8 code can say it
       if constexpr (TPR > 64) any = (uint32_t)__syncthreads_or(any > kInfBits);
       else any = __any(any > kInfBits) ? 1u : 0u;
@@ -215,7 +258,7 @@ __global__ __launch_bounds__(row_threads(TPR)) void row_kernel(const NormArgs a)
     if (t == 0) a.scales[row] = any ? __uint_as_float(0x7fc00000u) : (plain ? m * rs : m) / 127.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const u32x2_t q = plain ? codes8_i8<false>(z[c], m) : codes8_i8<true>(z[c], m);
+      const u32x2_t q = plain ? codes8_i8<!NORM && F32, false>(z[c], m) : codes8_i8<true, true>(z[c], m);
       store_codes((uint8_t*)a.Y + at + (c * TPR + t) * 8, n[c], q);
     }
   } else {
@@ -228,7 +271,7 @@ __global__ __launch_bounds__(row_threads(TPR)) void row_kernel(const NormArgs a)
       float m = zm, scale = zm * rs / kMax;
       u32x2_t q;
       if (plain) {
-        q = codes8<true, false>(z[c], m);
+        q = codes8_of_result(z[c], m);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[c][i] *= rs;
@@ -254,10 +297,17 @@ int launch(const NormArgs& a, hipStream_t s) {
 
 template <bool F32, int OUT, bool NORM>
 int pick(const NormArgs& a, hipStream_t s) {
+  // One or two pieces a thread: one barrier for few loads, and still enough in
+  // flight.  e4m3 codes, whose scales are found sixteen lanes at a time, take one
+  // (24 rows of 4096: 3.2 us, 3.5 with two; 8192 rows 45.0 and 45.4), a scale per
+  // row and results of X's type two (int8 norm of 8192 rows of 4096: 43.4 us, 49
+  // with one, 53 with a wave's eight; quantisation of 8192 rows of 8192: 38.9, 54
+  // with one).
+  constexpr bool ONE = OUT == OUT_F8;
   if (a.K <= 512) return launch<F32, OUT, NORM, 64, 1>(a, s);
-  if (a.K <= 1024) return launch<F32, OUT, NORM, 64, 2>(a, s);
-  if (a.K <= 2048) return launch<F32, OUT, NORM, 256, 1>(a, s);
-  if (a.K <= 4096) return launch<F32, OUT, NORM, 256, 2>(a, s);
+  if (a.K <= 1024) return launch<F32, OUT, NORM, ONE ? 128 : 64, ONE ? 1 : 2>(a, s);
+  if (a.K <= 2048) return launch<F32, OUT, NORM, ONE ? 256 : 128, ONE ? 1 : 2>(a, s);
+  if (a.K <= 4096) return launch<F32, OUT, NORM, ONE ? 512 : 256, ONE ? 1 : 2>(a, s);
   if (a.K <= 8192) return launch<F32, OUT, NORM, 512, 2>(a, s);
   if (a.K <= 16384) return launch<F32, OUT, NORM, 1024, 2>(a, s);
   if (a.K <= 32768) return launch<F32, OUT, NORM, 1024, 4>(a, s);
