@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libox.so")
 
 OX_OK, OX_ERR_INVALID_ARG, OX_ERR_SHAPE, OX_ERR_UNSUPPORTED, OX_ERR_HIP = 0, 1, 2, 3, 4
 OX_F32, OX_BF16, OX_I8, OX_I32, OX_F8E4M3 = 0, 1, 2, 3, 4
-ACT = {"none": 0, "relu": 1, "relu6": 2, "gelu": 3}
+ACT = {"none": 0, "relu": 1, "relu6": 2, "gelu": 3, "silu": 4}     # silu: ox_moe_few alone
 STATUS_NAMES = {0: "OX_OK", 1: "OX_ERR_INVALID_ARG", 2: "OX_ERR_SHAPE",
                 3: "OX_ERR_UNSUPPORTED", 4: "OX_ERR_HIP"}
 
@@ -31,7 +31,8 @@ EXPORTS = ("ox_matmul_batched", "ox_gemm_fused", "ox_conv2d_fused", "ox_conv2d_i
            "ox_int8_prepare_ex", "ox_dynamic_quantize_workspace_bytes", "ox_dynamic_quantize_linear",
            "ox_matmul_nbits", "ox_gemm_workspace_bytes", "ox_gemm_fused_ws",
            "ox_static_scratch_bytes", "ox_conv2d_fused_static", "ox_quantize_fp8", "ox_gemm_fp8",
-           "ox_gemm_grouped", "ox_gemm_grouped_fp8", "ox_quantize_i8", "ox_gemm_i8", "ox_rmsnorm")
+           "ox_gemm_grouped", "ox_gemm_grouped_fp8", "ox_quantize_i8", "ox_gemm_i8", "ox_rmsnorm",
+           "ox_moe_few_workspace_bytes", "ox_moe_few")
 
 
 class OxError(RuntimeError):
@@ -89,6 +90,8 @@ def _load():
         "ox_quantize_i8": (I, [I, I64, I64, P, P, P, P]),
         "ox_gemm_i8": (I, [I, I64, I64, I64, P, P, P, P, P, I, P, P]),
         "ox_rmsnorm": (I, [I, I64, I64, P, P, P, F, P, I, P, P, P]),
+        "ox_moe_few_workspace_bytes": (C.c_size_t, [I64] * 5),
+        "ox_moe_few": (I, [I, I] + [I64] * 5 + [P, I, P, I, P, P, P, I, I, P, P, P, P, P, P, P, C.c_size_t, P]),
         "ox_last_error": (C.c_char_p, []),
         "ox_version": (C.c_char_p, []),
     }
@@ -655,6 +658,82 @@ def ox_rmsnorm(X, gamma=None, residual=None, eps=1e-6, out="same", Y=None, scale
     if st:
         _check(st)
     return Y, scales, S
+
+
+def ox_moe_few_workspace_bytes(T, D, H, E, top):
+    return int(lib.ox_moe_few_workspace_bytes(T, D, H, E, top))
+
+
+def ox_moe_few(X, scores, W1, W2, top, w1_scales=None, w2_scales=None, b1=None, b2=None, act="silu", gated=True,
+               renormalise=True, Y=None, experts=None, weights=None, workspace=None, stream=None):
+    """A feed-forward layer of routed experts for up to 64 tokens: Y [T, D] of X
+    [T, D] (float32 or bfloat16) and the router's scores [T, E] (float32 or
+    bfloat16); each token's `top` best experts, with softmax weights over them
+    (renormalise) or over all.  W1 [E, 2H, D] (gated: gate rows, then up rows) or
+    [E, H, D], W2 [E, D, H], of X's type, or float8_e4m3fn (uint8 codes) with
+    scales per 128 x 128 beside bfloat16 X; b1, b2 of X's type.  experts (int32)
+    and weights (float32) [T, top] are filled if given.  workspace: any dense
+    device tensor of ox_moe_few_workspace_bytes bytes (made if None)."""
+    f8, u8, f32, i32, raw = _F8 or _types()
+    bf16 = (_I8 or _small_types())[1]
+    T, D = X.shape
+    E, wide, D1 = W1.shape
+    H = wide >> 1 if gated else wide
+    dtype = X.dtype
+    code = _dtype_code(X)
+    if D1 != D or (gated and wide & 1) or W2.shape != (E, D, H):
+        raise ValueError("W1 is %s and W2 %s, X %s" % (tuple(W1.shape), tuple(W2.shape), (T, D)))
+    if scores.shape != (T, E):
+        raise _shape_error("scores", scores, (T, E))
+    if scores.dtype != f32 and scores.dtype != bf16:
+        raise TypeError("scores must be float32 or bfloat16")
+    if W1.dtype != W2.dtype:
+        raise TypeError("W1 is %s, W2 %s" % (W1.dtype, W2.dtype))
+    if W1.dtype == dtype:
+        w_code = code
+        if w1_scales is not None or w2_scales is not None:
+            raise ValueError("scales go with float8_e4m3fn weights")
+    elif (W1.dtype == f8 or W1.dtype == u8) and dtype == bf16:
+        w_code = OX_F8E4M3
+        for name, t, want in (("w1_scales", w1_scales, (E, (wide + 127) >> 7, (D + 127) >> 7)),
+                              ("w2_scales", w2_scales, (E, (D + 127) >> 7, (H + 127) >> 7))):
+            if t is None:
+                raise ValueError("%s is needed with float8_e4m3fn weights" % name)
+            if t.shape != want:
+                raise _shape_error(name, t, want)
+            if t.dtype != f32:
+                raise TypeError("%s must be float32" % name)
+    else:
+        raise TypeError("W1 and W2 are %s, X %s" % (W1.dtype, dtype))
+    if Y is None:
+        Y = _new_result((T, D), dtype, X.device)
+    elif Y.shape != (T, D):
+        raise _shape_error("Y", Y, (T, D))
+    elif Y.dtype != dtype:
+        raise TypeError("Y is %s, X %s" % (Y.dtype, dtype))
+    if b1 is not None and (b1.shape != (E, wide) or b1.dtype != dtype):
+        raise _shape_error("b1", b1, (E, wide)) if b1.shape != (E, wide) else TypeError("b1 is %s, X %s" % (b1.dtype, dtype))
+    if b2 is not None and (b2.shape != (E, D) or b2.dtype != dtype):
+        raise _shape_error("b2", b2, (E, D)) if b2.shape != (E, D) else TypeError("b2 is %s, X %s" % (b2.dtype, dtype))
+    if experts is not None and (experts.shape != (T, top) or experts.dtype != i32):
+        raise ValueError("experts must be int32 %s" % ((T, top),))
+    if weights is not None and (weights.shape != (T, top) or weights.dtype != f32):
+        raise ValueError("weights must be float32 %s" % ((T, top),))
+    if workspace is None:
+        workspace = _new_result((lib.ox_moe_few_workspace_bytes(T, D, H, E, top),), u8, X.device)
+    dev = X.get_device()
+    for t in (X, scores, W1, W2, Y, w1_scales, w2_scales, b1, b2, experts, weights, workspace):
+        if t is not None and (dev < 0 or t.get_device() != dev or not t.is_contiguous()):
+            raise _refuse_memory(("X", "scores", "W1", "W2", "Y", "w1_scales", "w2_scales", "b1", "b2", "experts", "weights",
+                                  "workspace"), X, scores, W1, W2, Y, w1_scales, w2_scales, b1, b2, experts, weights, workspace)
+    st = lib.ox_moe_few(code, w_code, T, D, H, E, top, X.data_ptr(), OX_F32 if scores.dtype == f32 else OX_BF16,
+                        scores.data_ptr(), 1 if renormalise else 0, W1.data_ptr(), _ptr(w1_scales), _ptr(b1), ACT[act],
+                        1 if gated else 0, W2.data_ptr(), _ptr(w2_scales), _ptr(b2), _ptr(experts), _ptr(weights),
+                        Y.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                        raw(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
+    return Y
 
 
 def ox_dynamic_quantize_linear(X, Y=None, y_scale=None, y_zp=None, workspace=None, stream=None):

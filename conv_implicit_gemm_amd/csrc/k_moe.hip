@@ -1,0 +1,664 @@
+// k_moe.hip -- a routed feed-forward layer for up to 64 tokens, in two kernels.
+//
+//   up:    router scores -> each token's best experts and their weights;
+//          h = act(W1[e] x + b1[e]), or act(gate) * up where W1 holds both
+//   down:  Y = sum over a token's experts of weight * (W2[e] h + b2[e])
+//
+// With so few tokens the chosen experts' weights are what there is to move: they
+// are read once, straight into registers, as the matrix instructions take them
+// (16 rows of weights x 16 tokens).  A wave takes two fragments of 16 rows and a
+// range of K, so that a fragment of the tokens serves both, and the waves' sums
+// are added in their order: every sum's order depends on the sizes and on the
+// routing alone.
+//
+// Every block of the first kernel routes all tokens for itself (a launch and a
+// trip to memory less than a kernel of its own); its first block leaves the
+// result for the second kernel, the slots (token, expert) ordered by expert.
+// The second kernel's K is the experts' hidden rows one after the other; it is
+// cut into equal ranges whatever the routing.  Blocks that share columns leave
+// fp32 sums, and the last of them to arrive adds them in order.
+//
+// Precision.  bf16 weights (and e4m3 ones, widened: exact) meet bf16 tokens in
+// the bf16 instruction, whose sums are fp32; h is kept as two bf16 numbers (16
+// bits of significand, off by 2^-17 at most), each of which meets W2, so that the only
+// rounding that counts is Y's.  Every batch of K starts a chain of sums from zero.
+#include "expert_gemm.hpp"
+
+namespace ox {
+
+namespace {
+
+constexpr int kMoeThreads = 512, kMoeWaves = kMoeThreads / 64;
+constexpr int kPairs = kMoeTokens * kMoeTop;
+
+__device__ __forceinline__ f32x4_t add4(f32x4_t a, f32x4_t b) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) a[r] += b[r];
+  return a;
+}
+
+__device__ __forceinline__ float moe_act(int act, float v) {
+  return act == ACT_SILU ? v / (1.0f + expf(-v)) : apply_act(act, v);
+}
+
+// ------------------------------------------------------------- routing --
+
+// What the routing finds, in a block's shared memory.
+struct Route {
+  uint64_t mask[kMoeExperts];       // the tokens of each expert
+  uint16_t first[kMoeExperts];      // an expert's first slot
+  uint16_t act[kMoeExperts];        // the experts that have tokens, in order
+  uint16_t off[kMoeExperts + 1];    // their slots
+  int16_t choice[kMoeTokens][kMoeTop];
+  float weight[kMoeTokens][kMoeTop];
+  uint8_t tok[kPairs];              // the token of each slot
+  int nact, slots;
+};
+
+// The same for the second kernel, in the workspace.
+struct RouteOut {
+  int nact, slots;
+  int act[kMoeExperts], off[kMoeExperts + 1];
+  int tok[kPairs];
+  float weight[kPairs];
+};
+
+// Scores as whole numbers in their order; 0 for what is never chosen (NaN, -inf)
+__device__ __forceinline__ uint32_t score_key(float s) {
+  if (!(s > -INFINITY)) return 0u;
+  const uint32_t u = __float_as_uint(s == 0.0f ? 0.0f : fminf(s, 3.4028234663852886e38f));      // (-0 and 0 are a tie)
+  return (u >> 31) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_score(uint32_t k) {
+  return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
+}
+
+__device__ __forceinline__ uint32_t row16_max(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xf, 0xf, true));
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xf, 0xf, true));
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xf, 0xf, true));
+  return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xf, 0xf, true));
+}
+__device__ __forceinline__ uint32_t all_max(uint32_t m) {
+  m = row16_max(m);
+  const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)m, 0), (uint32_t)__builtin_amdgcn_readlane((int)m, 16));
+  const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)m, 32), (uint32_t)__builtin_amdgcn_readlane((int)m, 48));
+  return max(a, b);
+}
+__device__ __forceinline__ float all_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+  return v;
+}
+
+// B tokens of a wave at a time (their loads together), PL scores of each a lane.
+template <int PL, int B>
+__device__ __forceinline__ void route_tokens(const MoeArgs& a, Route& rt, bool weights) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int t0 = wave; t0 < a.T; t0 += kMoeWaves * B) {
+    uint32_t key[B][PL];
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int i = 0; i < PL; ++i) {
+        const int t = min(t0 + b * kMoeWaves, a.T - 1), e = i * 64 + lane;
+        const int64_t at = (int64_t)t * a.E + min(e, a.E - 1);
+        const float s = a.scores_dt == DT_F32 ? ((const float*)a.scores)[at] : bf16_to_f32(((const uint16_t*)a.scores)[at]);
+        key[b][i] = e < a.E ? score_key(s) : 0u;
+      }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int t = t0 + b * kMoeWaves;
+      if (t >= a.T) break;
+      float all = 0.0f, top = 0.0f;
+      uint32_t mine = 0u;
+      int expert = -1;
+      for (int j = 0; j < a.top; ++j) {
+        uint32_t m = key[b][0];
+#pragma unroll
+        for (int i = 1; i < PL; ++i) m = max(m, key[b][i]);
+        m = all_max(m);
+        if (m == 0u) break;
+        // the lowest of the experts that have it
+        int e = -1;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+          const uint64_t has = __ballot(key[b][i] == m);
+          if (e < 0 && has) e = i * 64 + __ffsll((unsigned long long)has) - 1;
+        }
+        if (j == 0) {
+          top = key_score(m);
+          if (weights && !a.renormalise) {
+#pragma unroll
+            for (int i = 0; i < PL; ++i) all += key[b][i] ? expf(key_score(key[b][i]) - top) : 0.0f;
+            all = all_sum(all);
+          }
+        }
+        if (lane == j) {
+          mine = m;
+          expert = e;
+        }
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+          if (i * 64 + lane == e) key[b][i] = 0u;
+      }
+      if (lane < a.top) {
+        rt.choice[t][lane] = (int16_t)expert;
+        if (expert >= 0) atomicOr((unsigned long long*)&rt.mask[expert], 1ull << t);
+      }
+      if (weights) {
+        const float p = mine ? expf(key_score(mine) - top) : 0.0f;
+        if (a.renormalise) all = all_sum(p);
+        if (lane < a.top) rt.weight[t][lane] = mine ? p / all : 0.0f;
+      }
+    }
+  }
+}
+
+// Fills rt; with `out`, the block also writes what the second kernel and the
+// caller read, and clears the counters.
+__device__ __forceinline__ void route(const MoeArgs& a, Route& rt, bool out) {
+  for (int e = threadIdx.x; e < a.E; e += kMoeThreads) rt.mask[e] = 0;
+  __syncthreads();
+  if (a.E <= 64) route_tokens<1, 8>(a, rt, out);
+  else if (a.E <= 128) route_tokens<2, 4>(a, rt, out);
+  else if (a.E <= 256) route_tokens<4, 2>(a, rt, out);
+  else route_tokens<8, 1>(a, rt, out);
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int acts = 0, slots = 0;
+    for (int base = 0; base < a.E; base += 64) {
+      const int e = base + lane;
+      const int n = e < a.E ? __popcll(rt.mask[e]) : 0;
+      const int s = wave_scan(n), k = wave_scan(n ? 1 : 0);
+      if (e < a.E) rt.first[e] = (uint16_t)(slots + s - n);
+      if (n) {
+        rt.act[acts + k - 1] = (uint16_t)e;
+        rt.off[acts + k - 1] = (uint16_t)(slots + s - n);
+      }
+      slots += __builtin_amdgcn_readlane(s, 63);
+      acts += __builtin_amdgcn_readlane(k, 63);
+    }
+    if (lane == 0) {
+      rt.off[acts] = (uint16_t)slots;
+      rt.nact = acts;
+      rt.slots = slots;
+    }
+  }
+  __syncthreads();
+  RouteOut* ro = (RouteOut*)a.route;
+  for (int p = threadIdx.x; p < a.T * a.top; p += kMoeThreads) {
+    const int t = p / a.top, j = p - t * a.top, e = rt.choice[t][j];
+    if (e >= 0) {
+      const int slot = rt.first[e] + __popcll(rt.mask[e] & ((1ull << t) - 1));
+      rt.tok[slot] = (uint8_t)t;
+      if (out) {
+        ro->tok[slot] = t;
+        ro->weight[slot] = rt.weight[t][j];
+      }
+    }
+    if (out && a.experts) a.experts[p] = e;
+    if (out && a.weights) a.weights[p] = rt.weight[t][j];
+  }
+  if (out) {
+    for (int i = threadIdx.x; i <= rt.nact; i += kMoeThreads) {
+      if (i < rt.nact) ro->act[i] = rt.act[i];
+      ro->off[i] = rt.off[i];
+    }
+    if (threadIdx.x == 0) {
+      ro->nact = rt.nact;
+      ro->slots = rt.slots;
+    }
+    for (int i = threadIdx.x; i < a.tiles; i += kMoeThreads) a.counters[i] = 0;
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------ products --
+
+// bytes [0, n) of 16 at p, whole elements of ESZ bytes; zeros behind them (n <= 0:
+// none)
+template <int ESZ>
+__device__ __forceinline__ u32x4_t part_of_piece(const char* p, int n) {
+  if (n >= 16) return ((const Bytes16*)p)->v;
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 16; i += ESZ)
+    if (i < n) {
+      if constexpr (ESZ == 4) w[i / 4] = *(const uint32_t*)(p + i);
+      else if constexpr (ESZ == 2) w[i / 4] |= (uint32_t)*(const uint16_t*)(p + i) << (8 * (i % 4));
+      else w[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
+    }
+  return u32x4_t{w[0], w[1], w[2], w[3]};
+}
+
+// Two fragments of 16 rows of weights times MF fragments of 16 tokens, over steps
+// [k0, k1) of K (128 bytes of a weight row each).  The tokens' rows come in HL
+// parts that are added (the hidden rows: 2).
+template <int FMT, int MF, int HL>
+struct MoeProduct {
+  typedef FmtOps<FMT> Mm;
+  typedef typename Mm::Frag Frag;
+  static constexpr bool F8 = FMT == FMT_FP8X;
+  static constexpr int KE = 128 / Mm::ESZ;         // K of a step
+  static constexpr int XP = F8 ? 4 : 2;            // pieces of a token's step
+  static constexpr int XB = F8 ? 256 : 128;        // its bytes
+  // Steps in flight: with 16 waves on a CU, 16 KB of weights a wave would do;
+  // the tokens' pieces share the registers.
+  static constexpr int U = MF * HL * XP >= 16 ? 1 : 2;
+
+  const char* w[2];            // this lane's rows of weights
+  const char* x[MF][HL];       // this lane's tokens
+  int frags;                   // token fragments that hold tokens
+  const float* sw[2];          // e4m3: the rows' scales (step 0) ...
+  int sw_rows[2][4];           // ... and where a lane's four rows have theirs
+  bool sw_one;                 // all rows of a fragment share one
+  int K;
+
+  static __device__ __forceinline__ int x_at(int i) {
+    const int g = (threadIdx.x & 63) >> 4;
+    return F8 ? g * 32 + (i & 1) * 16 + (i >> 1) * 128 : g * 16 + i * 64;
+  }
+
+  struct Step {
+    u32x4_t w[2][2], x[MF][HL][XP];
+    float s[2][4];
+  };
+  // PART: K may end inside the step
+  template <bool PART>
+  __device__ __forceinline__ void load(int k, Step& st) const {
+    const int g = (threadIdx.x & 63) >> 4;
+    const int left = (int)min((int64_t)XB, ((int64_t)K - (int64_t)k * KE) * Mm::ESZ);      // bytes of a weight row
+    const int64_t wk = (int64_t)k * 128, xk = (int64_t)k * XB;
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int o = g * 16 + i * 64;
+        st.w[f][i] = PART ? part_of_piece<Mm::ESZ>(w[f] + wk + o, left - o) : ((const Bytes16*)(w[f] + wk + o))->v;
+      }
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      if (m > 0 && m >= frags) break;
+#pragma unroll
+      for (int h = 0; h < HL; ++h)
+#pragma unroll
+        for (int i = 0; i < XP; ++i) {
+          const int o = x_at(i);
+          st.x[m][h][i] = PART ? part_of_piece<F8 ? 2 : Mm::ESZ>(x[m][h] + xk + o, left * (XB / 128) - o)
+                               : ((const Bytes16*)(x[m][h] + xk + o))->v;
+        }
+    }
+    if constexpr (F8) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        st.s[f][0] = sw[f][sw_rows[f][0] + k];
+#pragma unroll
+        for (int r = 1; r < 4; ++r) st.s[f][r] = sw_one ? st.s[f][0] : sw[f][sw_rows[f][r] + k];
+      }
+    }
+  }
+  static __device__ __forceinline__ Frag token_frag(const u32x4_t (&p)[XP]) {
+    Frag f;
+#pragma unroll
+    for (int i = 0; i < XP; ++i) f.v[i] = p[i];
+    return f;
+  }
+  template <int N>
+  __device__ __forceinline__ void multiply(const Step (&st)[N], f32x4_t (&acc)[2][MF]) const {
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      if (m > 0 && m >= frags) break;
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        f32x4_t chain = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          const Frag b = Mm::widen(st[u].w[f][0], st[u].w[f][1]);
+          if constexpr (F8) chain = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < HL; ++h) {
+            const Frag t = token_frag(st[u].x[m][h]);
+            chain = Mm::template half<0>(b, t, chain);
+            chain = Mm::template half<1>(b, t, chain);
+            if constexpr (F8) {
+              chain = Mm::template half<2>(b, t, chain);
+              chain = Mm::template half<3>(b, t, chain);
+            }
+          }
+          if constexpr (F8) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[f][m][r] = __builtin_fmaf(st[u].s[f][r], chain[r], acc[f][m][r]);
+          }
+        }
+        if constexpr (!F8) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[f][m][r] += chain[r];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void run(int k0, int k1, f32x4_t (&acc)[2][MF]) const {
+    if (K == 0) return;
+    int k = k0;
+#pragma unroll 1
+    for (; k + U <= k1 && (int64_t)(k + U) * KE <= K; k += U) {
+      Step st[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) load<false>(k + u, st[u]);
+      __builtin_amdgcn_sched_barrier(0);      // every load goes out before the first product
+      multiply(st, acc);
+    }
+#pragma unroll 1
+    for (; k < k1; ++k) {
+      Step st[1];
+      load<true>(k, st[0]);
+      multiply(st, acc);
+    }
+  }
+  // fragment f: rows n .. n + 15 of expert e's `rows` rows, of which those below
+  // `end` count
+  __device__ __forceinline__ void weights(int f, const void* W, const float* scales, int e, int rows, int n, int end) {
+    const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    w[f] = (const char*)W + ((int64_t)e * rows + min(n + i, end - 1)) * K * Mm::ESZ;
+    if constexpr (F8) {
+      const int nb = ceil_div(rows, 128), kb = ceil_div(K, 128);
+      sw[f] = scales + (int64_t)e * nb * kb;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sw_rows[f][r] = min(n + g * 4 + r, end - 1) / 128 * kb;
+    }
+  }
+};
+
+// Four consecutive hidden values of a slot, as the second kernel reads them.
+template <int FMT>
+__device__ __forceinline__ void store_hidden(const MoeArgs& a, int slot, int n, const float (&h)[4]) {
+  if constexpr (FMT == FMT_F32) {
+    *(f32x4_t*)((float*)a.hidden + (int64_t)slot * a.ldh + n) = f32x4_t{h[0], h[1], h[2], h[3]};
+  } else {
+    float hi[4], lo[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      hi[r] = bf16_to_f32((uint16_t)pack_bf16x2(h[r], 0.0f));
+      lo[r] = __builtin_isfinite(hi[r]) ? h[r] - hi[r] : 0.0f;
+    }
+    uint16_t* p = (uint16_t*)a.hidden + (int64_t)slot * a.ldh + n;
+    *(u32x2_t*)p = u32x2_t{pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
+    *(u32x2_t*)(p + (int64_t)a.T * a.top * a.ldh) = u32x2_t{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3])};
+  }
+}
+template <int FMT>
+__device__ __forceinline__ float value_at(const void* p, int64_t at) {
+  return FMT == FMT_F32 ? ((const float*)p)[at] : bf16_to_f32(((const uint16_t*)p)[at]);
+}
+
+// Units of one expert x a group of column tiles, in turn over the grid's blocks.
+// A column tile is 16 gate rows and the 16 up rows beside them, or 32 rows.
+template <int FMT, int MF>
+__global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(const MoeArgs a) {
+  typedef MoeProduct<FMT, MF, 1> MP;
+  __shared__ Route rt;
+  __shared__ f32x4_t part[2][kMoeWaves][2 * MF][64];
+  route(a, rt, blockIdx.x == 0);
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wide = a.gated ? 2 * a.H : a.H, per = a.gated ? 16 : 32, tiles = ceil_div(a.H, per);
+  const int nk = ceil_div(a.D, MP::KE);
+  const int SPL = a.slices, CT = kMoeWaves / SPL, groups = ceil_div(tiles, CT);
+  const int ct = wave / SPL, sl = wave - ct * SPL;
+  const int k0 = (int)((int64_t)nk * sl / SPL), k1 = (int)((int64_t)nk * (sl + 1) / SPL);
+  int turn = 0;
+  for (int unit = blockIdx.x; unit < rt.nact * groups; unit += gridDim.x) {
+    const int ai = unit / groups, tile = (unit - ai * groups) * CT + ct, n0 = tile * per;
+    const int e = rt.act[ai], lo = rt.off[ai], hi = rt.off[ai + 1];
+    const bool live = tile < tiles;      // whole waves; the barriers below are passed by all
+    MP mp;
+    mp.K = a.D;
+    if (live) {
+      mp.weights(0, a.W1, a.s1, e, wide, n0, a.H);
+      if (a.gated) mp.weights(1, a.W1, a.s1, e, wide, a.H + n0, wide);
+      else mp.weights(1, a.W1, a.s1, e, wide, min(n0 + 16, a.H - 1), a.H);
+      mp.sw_one = a.gated ? a.H % 16 == 0 : true;
+    }
+    for (int s0 = lo; s0 < hi; s0 += 16 * MF, turn ^= 1) {
+      f32x4_t acc[2][MF];
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int m = 0; m < MF; ++m) acc[f][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (live) {
+        mp.frags = ceil_div(hi - s0, 16);
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+          mp.x[m][0] = (const char*)a.X + (int64_t)rt.tok[min(s0 + m * 16 + i, hi - 1)] * a.D * (FMT == FMT_F32 ? 4 : 2);
+        mp.run(k0, k1, acc);
+      }
+      if (SPL > 1) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+          for (int m = 0; m < MF; ++m) part[turn][wave][f * MF + m][lane] = acc[f][m];
+        __syncthreads();
+        if (sl != 0) continue;
+        for (int q = 1; q < SPL; ++q)
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int m = 0; m < MF; ++m) acc[f][m] = add4(acc[f][m], part[turn][wave + q][f * MF + m][lane]);
+      }
+      if (!live) continue;
+#pragma unroll
+      for (int m = 0; m < MF; ++m) {
+        const int slot = s0 + m * 16 + i;
+        if (slot >= hi) continue;
+        float v[2][4];
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int n = n0 + g * 4 + r + (a.gated ? 0 : f * 16);
+            v[f][r] = acc[f][m][r];
+            if (a.b1 && n < a.H) v[f][r] += value_at<FMT>(a.b1, (int64_t)e * wide + n + (a.gated ? f * a.H : 0));
+          }
+        float h[2][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          h[0][r] = moe_act(a.act, v[0][r]);
+          if (a.gated) h[0][r] *= v[1][r];
+          else h[1][r] = moe_act(a.act, v[1][r]);
+        }
+        // (the rows of `hidden` are padded to whole steps: no partial store)
+        if (n0 + g * 4 < a.H) store_hidden<FMT>(a, slot, n0 + g * 4, h[0]);
+        if (!a.gated && n0 + 16 + g * 4 < a.H) store_hidden<FMT>(a, slot, n0 + 16 + g * 4, h[1]);
+      }
+    }
+  }
+}
+
+// Block (tile, s): columns 32 tile .. + 31 of Y, range s of all the chosen
+// experts' hidden rows.
+template <int FMT, int MF>
+__global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(const MoeArgs a) {
+  constexpr int HL = FMT == FMT_F32 ? 1 : 2;
+  typedef MoeProduct<FMT, MF, HL> MP;
+  extern __shared__ __attribute__((aligned(16))) float yw[];      // [waves][T][32]
+  __shared__ RouteOut rt;
+  __shared__ int last;
+  const RouteOut* ro = (const RouteOut*)a.route;
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // (all of it at once, before the number of experts is known)
+  const int pairs = a.T * a.top, acts = min(a.E, pairs);
+  for (int p = threadIdx.x; p < pairs; p += kMoeThreads) {
+    rt.tok[p] = ro->tok[p];
+    rt.weight[p] = ro->weight[p];
+  }
+  for (int p = threadIdx.x; p <= acts; p += kMoeThreads) {
+    if (p < acts) rt.act[p] = ro->act[p];
+    rt.off[p] = ro->off[p];
+  }
+  if (threadIdx.x == 0) rt.nact = ro->nact;
+  float* mine = yw + wave * a.T * 32;
+  for (int p = lane; p < a.T * 32; p += 64) mine[p] = 0.0f;
+  __syncthreads();
+
+  const int tile = blockIdx.x / a.S, s = blockIdx.x - tile * a.S, n0 = tile * 32;
+  const int nk = max(1, ceil_div(a.H, MP::KE));
+  const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(rt.nact) * nk, parts = (int64_t)a.S * kMoeWaves;
+  int st = (int)(total * (s * kMoeWaves + wave) / parts);
+  const int end = (int)(total * (s * kMoeWaves + wave + 1) / parts);
+  MP mp;
+  mp.K = a.H;
+  mp.sw_one = true;
+  while (st < end) {
+    const int ai = __builtin_amdgcn_readfirstlane(st / nk), k0 = st - ai * nk, k1 = min(nk, k0 + end - st);
+    const int e = __builtin_amdgcn_readfirstlane(rt.act[ai]), lo = __builtin_amdgcn_readfirstlane(rt.off[ai]);
+    const int hi = __builtin_amdgcn_readfirstlane(rt.off[ai + 1]);
+    mp.weights(0, a.W2, a.s2, e, a.D, n0, a.D);
+    mp.weights(1, a.W2, a.s2, e, a.D, min(n0 + 16, a.D - 1), a.D);
+    for (int s0 = lo; s0 < hi; s0 += 16 * MF) {
+      f32x4_t acc[2][MF];
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int m = 0; m < MF; ++m) acc[f][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      mp.frags = ceil_div(hi - s0, 16);
+#pragma unroll
+      for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int h = 0; h < HL; ++h)
+          mp.x[m][h] = (const char*)a.hidden +
+                       ((int64_t)min(s0 + m * 16 + i, hi - 1) + (int64_t)h * pairs) * a.ldh * (FMT == FMT_F32 ? 4 : 2);
+      mp.run(k0, k1, acc);
+      // into this wave's sums of the tokens (a token has one slot of an expert)
+#pragma unroll
+      for (int m = 0; m < MF; ++m) {
+        const int slot = s0 + m * 16 + i;
+        if (slot >= hi) continue;
+        const float wt = rt.weight[slot];
+        float* y = mine + rt.tok[slot] * 32 + g * 4;
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          f32x4_t v = acc[f][m];
+          if (a.b2 && k0 == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int n = n0 + f * 16 + g * 4 + r;
+              if (n < a.D) v[r] += value_at<FMT>(a.b2, (int64_t)e * a.D + n);
+            }
+          }
+          f32x4_t o = *(f32x4_t*)(y + f * 16);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(wt, v[r], o[r]);
+          *(f32x4_t*)(y + f * 16) = o;
+        }
+      }
+    }
+    st += k1 - k0;
+  }
+  __syncthreads();
+
+  const int quads = a.T * 8;      // four columns of a token
+  auto store = [&](int q, f32x4_t v) {
+    const int t = q >> 3, n = n0 + (q & 7) * 4;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n + r < a.D) {
+        const int64_t at = (int64_t)t * a.D + n + r;
+        if constexpr (FMT == FMT_F32) ((float*)a.Y)[at] = v[r];
+        else ((uint16_t*)a.Y)[at] = (uint16_t)pack_bf16x2(v[r], 0.0f);
+      }
+  };
+  f32x4_t* ws = (f32x4_t*)a.partials + (int64_t)tile * a.S * quads;
+  for (int q = threadIdx.x; q < quads; q += kMoeThreads) {
+    f32x4_t v = ((f32x4_t*)yw)[q];
+#pragma unroll
+    for (int w = 1; w < kMoeWaves; ++w) v = add4(v, ((f32x4_t*)yw)[w * quads + q]);
+    if (a.S == 1) store(q, v);
+    else ws[(int64_t)s * quads + q] = v;
+  }
+  if (a.S == 1) return;
+  // the last block of the tile adds the ranges in their order
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(a.counters + tile, 1) == a.S - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (int q = threadIdx.x; q < quads; q += kMoeThreads) {
+    f32x4_t v = ws[q];
+    for (int p = 1; p < a.S; ++p) v = add4(v, ws[(int64_t)p * quads + q]);
+    store(q, v);
+  }
+}
+
+template <int FMT, int MF>
+int launch(const MoeArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((moe_up_kernel<FMT, MF>), dim3(a.up_blocks), dim3(kMoeThreads), 0, s, a);
+  int rc = (int)hipGetLastError();
+  if (rc) return rc;
+  hipLaunchKernelGGL((moe_down_kernel<FMT, MF>), dim3(a.tiles * a.S), dim3(kMoeThreads), kMoeWaves * a.T * 32 * 4, s, a);
+  return (int)hipGetLastError();
+}
+
+constexpr int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+
+}  // namespace
+
+// Ranges of K that the second kernel's tiles are cut into: about two blocks for
+// every CU.
+static int moe_ranges(int64_t D) {
+  const int64_t tiles = (D + 31) / 32;
+  const int64_t s = (2 * kCus + tiles - 1) / tiles;
+  return (int)(s < 1 ? 1 : s);
+}
+
+// Workspace: routing, counters, hidden rows, partial sums.
+struct MoePlan {
+  int64_t counters, hidden, partials, bytes, ldh;
+};
+static MoePlan moe_plan(int64_t T, int64_t D, int64_t H, int64_t top) {
+  MoePlan p;
+  p.ldh = (H + 63) / 64 * 64;
+  p.counters = up16(sizeof(RouteOut));
+  p.hidden = p.counters + up16((D + 31) / 32 * 4);
+  p.partials = p.hidden + up16(T * top * p.ldh * 4);
+  p.bytes = p.partials + (int64_t)moe_ranges(D) * T * ((D + 31) / 32 * 32) * 4;
+  return p;
+}
+size_t moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t top) {
+  (void)E;
+  return (size_t)moe_plan(T, D, H, top).bytes;
+}
+
+int launch_moe(MoeArgs& a, void* workspace, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  const MoePlan p = moe_plan(a.T, a.D, a.H, a.top);
+  char* ws = (char*)workspace;
+  a.route = ws;
+  a.counters = (int*)(ws + p.counters);
+  a.hidden = ws + p.hidden;
+  a.partials = (float*)(ws + p.partials);
+  a.ldh = p.ldh;
+  a.tiles = ceil_div(a.D, 32);
+  const int64_t experts = a.E < a.T * a.top ? a.E : a.T * a.top;
+  const int esz = a.w_dt == DT_F32 ? 4 : a.w_dt == DT_BF16 ? 2 : 1;
+  // no more ranges than give every wave a step
+  const int64_t steps = experts * (((int64_t)a.H * esz + 127) / 128);
+  int64_t S = moe_ranges(a.D);
+  while (S > 1 && S * kMoeWaves > steps) S = (S + 1) / 2;
+  a.S = (int)S;
+  const int nk = (int)(((int64_t)a.D * esz + 127) / 128);
+  a.slices = 1;
+  while (a.slices < kMoeWaves && a.slices < nk) a.slices *= 2;
+  const int64_t units = experts * ceil_div(ceil_div(a.H, a.gated ? 16 : 32), kMoeWaves / a.slices);
+  a.up_blocks = (int)(units < 1 ? 1 : units < 2 * kCus ? units : 2 * kCus);
+  const bool two = a.T > 16;
+  if (a.w_dt == DT_F32) return two ? launch<FMT_F32, 2>(a, s) : launch<FMT_F32, 1>(a, s);
+  if (a.w_dt == DT_BF16) return two ? launch<FMT_BF16, 2>(a, s) : launch<FMT_BF16, 1>(a, s);
+  return two ? launch<FMT_FP8X, 2>(a, s) : launch<FMT_FP8X, 1>(a, s);
+}
+
+}  // namespace ox

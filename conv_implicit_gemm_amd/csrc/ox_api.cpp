@@ -1212,6 +1212,78 @@ ox_status ox_quantize_i8(ox_dtype t, int64_t rows, int64_t K, const void* X, int
   return norm_result(fn, rows, K, launch_quantize_i8(a, stream));
 }
 
+size_t ox_moe_few_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t top) {
+  if (T < 1 || T > kMoeTokens || D < 1 || H < 0 || E < 1 || E > kMoeExperts || top < 1 || top > kMoeTop || top > E ||
+      D > kMoeWidth || H > kMoeWidth || too_big(T, D) || too_big(E, D, H))
+    return 0;
+  return moe_workspace_bytes(T, D, H, E, top);
+}
+
+ox_status ox_moe_few(ox_dtype t, ox_dtype w_type, int64_t T, int64_t D, int64_t H, int64_t E, int64_t top,
+                     const void* X, ox_dtype scores_type, const void* scores, int renormalise, const void* W1,
+                     const float* w1_scales, const void* b1, ox_act act, int gated, const void* W2,
+                     const float* w2_scales, const void* b2, int32_t* experts, float* weights, void* Y,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "ox_moe_few";
+  ox_status st = check_float_dt(fn, t);
+  if (st) return st;
+  if (w_type != t && !(t == OX_BF16 && w_type == OX_F8E4M3))
+    return fail(OX_ERR_UNSUPPORTED, "%s: w_type %d is neither t nor OX_F8E4M3 beside OX_BF16", fn, (int)w_type);
+  if (scores_type != OX_F32 && scores_type != OX_BF16)
+    return fail(OX_ERR_UNSUPPORTED, "%s: scores_type %d is not OX_F32 or OX_BF16", fn, (int)scores_type);
+  if (act != OX_ACT_SILU) {
+    st = check_act(fn, act);
+    if (st) return st;
+  }
+  if (T < 0 || D < 0 || H < 0 || E < 0)
+    return fail(OX_ERR_SHAPE, "%s: a negative size (T %lld, D %lld, H %lld, experts %lld)", fn, (long long)T, (long long)D,
+                (long long)H, (long long)E);
+  if (T > kMoeTokens)
+    return fail(OX_ERR_UNSUPPORTED, "%s: T=%lld, up to %d tokens (ox_gemm_grouped takes more)", fn, (long long)T, kMoeTokens);
+  if (T == 0 || D == 0) return ok();
+  if (E > kMoeExperts) return fail(OX_ERR_UNSUPPORTED, "%s: %lld experts, up to %d", fn, (long long)E, kMoeExperts);
+  if (top < 1 || top > E) return fail(OX_ERR_SHAPE, "%s: top=%lld of %lld experts", fn, (long long)top, (long long)E);
+  if (top > kMoeTop) return fail(OX_ERR_UNSUPPORTED, "%s: top=%lld, up to %d experts a token", fn, (long long)top, kMoeTop);
+  if (D > kMoeWidth || H > kMoeWidth)
+    return fail(OX_ERR_UNSUPPORTED, "%s: D=%lld or H=%lld is above %d", fn, (long long)D, (long long)H, kMoeWidth);
+  if (too_big(T, D) || too_big(E, gated ? 2 * H : H, D)) return fail(OX_ERR_UNSUPPORTED, "%s: a tensor holds 2^31 elements or more", fn);
+  if (!X || !scores || !Y) return fail(OX_ERR_INVALID_ARG, "%s: X, scores or Y is NULL", fn);
+  if (H > 0 && (!W1 || !W2)) return fail(OX_ERR_INVALID_ARG, "%s: W1 or W2 is NULL", fn);
+  if (H > 0 && w_type == OX_F8E4M3 && (!w1_scales || !w2_scales))
+    return fail(OX_ERR_INVALID_ARG, "%s: w1_scales or w2_scales is NULL", fn);
+  const int n = esize(t), m = w_type == OX_F8E4M3 ? 1 : n;
+  if (!aligned_to(X, n) || !aligned_to(Y, n) || !aligned_to(b1, n) || !aligned_to(b2, n) || !aligned_to(W1, m) ||
+      !aligned_to(W2, m) || !aligned_to(scores, esize(scores_type)) || !aligned_to(w1_scales, 4) ||
+      !aligned_to(w2_scales, 4) || !aligned_to(experts, 4) || !aligned_to(weights, 4))
+    return fail(OX_ERR_INVALID_ARG, "%s: a pointer is not aligned to its element size", fn);
+  const size_t need = moe_workspace_bytes(T, D, H, E, top);
+  if (!workspace || workspace_bytes < need || !aligned16(workspace))
+    return fail(OX_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned and hold %zu bytes", fn, need);
+  MoeArgs a = {};
+  a.T = (int)T;
+  a.D = (int)D;
+  a.H = (int)H;
+  a.E = (int)E;
+  a.top = (int)top;
+  a.w_dt = w_type == OX_F8E4M3 ? DT_F8 : (int)t;
+  a.scores_dt = scores_type;
+  a.renormalise = renormalise != 0;
+  a.gated = gated != 0;
+  a.act = act;
+  a.X = X;
+  a.scores = scores;
+  a.W1 = W1;
+  a.s1 = w1_scales;
+  a.b1 = b1;
+  a.W2 = W2;
+  a.s2 = w2_scales;
+  a.b2 = b2;
+  a.experts = experts;
+  a.weights = weights;
+  a.Y = Y;
+  return hip_result(fn, launch_moe(a, workspace, stream));
+}
+
 size_t ox_dynamic_quantize_workspace_bytes(void) { return dynq_workspace_bytes(); }
 
 ox_status ox_dynamic_quantize_linear(int64_t n, const float* X, uint8_t* Y, float* y_scale,

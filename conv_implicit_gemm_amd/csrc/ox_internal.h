@@ -13,7 +13,7 @@ namespace ox {
 enum Dt : int { DT_F32 = 0, DT_BF16 = 1, DT_I8 = 2, DT_I32 = 3, DT_F8 = 4 };
 
 // activations (same values as ox_act)
-enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_RELU6 = 2, ACT_GELU = 3 };
+enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_RELU6 = 2, ACT_GELU = 3, ACT_SILU = 4 };
 
 // Tile shapes of the MFMA tile engine (block tile BM x BN, 4 waves in 2x2).
 enum Tile : int {
@@ -338,6 +338,35 @@ struct NormArgs {
 };
 int launch_rmsnorm(const NormArgs& a, void* stream);
 int launch_quantize_i8(const NormArgs& a, void* stream);
+
+// A routed feed-forward layer of a few tokens.
+constexpr int kMoeTokens = 64, kMoeTop = 16, kMoeExperts = 512, kMoeWidth = 1 << 24;   // the most of each
+struct MoeArgs {
+  int T, D, H, E, top;     // tokens, their width, the experts' hidden width, experts, experts of a token
+  int w_dt;                // W1, W2: DT_F32, DT_BF16 (X, biases and Y too) or DT_F8 (those bf16)
+  int scores_dt;           // DT_F32 or DT_BF16
+  int renormalise, gated, act;
+  const void* X;           // [T, D]
+  const void* scores;      // [T, E]
+  const void* W1;          // [E][H, D], or [E][2H, D] when gated: gate rows, then up rows
+  const float* s1;         // e4m3: scales [E][ceil(rows/128)][ceil(D/128)]
+  const void* b1;          // [E][rows of W1] or null
+  const void* W2;          // [E][D, H]
+  const float* s2;         // e4m3: scales [E][ceil(D/128)][ceil(H/128)]
+  const void* b2;          // [E][D] or null
+  int32_t* experts;        // [T, top] or null
+  float* weights;          // [T, top] or null
+  void* Y;                 // [T, D]
+  // set by the launcher: the workspace's parts and the grids
+  void* route;
+  int* counters;           // [tiles]
+  void* hidden;            // [T * top][ldh], bf16: twice (high and low parts)
+  float* partials;         // [tiles][S][T][32]
+  int64_t ldh;
+  int tiles, S, slices, up_blocks;
+};
+size_t moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t top);
+int launch_moe(MoeArgs& a, void* workspace, void* stream);
 
 size_t dynq_workspace_bytes();
 int launch_dynamic_quantize(int64_t n, const float* X, uint8_t* Y, float* y_scale, uint8_t* y_zp,

@@ -56,8 +56,8 @@ typedef enum { OX_F32 = 0, OX_BF16 = 1, OX_I8 = 2, OX_I32 = 3, OX_F8E4M3 = 4 } o
 /* Fused activations.  ReLU = max(v,0); ReLU6 = min(max(v,0),6) (the clamp the
  * Kyanite README "Optimizer" section merges relu/min/max into); GELU is the
  * exact erf form 0.5*v*(1+erf(v/sqrt(2))) (the Gelu composite of the Onyxia
- * README). */
-typedef enum { OX_ACT_NONE = 0, OX_ACT_RELU = 1, OX_ACT_RELU6 = 2, OX_ACT_GELU = 3 } ox_act;
+ * README); SiLU, v/(1+exp(-v)), is taken by ox_moe_few alone. */
+typedef enum { OX_ACT_NONE = 0, OX_ACT_RELU = 1, OX_ACT_RELU6 = 2, OX_ACT_GELU = 3, OX_ACT_SILU = 4 } ox_act;
 
 /* ONNX Conv geometry.  Input X [N, C, H, W], weights [M, C/group, kH, kW],
  * output Y [N, M, Ho, Wo] with
@@ -497,6 +497,44 @@ ox_status ox_gemm_grouped_fp8(ox_dtype y_type, int64_t T, int64_t N, int64_t K, 
                               const uint8_t* A, const float* a_scales, const uint8_t* B,
                               const float* b_scales, const int32_t* offsets, const void* bias,
                               ox_act act, void* Y, void* stream);
+
+/* A whole feed-forward layer of routed experts for up to 64 tokens (a decoding
+ * step), in two kernels: from the router's scores to the weighted sum.
+ *   chosen(t) = the `top` experts with the largest scores[t,:], ties to the
+ *               lowest index; NaN and -inf are never chosen, +inf counts as the
+ *               largest finite number
+ *   w[t,e]    = exp(scores[t,e]) / sum of exp(scores[t,:]) over chosen(t)
+ *               (renormalise != 0) or over all experts (renormalise = 0)
+ *   h[t,e]    = act(W1[e] X[t] + b1[e]), or where gated (W1[e] holds H gate rows,
+ *               then H up rows) act(gate) * up
+ *   Y[t]      = sum over chosen(t) of w[t,e] * (W2[e] h[t,e] + b2[e])
+ * A token with fewer scores to choose from takes those; one with none (a padded
+ * place: all -inf) gets zeros, and costs nothing.  What the weights of an
+ * expert hold reaches the tokens that chose it, no others (ReLU and ReLU6 take
+ * NaN to 0, as everywhere in this library).
+ * t: OX_F32 or OX_BF16, the type of X, Y DEVICE [T, D], b1 DEVICE [E][H or 2H]
+ * and b2 DEVICE [E][D] (each may be NULL).  scores: DEVICE [T, E] of
+ * scores_type, OX_F32 or OX_BF16 (the router's product, e.g. by ox_gemm_fused).
+ * W1: DEVICE [E][H or 2H, D], W2: DEVICE [E][D, H], of w_type: t, or OX_F8E4M3
+ * beside t = OX_BF16, with scales per 128 x 128 as ox_quantize_fp8 makes them,
+ * w1_scales DEVICE fp32 [E][ceil(rows/128)][ceil(D/128)], w2_scales
+ * [E][ceil(D/128)][ceil(H/128)] (ignored otherwise); the tokens stay bf16.
+ * act: any ox_act, OX_ACT_SILU included.
+ * experts: DEVICE int32 [T, top], the chosen by falling score (-1 where there is
+ * none), weights: DEVICE fp32 [T, top]; either may be NULL.
+ * Sums are fp32, and Y is rounded once (h passes in 16 bits of significand for
+ * bf16); their order depends on the sizes and on the routing alone.
+ * T <= 64, E <= 512, top <= 16, D and H <= 2^24 (OX_ERR_UNSUPPORTED above; ox_gemm_grouped takes
+ * any number of rows).  T = 0 or D = 0 enqueue nothing.
+ * workspace: DEVICE, 16-byte aligned, at least ox_moe_few_workspace_bytes(T, D,
+ * H, E, top) bytes (0 for sizes that the call refuses); its contents on entry do
+ * not matter.  Calls (and captured graphs) that share one must not overlap. */
+size_t ox_moe_few_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t top);
+ox_status ox_moe_few(ox_dtype t, ox_dtype w_type, int64_t T, int64_t D, int64_t H, int64_t E, int64_t top,
+                     const void* X, ox_dtype scores_type, const void* scores, int renormalise, const void* W1,
+                     const float* w1_scales, const void* b1, ox_act act, int gated, const void* W2,
+                     const float* w2_scales, const void* b2, int32_t* experts, float* weights, void* Y,
+                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* The message of the last failing call on this thread ("" if none). */
 const char* ox_last_error(void);
