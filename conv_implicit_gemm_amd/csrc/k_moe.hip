@@ -372,6 +372,23 @@ struct MoeProduct {
   }
 };
 
+// Four sums that a block of another XCD reads: past the L2s, which are not
+// coherent, by accesses of agent scope (an agent fence instead, which writes the
+// whole L2 back, cost 80 us in a kernel of 512 blocks).
+__device__ __forceinline__ void store_shared(f32x4_t* p, f32x4_t v) {
+  uint64_t w[2];
+  __builtin_memcpy(w, &v, 16);
+  __hip_atomic_store((uint64_t*)p, w[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store((uint64_t*)p + 1, w[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x4_t load_shared(const f32x4_t* p) {
+  uint64_t w[2] = {__hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
+                   __hip_atomic_load((const uint64_t*)p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)};
+  f32x4_t v;
+  __builtin_memcpy(&v, w, 16);
+  return v;
+}
+
 // Four consecutive hidden values of a slot, as the second kernel reads them.
 template <int FMT>
 __device__ __forceinline__ void store_hidden(const MoeArgs& a, int slot, int n, const float (&h)[4]) {
@@ -577,19 +594,20 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(const MoeArgs a) 
 #pragma unroll
     for (int w = 1; w < kMoeWaves; ++w) v = add4(v, ((f32x4_t*)yw)[w * quads + q]);
     if (a.S == 1) store(q, v);
-    else ws[(int64_t)s * quads + q] = v;
+    else store_shared(ws + (int64_t)s * quads + q, v);
   }
   if (a.S == 1) return;
-  // the last block of the tile adds the ranges in their order
-  __threadfence();
+  // the last block of the tile adds the ranges in their order; every wave's
+  // stores have arrived before its block counts itself
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(a.counters + tile, 1) == a.S - 1;
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(a.counters + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.S - 1;
   __syncthreads();
   if (!last) return;
-  __threadfence();
   for (int q = threadIdx.x; q < quads; q += kMoeThreads) {
-    f32x4_t v = ws[q];
-    for (int p = 1; p < a.S; ++p) v = add4(v, ws[(int64_t)p * quads + q]);
+    f32x4_t v = load_shared(ws + q);
+    for (int p = 1; p < a.S; ++p) v = add4(v, load_shared(ws + (int64_t)p * quads + q));
     store(q, v);
   }
 }
