@@ -218,26 +218,41 @@ __device__ __forceinline__ void route(const MoeArgs& a, Route& rt, bool out) {
 
 // ------------------------------------------------------------ products --
 
+// A pointer in scalar registers, known to be global memory: loads take it as
+// their base beside a 32-bit offset.
+#define OX_GLOBAL __attribute__((address_space(1)))
+typedef const OX_GLOBAL char* Global;
+__device__ __forceinline__ Global uniform_global(const void* p) {
+  return (Global)(uintptr_t)uniform_ptr((const char*)p);
+}
+
+// The same number, of which the compiler knows nothing: it would add a lane's
+// offsets to the bases once for all, 64 bits for every load, and spill.
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // bytes [0, n) of 16 at p, whole elements of ESZ bytes; zeros behind them (n <= 0:
 // none)
 template <int ESZ>
-__device__ __forceinline__ u32x4_t part_of_piece(const char* p, int n) {
-  if (n >= 16) return ((const Bytes16*)p)->v;
+__device__ __forceinline__ u32x4_t part_of_piece(Global p, int n) {
+  if (n >= 16) return ((const OX_GLOBAL Bytes16*)p)->v;
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int i = 0; i < 16; i += ESZ)
     if (i < n) {
-      if constexpr (ESZ == 4) w[i / 4] = *(const uint32_t*)(p + i);
-      else if constexpr (ESZ == 2) w[i / 4] |= (uint32_t)*(const uint16_t*)(p + i) << (8 * (i % 4));
+      if constexpr (ESZ == 4) w[i / 4] = *(const OX_GLOBAL uint32_t*)(p + i);
+      else if constexpr (ESZ == 2) w[i / 4] |= (uint32_t)*(const OX_GLOBAL uint16_t*)(p + i) << (8 * (i % 4));
       else w[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
     }
   return u32x4_t{w[0], w[1], w[2], w[3]};
 }
 
 // Two fragments of 16 rows of weights times MF fragments of 16 tokens, over steps
-// [k0, k1) of K (128 bytes of a weight row each).  The tokens' rows come in HL
-// parts that are added (the hidden rows: 2).
-template <int FMT, int MF, int HL>
+// [k0, k1) of K (128 bytes of a weight row each).
+// ONE: a fragment's sixteen rows of weights share a scale (e4m3).
+template <int FMT, int MF, bool ONE>
 struct MoeProduct {
   typedef FmtOps<FMT> Mm;
   typedef typename Mm::Frag Frag;
@@ -245,26 +260,27 @@ struct MoeProduct {
   static constexpr int KE = 128 / Mm::ESZ;         // K of a step
   static constexpr int XP = F8 ? 4 : 2;            // pieces of a token's step
   static constexpr int XB = F8 ? 256 : 128;        // its bytes
-  // Steps in flight: with 16 waves on a CU, 16 KB of weights a wave would do;
-  // the tokens' pieces share the registers.
-  static constexpr int U = MF * HL * XP >= 16 ? 1 : 2;
+  // Steps in flight, as many as 128 registers hold (16 waves a CU).
+  static constexpr int REGS = 16 + MF * XP * 4 + (F8 ? ONE ? 0 : 8 : 0);
+  static constexpr int U = REGS <= 24 ? 3 : REGS <= 40 ? 2 : 1;
 
-  const char* w[2];            // this lane's rows of weights
-  const char* x[MF][HL];       // this lane's tokens
+  // Bases for all lanes, and this lane's offsets from them (its row, its first
+  // piece): a load is a scalar base, a 32-bit offset and a constant.
+  Global w[2];                 // the fragments' first rows of weights
+  uint32_t wo[2];
+  Global x;                    // the first token
+  uint32_t xo[MF];
   int frags;                   // token fragments that hold tokens
-  const float* sw[2];          // e4m3: the rows' scales (step 0) ...
-  int sw_rows[2][4];           // ... and where a lane's four rows have theirs
-  bool sw_one;                 // all rows of a fragment share one
+  const float* sw[2];          // e4m3: the expert's scales, ONE: the fragment's (step 0)
+  int sw_rows[2][4];           // ... where a lane's four rows have theirs
   int K;
 
-  static __device__ __forceinline__ int x_at(int i) {
-    const int g = (threadIdx.x & 63) >> 4;
-    return F8 ? g * 32 + (i & 1) * 16 + (i >> 1) * 128 : g * 16 + i * 64;
-  }
+  // piece i of a token's step, behind the lane's first
+  static __device__ __forceinline__ constexpr int x_at(int i) { return F8 ? (i & 1) * 16 + (i >> 1) * 128 : i * 64; }
 
   struct Step {
-    u32x4_t w[2][2], x[MF][HL][XP];
-    float s[2][4];
+    u32x4_t w[2][2], x[MF][XP];
+    float s[2][ONE ? 1 : 4];
   };
   // PART: K may end inside the step
   template <bool PART>
@@ -273,30 +289,42 @@ struct MoeProduct {
     const int left = (int)min((int64_t)XB, ((int64_t)K - (int64_t)k * KE) * Mm::ESZ);      // bytes of a weight row
     const int64_t wk = (int64_t)k * 128, xk = (int64_t)k * XB;
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < 2; ++f) {
+      const Global p = w[f] + wk;
+      const uint32_t o = opaque(wo[f]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int o = g * 16 + i * 64;
-        st.w[f][i] = PART ? part_of_piece<Mm::ESZ>(w[f] + wk + o, left - o) : ((const Bytes16*)(w[f] + wk + o))->v;
-      }
+      for (int i = 0; i < 2; ++i)
+        if constexpr (PART) {
+          st.w[f][i] = part_of_piece<Mm::ESZ>(p + o + i * 64, left - g * 16 - i * 64);
+          __builtin_amdgcn_sched_barrier(0);      // (one at a time: registers)
+        } else {
+          st.w[f][i] = ((const OX_GLOBAL Bytes16*)(p + o + i * 64))->v;
+        }
+    }
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
       if (m > 0 && m >= frags) break;
+      const Global p = x + xk;
+      const uint32_t o = opaque(xo[m]);
 #pragma unroll
-      for (int h = 0; h < HL; ++h)
-#pragma unroll
-        for (int i = 0; i < XP; ++i) {
-          const int o = x_at(i);
-          st.x[m][h][i] = PART ? part_of_piece<F8 ? 2 : Mm::ESZ>(x[m][h] + xk + o, left * (XB / 128) - o)
-                               : ((const Bytes16*)(x[m][h] + xk + o))->v;
+      for (int i = 0; i < XP; ++i)
+        if constexpr (PART) {
+          st.x[m][i] = part_of_piece<F8 ? 2 : Mm::ESZ>(p + o + x_at(i), (left - g * 16) * (XB / 128) - x_at(i));
+          __builtin_amdgcn_sched_barrier(0);
+        } else {
+          st.x[m][i] = ((const OX_GLOBAL Bytes16*)(p + o + x_at(i)))->v;
         }
     }
     if constexpr (F8) {
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        st.s[f][0] = sw[f][sw_rows[f][0] + k];
+        typedef const __attribute__((address_space(4))) float* Scalar;
+        if constexpr (ONE) {
+          st.s[f][0] = *(Scalar)(uintptr_t)(sw[f] + k);      // (by a scalar load)
+        } else {
 #pragma unroll
-        for (int r = 1; r < 4; ++r) st.s[f][r] = sw_one ? st.s[f][0] : sw[f][sw_rows[f][r] + k];
+          for (int r = 0; r < 4; ++r) st.s[f][r] = sw[f][sw_rows[f][r] + k];
+        }
       }
     }
   }
@@ -306,66 +334,85 @@ struct MoeProduct {
     for (int i = 0; i < XP; ++i) f.v[i] = p[i];
     return f;
   }
-  template <int N>
-  __device__ __forceinline__ void multiply(const Step (&st)[N], f32x4_t (&acc)[2][MF]) const {
+  __device__ __forceinline__ void multiply(const Step& st, f32x4_t (&acc)[2][MF]) const {
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
       if (m > 0 && m >= frags) break;
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         f32x4_t chain = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-          const Frag b = Mm::widen(st[u].w[f][0], st[u].w[f][1]);
-          if constexpr (F8) chain = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int h = 0; h < HL; ++h) {
-            const Frag t = token_frag(st[u].x[m][h]);
-            chain = Mm::template half<0>(b, t, chain);
-            chain = Mm::template half<1>(b, t, chain);
-            if constexpr (F8) {
-              chain = Mm::template half<2>(b, t, chain);
-              chain = Mm::template half<3>(b, t, chain);
-            }
-          }
-          if constexpr (F8) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[f][m][r] = __builtin_fmaf(st[u].s[f][r], chain[r], acc[f][m][r]);
-          }
+        const Frag b = Mm::widen(st.w[f][0], st.w[f][1]), t = token_frag(st.x[m]);
+        chain = Mm::template half<0>(b, t, chain);
+        chain = Mm::template half<1>(b, t, chain);
+        if constexpr (F8) {
+          chain = Mm::template half<2>(b, t, chain);
+          chain = Mm::template half<3>(b, t, chain);
         }
-        if constexpr (!F8) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[f][m][r] += chain[r];
-        }
+        for (int r = 0; r < 4; ++r)
+          acc[f][m][r] = F8 ? __builtin_fmaf(st.s[f][ONE ? 0 : r], chain[r], acc[f][m][r]) : acc[f][m][r] + chain[r];
       }
     }
   }
-  __device__ __forceinline__ void run(int k0, int k1, f32x4_t (&acc)[2][MF]) const {
+  __device__ __forceinline__ void run(int first, int end, f32x4_t (&acc)[2][MF]) const {
+    const int k0 = __builtin_amdgcn_readfirstlane(first), k1 = __builtin_amdgcn_readfirstlane(end);
     if (K == 0) return;
+    const int whole = min(k1, K / KE);      // steps that K does not end inside
     int k = k0;
-#pragma unroll 1
-    for (; k + U <= k1 && (int64_t)(k + U) * KE <= K; k += U) {
+    if (k + U <= whole) {
+      // U steps in flight: each is loaded again, U further on, as soon as it is
+      // multiplied (the order is pinned: loads would sink to their uses)
       Step st[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) load<false>(k + u, st[u]);
-      __builtin_amdgcn_sched_barrier(0);      // every load goes out before the first product
-      multiply(st, acc);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll 1
+      for (; k + 2 * U <= whole; k += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          multiply(st[u], acc);
+          load<false>(k + U + u, st[u]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      // what is left: fewer than U steps behind those in flight
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        multiply(st[u], acc);
+        if (u + 1 < U && k + U + u < whole) load<false>(k + U + u, st[u]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      k += U;
+#pragma unroll
+      for (int u = 0; u + 1 < U; ++u)
+        if (k + u < whole) multiply(st[u], acc);
+      k = max(k, whole);
     }
 #pragma unroll 1
-    for (; k < k1; ++k) {
-      Step st[1];
-      load<true>(k, st[0]);
+    for (; k < whole; ++k) {
+      Step st;
+      load<false>(k, st);
       multiply(st, acc);
     }
+    if (k < k1) {
+      Step st;
+      load<true>(k, st);
+      multiply(st, acc);
+    }
+  }
+  // token fragment m: this lane's row, `ld` bytes to a row
+  __device__ __forceinline__ void token(int m, uint32_t row, uint32_t ld) {
+    xo[m] = row * ld + ((threadIdx.x & 63) >> 4) * (XB / 8);
   }
   // fragment f: rows n .. n + 15 of expert e's `rows` rows, of which those below
   // `end` count
   __device__ __forceinline__ void weights(int f, const void* W, const float* scales, int e, int rows, int n, int end) {
     const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-    w[f] = (const char*)W + ((int64_t)e * rows + min(n + i, end - 1)) * K * Mm::ESZ;
+    w[f] = uniform_global((const char*)W + ((int64_t)e * rows + n) * K * Mm::ESZ);
+    wo[f] = (uint32_t)min(i, end - 1 - n) * (uint32_t)K * Mm::ESZ + g * 16;
     if constexpr (F8) {
       const int nb = ceil_div(rows, 128), kb = ceil_div(K, 128);
-      sw[f] = scales + (int64_t)e * nb * kb;
+      sw[f] = uniform_ptr(scales + (int64_t)e * nb * kb + (ONE ? min(n, end - 1) / 128 * kb : 0));
 #pragma unroll
       for (int r = 0; r < 4; ++r) sw_rows[f][r] = min(n + g * 4 + r, end - 1) / 128 * kb;
     }
@@ -401,9 +448,9 @@ __device__ __forceinline__ void store_hidden(const MoeArgs& a, int slot, int n, 
       hi[r] = bf16_to_f32((uint16_t)pack_bf16x2(h[r], 0.0f));
       lo[r] = __builtin_isfinite(hi[r]) ? h[r] - hi[r] : 0.0f;
     }
-    uint16_t* p = (uint16_t*)a.hidden + (int64_t)slot * a.ldh + n;
+    uint16_t* p = (uint16_t*)a.hidden + (int64_t)slot * 2 * a.ldh + n;      // the two parts in turn
     *(u32x2_t*)p = u32x2_t{pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
-    *(u32x2_t*)(p + (int64_t)a.T * a.top * a.ldh) = u32x2_t{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3])};
+    *(u32x2_t*)(p + a.ldh) = u32x2_t{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3])};
   }
 }
 template <int FMT>
@@ -413,9 +460,9 @@ __device__ __forceinline__ float value_at(const void* p, int64_t at) {
 
 // Units of one expert x a group of column tiles, in turn over the grid's blocks.
 // A column tile is 16 gate rows and the 16 up rows beside them, or 32 rows.
-template <int FMT, int MF>
-__global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(const MoeArgs a) {
-  typedef MoeProduct<FMT, MF, 1> MP;
+template <int FMT, int MF, bool ONE>
+__global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(const MoeArgs a) {
+  typedef MoeProduct<FMT, MF, ONE> MP;
   __shared__ Route rt;
   __shared__ f32x4_t part[2][kMoeWaves][2 * MF][64];
   route(a, rt, blockIdx.x == 0);
@@ -424,12 +471,13 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(const MoeArgs a) {
   const int wide = a.gated ? 2 * a.H : a.H, per = a.gated ? 16 : 32, tiles = ceil_div(a.H, per);
   const int nk = ceil_div(a.D, MP::KE);
   const int SPL = a.slices, CT = kMoeWaves / SPL, groups = ceil_div(tiles, CT);
-  const int ct = wave / SPL, sl = wave - ct * SPL;
+  const int ct = __builtin_amdgcn_readfirstlane(wave / SPL), sl = wave - ct * SPL;
   const int k0 = (int)((int64_t)nk * sl / SPL), k1 = (int)((int64_t)nk * (sl + 1) / SPL);
   int turn = 0;
   for (int unit = blockIdx.x; unit < rt.nact * groups; unit += gridDim.x) {
     const int ai = unit / groups, tile = (unit - ai * groups) * CT + ct, n0 = tile * per;
-    const int e = rt.act[ai], lo = rt.off[ai], hi = rt.off[ai + 1];
+    const int e = __builtin_amdgcn_readfirstlane(rt.act[ai]), lo = __builtin_amdgcn_readfirstlane(rt.off[ai]);
+    const int hi = __builtin_amdgcn_readfirstlane(rt.off[ai + 1]);
     const bool live = tile < tiles;      // whole waves; the barriers below are passed by all
     MP mp;
     mp.K = a.D;
@@ -437,7 +485,6 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(const MoeArgs a) {
       mp.weights(0, a.W1, a.s1, e, wide, n0, a.H);
       if (a.gated) mp.weights(1, a.W1, a.s1, e, wide, a.H + n0, wide);
       else mp.weights(1, a.W1, a.s1, e, wide, min(n0 + 16, a.H - 1), a.H);
-      mp.sw_one = a.gated ? a.H % 16 == 0 : true;
     }
     for (int s0 = lo; s0 < hi; s0 += 16 * MF, turn ^= 1) {
       f32x4_t acc[2][MF];
@@ -447,9 +494,9 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(const MoeArgs a) {
         for (int m = 0; m < MF; ++m) acc[f][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       if (live) {
         mp.frags = ceil_div(hi - s0, 16);
+        mp.x = uniform_global(a.X);
 #pragma unroll
-        for (int m = 0; m < MF; ++m)
-          mp.x[m][0] = (const char*)a.X + (int64_t)rt.tok[min(s0 + m * 16 + i, hi - 1)] * a.D * (FMT == FMT_F32 ? 4 : 2);
+        for (int m = 0; m < MF; ++m) mp.token(m, rt.tok[min(s0 + m * 16 + i, hi - 1)], a.D * (FMT == FMT_F32 ? 4 : 2));
         mp.run(k0, k1, acc);
       }
       if (SPL > 1) {
@@ -495,11 +542,12 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(const MoeArgs a) {
 }
 
 // Block (tile, s): columns 32 tile .. + 31 of Y, range s of all the chosen
-// experts' hidden rows.
+// experts' hidden rows.  A hidden row's two parts lie in neighbouring columns of
+// a token fragment, which holds eight slots then, and their sums are added.
 template <int FMT, int MF>
-__global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(const MoeArgs a) {
-  constexpr int HL = FMT == FMT_F32 ? 1 : 2;
-  typedef MoeProduct<FMT, MF, HL> MP;
+__global__ __launch_bounds__(kMoeThreads, 4) void moe_down_kernel(const MoeArgs a) {
+  constexpr int PARTS = FMT == FMT_F32 ? 1 : 2, SLOTS = 16 / PARTS;      // of a hidden row; of a fragment
+  typedef MoeProduct<FMT, MF, true> MP;
   extern __shared__ __attribute__((aligned(16))) float yw[];      // [waves][T][32]
   __shared__ RouteOut rt;
   __shared__ int last;
@@ -528,32 +576,36 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(const MoeArgs a) 
   const int end = (int)(total * (s * kMoeWaves + wave + 1) / parts);
   MP mp;
   mp.K = a.H;
-  mp.sw_one = true;
   while (st < end) {
     const int ai = __builtin_amdgcn_readfirstlane(st / nk), k0 = st - ai * nk, k1 = min(nk, k0 + end - st);
     const int e = __builtin_amdgcn_readfirstlane(rt.act[ai]), lo = __builtin_amdgcn_readfirstlane(rt.off[ai]);
     const int hi = __builtin_amdgcn_readfirstlane(rt.off[ai + 1]);
     mp.weights(0, a.W2, a.s2, e, a.D, n0, a.D);
     mp.weights(1, a.W2, a.s2, e, a.D, min(n0 + 16, a.D - 1), a.D);
-    for (int s0 = lo; s0 < hi; s0 += 16 * MF) {
+    mp.x = uniform_global((const char*)a.hidden + (int64_t)lo * a.ldh * 4);
+    for (int s0 = lo; s0 < hi; s0 += SLOTS * MF) {
       f32x4_t acc[2][MF];
 #pragma unroll
       for (int f = 0; f < 2; ++f)
 #pragma unroll
         for (int m = 0; m < MF; ++m) acc[f][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      mp.frags = ceil_div(hi - s0, 16);
+      mp.frags = ceil_div(hi - s0, SLOTS);
 #pragma unroll
       for (int m = 0; m < MF; ++m)
-#pragma unroll
-        for (int h = 0; h < HL; ++h)
-          mp.x[m][h] = (const char*)a.hidden +
-                       ((int64_t)min(s0 + m * 16 + i, hi - 1) + (int64_t)h * pairs) * a.ldh * (FMT == FMT_F32 ? 4 : 2);
+        mp.token(m, (min(s0 + m * SLOTS + i / PARTS, hi - 1) - lo) * PARTS + i % PARTS, (uint32_t)a.ldh * (4 / PARTS));
       mp.run(k0, k1, acc);
       // into this wave's sums of the tokens (a token has one slot of an expert)
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
-        const int slot = s0 + m * 16 + i;
-        if (slot >= hi) continue;
+        const int slot = s0 + m * SLOTS + i / PARTS;
+        if constexpr (PARTS == 2) {
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[f][m][r] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc[f][m][r]), 0xB1, 0xf, 0xf, true));   // lane ^ 1
+        }
+        if (slot >= hi || i % PARTS != 0) continue;
         const float wt = rt.weight[slot];
         float* y = mine + rt.tok[slot] * 32 + g * 4;
 #pragma unroll
@@ -606,18 +658,31 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(const MoeArgs a) 
   __syncthreads();
   if (!last) return;
   for (int q = threadIdx.x; q < quads; q += kMoeThreads) {
-    f32x4_t v = load_shared(ws + q);
-    for (int p = 1; p < a.S; ++p) v = add4(v, load_shared(ws + (int64_t)p * quads + q));
+    // (eight loads at a time: one after the other they cost a trip to memory each)
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    for (int p0 = 0; p0 < a.S; p0 += 8) {
+      f32x4_t o[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) o[p] = load_shared(ws + (int64_t)min(p0 + p, a.S - 1) * quads + q);
+#pragma unroll
+      for (int p = 0; p < 8; ++p)
+        if (p0 + p < a.S) v = add4(v, o[p]);
+    }
     store(q, v);
   }
 }
 
-template <int FMT, int MF>
+// UF, DF: token fragments at a time in the first and the second kernel
+template <int FMT, int UF, int DF>
 int launch(const MoeArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((moe_up_kernel<FMT, MF>), dim3(a.up_blocks), dim3(kMoeThreads), 0, s, a);
+  // (the up rows of a gated W1 start anywhere in a block of scales)
+  if (FMT == FMT_FP8X && a.gated && a.H % 16 != 0)
+    hipLaunchKernelGGL((moe_up_kernel<FMT, UF, FMT != FMT_FP8X>), dim3(a.up_blocks), dim3(kMoeThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((moe_up_kernel<FMT, UF, true>), dim3(a.up_blocks), dim3(kMoeThreads), 0, s, a);
   int rc = (int)hipGetLastError();
   if (rc) return rc;
-  hipLaunchKernelGGL((moe_down_kernel<FMT, MF>), dim3(a.tiles * a.S), dim3(kMoeThreads), kMoeWaves * a.T * 32 * 4, s, a);
+  hipLaunchKernelGGL((moe_down_kernel<FMT, DF>), dim3(a.tiles * a.S), dim3(kMoeThreads), kMoeWaves * a.T * 32 * 4, s, a);
   return (int)hipGetLastError();
 }
 
@@ -673,10 +738,11 @@ int launch_moe(MoeArgs& a, void* workspace, void* stream) {
   while (a.slices < kMoeWaves && a.slices < nk) a.slices *= 2;
   const int64_t units = experts * ceil_div(ceil_div(a.H, a.gated ? 16 : 32), kMoeWaves / a.slices);
   a.up_blocks = (int)(units < 1 ? 1 : units < 2 * kCus ? units : 2 * kCus);
-  const bool two = a.T > 16;
-  if (a.w_dt == DT_F32) return two ? launch<FMT_F32, 2>(a, s) : launch<FMT_F32, 1>(a, s);
-  if (a.w_dt == DT_BF16) return two ? launch<FMT_BF16, 2>(a, s) : launch<FMT_BF16, 1>(a, s);
-  return two ? launch<FMT_FP8X, 2>(a, s) : launch<FMT_FP8X, 1>(a, s);
+  // as many token fragments as one expert can need, two at most (then in passes)
+  if (a.w_dt == DT_F32) return a.T > 16 ? launch<FMT_F32, 2, 2>(a, s) : launch<FMT_F32, 1, 1>(a, s);
+  if (a.w_dt == DT_BF16)
+    return a.T > 16 ? launch<FMT_BF16, 2, 2>(a, s) : a.T > 8 ? launch<FMT_BF16, 1, 2>(a, s) : launch<FMT_BF16, 1, 1>(a, s);
+  return a.T > 16 ? launch<FMT_FP8X, 2, 2>(a, s) : a.T > 8 ? launch<FMT_FP8X, 1, 2>(a, s) : launch<FMT_FP8X, 1, 1>(a, s);
 }
 
 }  // namespace ox

@@ -340,7 +340,7 @@ int launch_rmsnorm(const NormArgs& a, void* stream);
 int launch_quantize_i8(const NormArgs& a, void* stream);
 
 // A routed feed-forward layer of a few tokens.
-constexpr int kMoeTokens = 64, kMoeTop = 16, kMoeExperts = 512, kMoeWidth = 1 << 24;   // the most of each
+constexpr int kMoeTokens = 64, kMoeTop = 16, kMoeExperts = 512, kMoeWidth = 1 << 22;   // the most of each
 struct MoeArgs {
   int T, D, H, E, top;     // tokens, their width, the experts' hidden width, experts, experts of a token
   int w_dt;                // W1, W2: DT_F32, DT_BF16 (X, biases and Y too) or DT_F8 (those bf16)

@@ -524,7 +524,7 @@ ox_status ox_gemm_grouped_fp8(ox_dtype y_type, int64_t T, int64_t N, int64_t K, 
  * none), weights: DEVICE fp32 [T, top]; either may be NULL.
  * Sums are fp32, and Y is rounded once (h passes in 16 bits of significand for
  * bf16); their order depends on the sizes and on the routing alone.
- * T <= 64, E <= 512, top <= 16, D and H <= 2^24 (OX_ERR_UNSUPPORTED above; ox_gemm_grouped takes
+ * T <= 64, E <= 512, top <= 16, D and H <= 2^22 (OX_ERR_UNSUPPORTED above; ox_gemm_grouped takes
  * any number of rows).  T = 0 or D = 0 enqueue nothing.
  * workspace: DEVICE, 16-byte aligned, at least ox_moe_few_workspace_bytes(T, D,
  * H, E, top) bytes (0 for sizes that the call refuses); its contents on entry do
