@@ -12,8 +12,8 @@
 // routing alone.
 //
 // Every block of the first kernel routes all tokens for itself (a launch and a
-// trip to memory less than a kernel of its own); its first block leaves the
-// result for the second kernel, the slots (token, expert) ordered by expert.
+// trip to memory less than a kernel of its own); its last block does nothing else
+// and leaves the result for the second kernel.
 // The second kernel's K is the experts' hidden rows one after the other; it is
 // cut into equal ranges whatever the routing.  Blocks that share columns leave
 // fp32 sums, and the last of them to arrive adds them in order.
@@ -43,22 +43,16 @@ __device__ __forceinline__ float moe_act(int act, float v) {
 
 // ------------------------------------------------------------- routing --
 
-// What the routing finds, in a block's shared memory.
+// What every block finds for itself: the tokens of each expert, as bits.
 struct Route {
-  uint64_t mask[kMoeExperts];       // the tokens of each expert
-  uint16_t first[kMoeExperts];      // an expert's first slot
-  uint16_t act[kMoeExperts];        // the experts that have tokens, in order
-  uint16_t off[kMoeExperts + 1];    // their slots
-  int16_t choice[kMoeTokens][kMoeTop];
-  float weight[kMoeTokens][kMoeTop];
-  uint8_t tok[kPairs];              // the token of each slot
-  int nact, slots;
+  uint64_t mask[kMoeExperts];
 };
 
-// The same for the second kernel, in the workspace.
+// What the first kernel's last block leaves for the second, in the workspace:
+// the slots (token, expert) in the order of the experts.
 struct RouteOut {
   int nact, slots;
-  int act[kMoeExperts], off[kMoeExperts + 1];
+  int act[kMoeExperts], off[kMoeExperts + 1];      // the experts that have tokens, and their first slots
   int tok[kPairs];
   float weight[kPairs];
 };
@@ -73,147 +67,183 @@ __device__ __forceinline__ float key_score(uint32_t k) {
   return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
 }
 
-__device__ __forceinline__ uint32_t row16_max(uint32_t m) {
-  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xf, 0xf, true));
-  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xf, 0xf, true));
-  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xf, 0xf, true));
-  return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xf, 0xf, true));
+// over the sixteen lanes of a row, in every lane (quad_perm 1,0,3,2 and 2,3,0,1,
+// then the mirrored half row and row)
+template <typename F>
+__device__ __forceinline__ uint32_t row16(uint32_t v, F&& f) {
+  v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xf, 0xf, true));
+  v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xf, 0xf, true));
+  v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));
+  return f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true));
 }
-__device__ __forceinline__ uint32_t all_max(uint32_t m) {
-  m = row16_max(m);
-  const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)m, 0), (uint32_t)__builtin_amdgcn_readlane((int)m, 16));
-  const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)m, 32), (uint32_t)__builtin_amdgcn_readlane((int)m, 48));
-  return max(a, b);
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+  return row16(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
-__device__ __forceinline__ float all_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-  return v;
+__device__ __forceinline__ uint32_t row16_min(uint32_t v) {
+  return row16(v, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+__device__ __forceinline__ float row16_sum(float v) {
+  return __uint_as_float(row16(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
 }
 
-// B tokens of a wave at a time (their loads together), PL scores of each a lane.
-template <int PL, int B>
-__device__ __forceinline__ void route_tokens(const MoeArgs& a, Route& rt, bool weights) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (int t0 = wave; t0 < a.T; t0 += kMoeWaves * B) {
-    uint32_t key[B][PL];
+// Sixteen lanes take a token, with PL scores each: its best expert is found
+// `top` times, and lane j of the sixteen keeps the j-th.  A wave does four tokens
+// at once (one token a wave, over all lanes, took 12 us for 64 tokens and 8 of 64
+// experts).  WEIGHTS: the block that writes what comes of it.
+template <int PL, bool WEIGHTS>
+__device__ __forceinline__ void route_tokens(const MoeArgs& a, Route& rt, int16_t* choice, float* weight) {
+  const int r = threadIdx.x & 15;
+  for (int t0 = 0; t0 < a.T; t0 += kMoeThreads / 16) {
+    const int t = t0 + threadIdx.x / 16;
+    const bool in = t < a.T;
+    uint32_t key[PL];
 #pragma unroll
-    for (int b = 0; b < B; ++b)
+    for (int i = 0; i < PL; ++i) {
+      const int e = i * 16 + r;
+      key[i] = 0u;
+      if (in && e < a.E) {
+        const int64_t at = (int64_t)t * a.E + e;
+        key[i] = score_key(a.scores_dt == DT_F32 ? ((const float*)a.scores)[at] : bf16_to_f32(((const uint16_t*)a.scores)[at]));
+      }
+    }
+    if (t0 == 0) {      // (under the first loads)
+      for (int e = threadIdx.x; e < a.E; e += kMoeThreads) rt.mask[e] = 0;
+      __syncthreads();
+    }
+    uint32_t mine = 0u, best = 0u;
+    int expert = -1;
+    float all = 0.0f;
+#pragma unroll 1
+    for (int j = 0; j < a.top; ++j) {
+      uint32_t m = key[0];
 #pragma unroll
-      for (int i = 0; i < PL; ++i) {
-        const int t = min(t0 + b * kMoeWaves, a.T - 1), e = i * 64 + lane;
-        const int64_t at = (int64_t)t * a.E + min(e, a.E - 1);
-        const float s = a.scores_dt == DT_F32 ? ((const float*)a.scores)[at] : bf16_to_f32(((const uint16_t*)a.scores)[at]);
-        key[b][i] = e < a.E ? score_key(s) : 0u;
+      for (int i = 1; i < PL; ++i) m = max(m, key[i]);
+      m = row16_max(m);
+      // the lowest of the experts that have it
+      uint32_t e = 0xffffu;
+#pragma unroll
+      for (int i = PL - 1; i >= 0; --i) e = key[i] == m ? i * 16 + r : e;
+      e = row16_min(e);
+      if (j == 0) {
+        best = m;
+        if (WEIGHTS && !a.renormalise) {
+#pragma unroll 1
+          for (int i = 0; i < PL; ++i) all += key[i] ? expf(key_score(key[i]) - key_score(best)) : 0.0f;
+          all = row16_sum(all);
+        }
+      }
+      if (r == j && m) {
+        mine = m;
+        expert = (int)e;
       }
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int t = t0 + b * kMoeWaves;
-      if (t >= a.T) break;
-      float all = 0.0f, top = 0.0f;
-      uint32_t mine = 0u;
-      int expert = -1;
-      for (int j = 0; j < a.top; ++j) {
-        uint32_t m = key[b][0];
-#pragma unroll
-        for (int i = 1; i < PL; ++i) m = max(m, key[b][i]);
-        m = all_max(m);
-        if (m == 0u) break;
-        // the lowest of the experts that have it
-        int e = -1;
-#pragma unroll
-        for (int i = 0; i < PL; ++i) {
-          const uint64_t has = __ballot(key[b][i] == m);
-          if (e < 0 && has) e = i * 64 + __ffsll((unsigned long long)has) - 1;
-        }
-        if (j == 0) {
-          top = key_score(m);
-          if (weights && !a.renormalise) {
-#pragma unroll
-            for (int i = 0; i < PL; ++i) all += key[b][i] ? expf(key_score(key[b][i]) - top) : 0.0f;
-            all = all_sum(all);
-          }
-        }
-        if (lane == j) {
-          mine = m;
-          expert = e;
-        }
-#pragma unroll
-        for (int i = 0; i < PL; ++i)
-          if (i * 64 + lane == e) key[b][i] = 0u;
-      }
-      if (lane < a.top) {
-        rt.choice[t][lane] = (int16_t)expert;
-        if (expert >= 0) atomicOr((unsigned long long*)&rt.mask[expert], 1ull << t);
-      }
-      if (weights) {
-        const float p = mine ? expf(key_score(mine) - top) : 0.0f;
-        if (a.renormalise) all = all_sum(p);
-        if (lane < a.top) rt.weight[t][lane] = mine ? p / all : 0.0f;
+      for (int i = 0; i < PL; ++i) key[i] = (uint32_t)(i * 16 + r) == e ? 0u : key[i];
+    }
+    if (in && expert >= 0) atomicOr((unsigned long long*)&rt.mask[expert], 1ull << t);
+    if constexpr (WEIGHTS) {
+      const float p = mine ? expf(key_score(mine) - key_score(best)) : 0.0f;
+      if (a.renormalise) all = row16_sum(p);
+      if (in && r < a.top) {
+        choice[t * kMoeTop + r] = (int16_t)expert;
+        weight[t * kMoeTop + r] = mine ? p / all : 0.0f;
       }
     }
   }
+  __syncthreads();
+}
+template <bool WEIGHTS>
+__device__ __forceinline__ void route(const MoeArgs& a, Route& rt, int16_t* choice = nullptr, float* weight = nullptr) {
+  if (a.E <= 16) route_tokens<1, WEIGHTS>(a, rt, choice, weight);
+  else if (a.E <= 64) route_tokens<4, WEIGHTS>(a, rt, choice, weight);
+  else if (a.E <= 128) route_tokens<8, WEIGHTS>(a, rt, choice, weight);
+  else route_tokens<32, WEIGHTS>(a, rt, choice, weight);
 }
 
-// Fills rt; with `out`, the block also writes what the second kernel and the
-// caller read, and clears the counters.
-__device__ __forceinline__ void route(const MoeArgs& a, Route& rt, bool out) {
-  for (int e = threadIdx.x; e < a.E; e += kMoeThreads) rt.mask[e] = 0;
-  __syncthreads();
-  if (a.E <= 64) route_tokens<1, 8>(a, rt, out);
-  else if (a.E <= 128) route_tokens<2, 4>(a, rt, out);
-  else if (a.E <= 256) route_tokens<4, 2>(a, rt, out);
-  else route_tokens<8, 1>(a, rt, out);
-  __syncthreads();
+// Experts that have tokens.
+__device__ __forceinline__ int active_experts(const MoeArgs& a, const Route& rt) {
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+  for (int base = 0; base < a.E; base += 64) n += __popcll(__ballot(base + lane < a.E && rt.mask[min(base + lane, a.E - 1)]));
+  return n;
+}
+// The ai-th of them: its index, first slot, and tokens (a wave's work).
+struct Active {
+  int e, first;
+  uint64_t mask;
+};
+__device__ __forceinline__ Active find_active(const MoeArgs& a, const Route& rt, int ai) {
+  const int lane = threadIdx.x & 63;
+  Active r = {0, 0, 0};
+  for (int base = 0; base < a.E; base += 64) {
+    const uint64_t m = base + lane < a.E ? rt.mask[base + lane] : 0;
+    const uint64_t has = __ballot(m != 0);
+    const int n = __popcll(m), s = wave_scan(n);
+    if (ai < __popcll(has)) {
+      // the lane whose bit is the ai-th
+      const uint64_t at = __ballot(m != 0 && (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(has >> 32),
+                                                                           __builtin_amdgcn_mbcnt_lo((uint32_t)has, 0)) == ai);
+      const int l = __ffsll((unsigned long long)at) - 1;
+      r.e = base + l;
+      r.first += __builtin_amdgcn_readlane(s - n, l);
+      r.mask = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)m, l) |
+               (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(m >> 32), l) << 32;
+      return r;
+    }
+    ai -= __popcll(has);
+    r.first += __builtin_amdgcn_readlane(s, 63);
+  }
+  return r;
+}
+// Lane i gets the i-th token of the mask.
+__device__ __forceinline__ int tokens_of(uint64_t mask) {
+  const int lane = threadIdx.x & 63;
+  const int before = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+  const bool has = (mask >> lane) & 1;
+  return __builtin_amdgcn_ds_permute(4 * (has ? before : __popcll(mask) + lane - before), lane);
+}
+
+// The first kernel's last block: what the second kernel and the caller read.
+__device__ __forceinline__ void write_route(const MoeArgs& a, Route& rt, char* smem) {
+  float* weight = (float*)smem;                                        // [kMoeTokens][kMoeTop]
+  int16_t* choice = (int16_t*)(smem + kPairs * 4);
+  uint16_t* first = (uint16_t*)(smem + kPairs * 6);                    // [kMoeExperts]: an expert's first slot
+  route<true>(a, rt, choice, weight);
+  RouteOut* ro = (RouteOut*)a.route;
   if (threadIdx.x < 64) {
     const int lane = threadIdx.x;
     int acts = 0, slots = 0;
     for (int base = 0; base < a.E; base += 64) {
-      const int e = base + lane;
-      const int n = e < a.E ? __popcll(rt.mask[e]) : 0;
+      const int e = base + lane, n = e < a.E ? __popcll(rt.mask[e]) : 0;
       const int s = wave_scan(n), k = wave_scan(n ? 1 : 0);
-      if (e < a.E) rt.first[e] = (uint16_t)(slots + s - n);
+      if (e < a.E) first[e] = (uint16_t)(slots + s - n);
       if (n) {
-        rt.act[acts + k - 1] = (uint16_t)e;
-        rt.off[acts + k - 1] = (uint16_t)(slots + s - n);
+        ro->act[acts + k - 1] = e;
+        ro->off[acts + k - 1] = slots + s - n;
       }
       slots += __builtin_amdgcn_readlane(s, 63);
       acts += __builtin_amdgcn_readlane(k, 63);
     }
     if (lane == 0) {
-      rt.off[acts] = (uint16_t)slots;
-      rt.nact = acts;
-      rt.slots = slots;
+      ro->off[acts] = slots;
+      ro->nact = acts;
+      ro->slots = slots;
     }
   }
   __syncthreads();
-  RouteOut* ro = (RouteOut*)a.route;
   for (int p = threadIdx.x; p < a.T * a.top; p += kMoeThreads) {
-    const int t = p / a.top, j = p - t * a.top, e = rt.choice[t][j];
+    const int t = p / a.top, j = p - t * a.top, e = choice[t * kMoeTop + j];
+    const float w = weight[t * kMoeTop + j];
     if (e >= 0) {
-      const int slot = rt.first[e] + __popcll(rt.mask[e] & ((1ull << t) - 1));
-      rt.tok[slot] = (uint8_t)t;
-      if (out) {
-        ro->tok[slot] = t;
-        ro->weight[slot] = rt.weight[t][j];
-      }
+      const int slot = first[e] + __popcll(rt.mask[e] & ((1ull << t) - 1));
+      ro->tok[slot] = t;
+      ro->weight[slot] = w;
     }
-    if (out && a.experts) a.experts[p] = e;
-    if (out && a.weights) a.weights[p] = rt.weight[t][j];
+    if (a.experts) a.experts[p] = e;
+    if (a.weights) a.weights[p] = w;
   }
-  if (out) {
-    for (int i = threadIdx.x; i <= rt.nact; i += kMoeThreads) {
-      if (i < rt.nact) ro->act[i] = rt.act[i];
-      ro->off[i] = rt.off[i];
-    }
-    if (threadIdx.x == 0) {
-      ro->nact = rt.nact;
-      ro->slots = rt.slots;
-    }
-    for (int i = threadIdx.x; i < a.tiles; i += kMoeThreads) a.counters[i] = 0;
-  }
-  __syncthreads();
+  for (int i = threadIdx.x; i < a.tiles; i += kMoeThreads) a.counters[i] = 0;
 }
 
 // ------------------------------------------------------------ products --
@@ -388,11 +418,16 @@ struct MoeProduct {
         if (k + u < whole) multiply(st[u], acc);
       k = max(k, whole);
     }
-#pragma unroll 1
-    for (; k < whole; ++k) {
-      Step st;
-      load<false>(k, st);
-      multiply(st, acc);
+    if (k < whole) {      // fewer than U in all: their loads together
+      Step st[U];
+#pragma unroll
+      for (int u = 0; u + 1 < U; ++u)
+        if (k + u < whole) load<false>(k + u, st[u]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u + 1 < U; ++u)
+        if (k + u < whole) multiply(st[u], acc);
+      k = whole;
     }
     if (k < k1) {
       Step st;
@@ -436,21 +471,17 @@ __device__ __forceinline__ f32x4_t load_shared(const f32x4_t* p) {
   return v;
 }
 
-// Four consecutive hidden values of a slot, as the second kernel reads them.
+// A hidden value of a slot, as the second kernel reads it.
 template <int FMT>
-__device__ __forceinline__ void store_hidden(const MoeArgs& a, int slot, int n, const float (&h)[4]) {
+__device__ __forceinline__ void store_hidden(const MoeArgs& a, int slot, int n, float h) {
   if constexpr (FMT == FMT_F32) {
-    *(f32x4_t*)((float*)a.hidden + (int64_t)slot * a.ldh + n) = f32x4_t{h[0], h[1], h[2], h[3]};
+    ((float*)a.hidden)[(int64_t)slot * a.ldh + n] = h;
   } else {
-    float hi[4], lo[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      hi[r] = bf16_to_f32((uint16_t)pack_bf16x2(h[r], 0.0f));
-      lo[r] = __builtin_isfinite(hi[r]) ? h[r] - hi[r] : 0.0f;
-    }
+    const uint16_t hi = (uint16_t)pack_bf16x2(h, 0.0f);
+    const float v = bf16_to_f32(hi), lo = __builtin_isfinite(v) ? h - v : 0.0f;
     uint16_t* p = (uint16_t*)a.hidden + (int64_t)slot * 2 * a.ldh + n;      // the two parts in turn
-    *(u32x2_t*)p = u32x2_t{pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
-    *(u32x2_t*)(p + a.ldh) = u32x2_t{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3])};
+    p[0] = hi;
+    p[a.ldh] = (uint16_t)pack_bf16x2(lo, 0.0f);
   }
 }
 template <int FMT>
@@ -458,14 +489,20 @@ __device__ __forceinline__ float value_at(const void* p, int64_t at) {
   return FMT == FMT_F32 ? ((const float*)p)[at] : bf16_to_f32(((const uint16_t*)p)[at]);
 }
 
-// Units of one expert x a group of column tiles, in turn over the grid's blocks.
-// A column tile is 16 gate rows and the 16 up rows beside them, or 32 rows.
+// Units of one expert x a group of column tiles, in turn over the grid's blocks
+// (the last of them routes for the second kernel instead).  A column tile is 16
+// gate rows and the 16 up rows beside them, or 32 rows.
 template <int FMT, int MF, bool ONE>
 __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(const MoeArgs a) {
   typedef MoeProduct<FMT, MF, ONE> MP;
+  constexpr int LANE = 4, SET = 64 * LANE + 48;      // floats: a lane's results, a fragment's (16 apart every 16 lanes: all banks)
   __shared__ Route rt;
-  __shared__ f32x4_t part[2][kMoeWaves][2 * MF][64];
-  route(a, rt, blockIdx.x == 0);
+  __shared__ __attribute__((aligned(16))) float part[2][kMoeWaves][2 * MF * SET];
+  if (blockIdx.x == gridDim.x - 1) {
+    write_route(a, rt, (char*)part);
+    return;
+  }
+  route<false>(a, rt);
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wide = a.gated ? 2 * a.H : a.H, per = a.gated ? 16 : 32, tiles = ceil_div(a.H, per);
@@ -473,69 +510,68 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(const MoeArgs a)
   const int SPL = a.slices, CT = kMoeWaves / SPL, groups = ceil_div(tiles, CT);
   const int ct = __builtin_amdgcn_readfirstlane(wave / SPL), sl = wave - ct * SPL;
   const int k0 = (int)((int64_t)nk * sl / SPL), k1 = (int)((int64_t)nk * (sl + 1) / SPL);
+  const int units = active_experts(a, rt) * groups;
   int turn = 0;
-  for (int unit = blockIdx.x; unit < rt.nact * groups; unit += gridDim.x) {
-    const int ai = unit / groups, tile = (unit - ai * groups) * CT + ct, n0 = tile * per;
-    const int e = __builtin_amdgcn_readfirstlane(rt.act[ai]), lo = __builtin_amdgcn_readfirstlane(rt.off[ai]);
-    const int hi = __builtin_amdgcn_readfirstlane(rt.off[ai + 1]);
+  for (int unit = blockIdx.x; unit < units; unit += gridDim.x - 1) {
+    const int ai = __builtin_amdgcn_readfirstlane(unit / groups), tile0 = (unit - ai * groups) * CT;
+    const Active ac = find_active(a, rt, ai);
+    const int e = ac.e, count = __popcll(ac.mask), tile = tile0 + ct, n0 = tile * per;
+    const int tok = tokens_of(ac.mask);
     const bool live = tile < tiles;      // whole waves; the barriers below are passed by all
     MP mp;
     mp.K = a.D;
+    mp.x = uniform_global(a.X);
     if (live) {
       mp.weights(0, a.W1, a.s1, e, wide, n0, a.H);
       if (a.gated) mp.weights(1, a.W1, a.s1, e, wide, a.H + n0, wide);
       else mp.weights(1, a.W1, a.s1, e, wide, min(n0 + 16, a.H - 1), a.H);
     }
-    for (int s0 = lo; s0 < hi; s0 += 16 * MF, turn ^= 1) {
+    for (int s0 = 0; s0 < count; s0 += 16 * MF, turn ^= 1) {
       f32x4_t acc[2][MF];
 #pragma unroll
       for (int f = 0; f < 2; ++f)
 #pragma unroll
         for (int m = 0; m < MF; ++m) acc[f][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      if (live) {
-        mp.frags = ceil_div(hi - s0, 16);
-        mp.x = uniform_global(a.X);
+      mp.frags = ceil_div(count - s0, 16);
 #pragma unroll
-        for (int m = 0; m < MF; ++m) mp.token(m, rt.tok[min(s0 + m * 16 + i, hi - 1)], a.D * (FMT == FMT_F32 ? 4 : 2));
-        mp.run(k0, k1, acc);
-      }
-      if (SPL > 1) {
+      for (int m = 0; m < MF; ++m)
+        mp.token(m, __builtin_amdgcn_ds_bpermute(4 * min(s0 + m * 16 + i, count - 1), tok), a.D * (FMT == FMT_F32 ? 4 : 2));
+      if (live) mp.run(k0, k1, acc);
+      float* to = part[turn][wave] + lane * LANE + g * 16;
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+      for (int f = 0; f < 2; ++f)
 #pragma unroll
-          for (int m = 0; m < MF; ++m) part[turn][wave][f * MF + m][lane] = acc[f][m];
-        __syncthreads();
-        if (sl != 0) continue;
-        for (int q = 1; q < SPL; ++q)
-#pragma unroll
-          for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int m = 0; m < MF; ++m) acc[f][m] = add4(acc[f][m], part[turn][wave + q][f * MF + m][lane]);
-      }
-      if (!live) continue;
-#pragma unroll
-      for (int m = 0; m < MF; ++m) {
-        const int slot = s0 + m * 16 + i;
-        if (slot >= hi) continue;
-        float v[2][4];
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int n = n0 + g * 4 + r + (a.gated ? 0 : f * 16);
-            v[f][r] = acc[f][m][r];
-            if (a.b1 && n < a.H) v[f][r] += value_at<FMT>(a.b1, (int64_t)e * wide + n + (a.gated ? f * a.H : 0));
-          }
-        float h[2][4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          h[0][r] = moe_act(a.act, v[0][r]);
-          if (a.gated) h[0][r] *= v[1][r];
-          else h[1][r] = moe_act(a.act, v[1][r]);
+        for (int m = 0; m < MF; ++m) *(f32x4_t*)(to + (f * MF + m) * SET) = acc[f][m];
+      __syncthreads();
+      // Every wave: four tokens x 16 columns of a tile, from the slices' sums in
+      // their order.  A wave may be a pass ahead of one that still reads, no more:
+      // two sets in turn.
+      const int quads = (min(count - s0, 16 * MF) + 3) / 4;
+#pragma unroll 1
+      for (int w = wave; w < CT * quads; w += kMoeWaves) {
+        const int c = w / quads, q = w - c * quads, t = q * 4 + g, col = i;
+        const int at = ((col >> 2) * 16 + (t & 15)) * LANE + (col >> 2) * 16 + (col & 3) + (t >> 4) * SET;
+        float v[2] = {0.0f, 0.0f};
+        for (int x = 0; x < SPL; ++x) {
+          v[0] += part[turn][c * SPL + x][at];
+          v[1] += part[turn][c * SPL + x][at + MF * SET];
         }
-        // (the rows of `hidden` are padded to whole steps: no partial store)
-        if (n0 + g * 4 < a.H) store_hidden<FMT>(a, slot, n0 + g * 4, h[0]);
-        if (!a.gated && n0 + 16 + g * 4 < a.H) store_hidden<FMT>(a, slot, n0 + 16 + g * 4, h[1]);
+        const int slot = s0 + t, n = (tile0 + c) * per + col;
+        if (slot >= count || n >= a.H) continue;
+        if (a.gated) {
+          if (a.b1) {
+            v[0] += value_at<FMT>(a.b1, (int64_t)e * wide + n);
+            v[1] += value_at<FMT>(a.b1, (int64_t)e * wide + a.H + n);
+          }
+          store_hidden<FMT>(a, ac.first + slot, n, moe_act(a.act, v[0]) * v[1]);
+        } else {
+#pragma unroll 1
+          for (int f = 0; f < 2; ++f) {
+            if (n + f * 16 >= a.H) break;
+            const float b = a.b1 ? value_at<FMT>(a.b1, (int64_t)e * wide + n + f * 16) : 0.0f;
+            store_hidden<FMT>(a, ac.first + slot, n + f * 16, moe_act(a.act, (f ? v[1] : v[0]) + b));
+          }
+        }
       }
     }
   }
@@ -566,7 +602,7 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_down_kernel(const MoeArgs 
   }
   if (threadIdx.x == 0) rt.nact = ro->nact;
   float* mine = yw + wave * a.T * 32;
-  for (int p = lane; p < a.T * 32; p += 64) mine[p] = 0.0f;
+  for (int p = lane; p < a.T * 8; p += 64) ((f32x4_t*)mine)[p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   __syncthreads();
 
   const int tile = blockIdx.x / a.S, s = blockIdx.x - tile * a.S, n0 = tile * 32;
@@ -690,11 +726,11 @@ constexpr int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
 
-// Ranges of K that the second kernel's tiles are cut into: about two blocks for
-// every CU.
+// Ranges of K that the second kernel's tiles are cut into: about one block for
+// every CU (two: one token 23.3 us, 21.7 with one; the others equal).
 static int moe_ranges(int64_t D) {
   const int64_t tiles = (D + 31) / 32;
-  const int64_t s = (2 * kCus + tiles - 1) / tiles;
+  const int64_t s = (kCus + tiles - 1) / tiles;
   return (int)(s < 1 ? 1 : s);
 }
 
@@ -737,7 +773,7 @@ int launch_moe(MoeArgs& a, void* workspace, void* stream) {
   a.slices = 1;
   while (a.slices < kMoeWaves && a.slices < nk) a.slices *= 2;
   const int64_t units = experts * ceil_div(ceil_div(a.H, a.gated ? 16 : 32), kMoeWaves / a.slices);
-  a.up_blocks = (int)(units < 1 ? 1 : units < 2 * kCus ? units : 2 * kCus);
+  a.up_blocks = 1 + (int)(units < 2 * kCus ? units : 2 * kCus);
   // as many token fragments as one expert can need, two at most (then in passes)
   if (a.w_dt == DT_F32) return a.T > 16 ? launch<FMT_F32, 2, 2>(a, s) : launch<FMT_F32, 1, 1>(a, s);
   if (a.w_dt == DT_BF16)
