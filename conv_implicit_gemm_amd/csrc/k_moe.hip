@@ -282,7 +282,7 @@ __device__ __forceinline__ u32x4_t part_of_piece(Global p, int n) {
 // Two fragments of 16 rows of weights times MF fragments of 16 tokens, over steps
 // [k0, k1) of K (128 bytes of a weight row each).
 // ONE: a fragment's sixteen rows of weights share a scale (e4m3).
-template <int FMT, int MF, bool ONE>
+template <int FMT, int MF, bool ONE, int BUDGET>
 struct MoeProduct {
   typedef FmtOps<FMT> Mm;
   typedef typename Mm::Frag Frag;
@@ -290,9 +290,10 @@ struct MoeProduct {
   static constexpr int KE = 128 / Mm::ESZ;         // K of a step
   static constexpr int XP = F8 ? 4 : 2;            // pieces of a token's step
   static constexpr int XB = F8 ? 256 : 128;        // its bytes
-  // Steps in flight, as many as 128 registers hold (16 waves a CU).
+  // Steps in flight, as many as BUDGET registers hold.
   static constexpr int REGS = 16 + MF * XP * 4 + (F8 ? ONE ? 0 : 8 : 0);
-  static constexpr int U = REGS <= 24 ? 3 : REGS <= 40 ? 2 : 1;
+  static constexpr int U = BUDGET / REGS;
+  static_assert(U >= 1, "a step fits");
 
   // Bases for all lanes, and this lane's offsets from them (its row, its first
   // piece): a load is a scalar base, a 32-bit offset and a constant.
@@ -384,24 +385,29 @@ struct MoeProduct {
       }
     }
   }
-  __device__ __forceinline__ void run(int first, int end, f32x4_t (&acc)[2][MF]) const {
+  // All steps [first, end).  They are taken in turn from an eighth of the way that
+  // `phase` gives: waves that all begin with a row's first bytes, and rows that
+  // are a power of two apart, would keep asking the same few memory channels.
+  __device__ __forceinline__ void run(int first, int end, int phase, f32x4_t (&acc)[2][MF]) const {
     const int k0 = __builtin_amdgcn_readfirstlane(first), k1 = __builtin_amdgcn_readfirstlane(end);
     if (K == 0) return;
     const int whole = min(k1, K / KE);      // steps that K does not end inside
+    const int turned = __builtin_amdgcn_readfirstlane(max(0, whole - k0) * phase / 8);
+    auto at = [&](int j) { return j + turned < whole ? j + turned : j + turned - (whole - k0); };
     int k = k0;
     if (k + U <= whole) {
       // U steps in flight: each is loaded again, U further on, as soon as it is
       // multiplied (the order is pinned: loads would sink to their uses)
       Step st[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) load<false>(k + u, st[u]);
+      for (int u = 0; u < U; ++u) load<false>(at(k + u), st[u]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll 1
       for (; k + 2 * U <= whole; k += U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           multiply(st[u], acc);
-          load<false>(k + U + u, st[u]);
+          load<false>(at(k + U + u), st[u]);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -409,7 +415,7 @@ struct MoeProduct {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         multiply(st[u], acc);
-        if (u + 1 < U && k + U + u < whole) load<false>(k + U + u, st[u]);
+        if (u + 1 < U && k + U + u < whole) load<false>(at(k + U + u), st[u]);
         __builtin_amdgcn_sched_barrier(0);
       }
       k += U;
@@ -422,7 +428,7 @@ struct MoeProduct {
       Step st[U];
 #pragma unroll
       for (int u = 0; u + 1 < U; ++u)
-        if (k + u < whole) load<false>(k + u, st[u]);
+        if (k + u < whole) load<false>(at(k + u), st[u]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int u = 0; u + 1 < U; ++u)
@@ -494,7 +500,7 @@ __device__ __forceinline__ float value_at(const void* p, int64_t at) {
 // gate rows and the 16 up rows beside them, or 32 rows.
 template <int FMT, int MF, bool ONE>
 __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(const MoeArgs a) {
-  typedef MoeProduct<FMT, MF, ONE> MP;
+  typedef MoeProduct<FMT, MF, ONE, 80> MP;
   constexpr int LANE = 4, SET = 64 * LANE + 48;      // floats: a lane's results, a fragment's (16 apart every 16 lanes: all banks)
   __shared__ Route rt;
   __shared__ __attribute__((aligned(16))) float part[2][kMoeWaves][2 * MF * SET];
@@ -507,12 +513,16 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(const MoeArgs a)
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wide = a.gated ? 2 * a.H : a.H, per = a.gated ? 16 : 32, tiles = ceil_div(a.H, per);
   const int nk = ceil_div(a.D, MP::KE);
-  const int SPL = a.slices, CT = kMoeWaves / SPL, groups = ceil_div(tiles, CT);
+  // Slices of K: as few as still give every block two units (64 experts of 1024 x
+  // 2048, 4096 tiles: 188 us with two slices, 195 with eight, 208 with one)
+  const int experts = active_experts(a, rt), blocks = gridDim.x - 1;
+  int SPL = 1;
+  while (SPL < a.slices && experts * ceil_div(tiles, kMoeWaves / SPL) < 2 * blocks) SPL *= 2;
+  const int CT = kMoeWaves / SPL, groups = ceil_div(tiles, CT), units = experts * groups;
   const int ct = __builtin_amdgcn_readfirstlane(wave / SPL), sl = wave - ct * SPL;
   const int k0 = (int)((int64_t)nk * sl / SPL), k1 = (int)((int64_t)nk * (sl + 1) / SPL);
-  const int units = active_experts(a, rt) * groups;
   int turn = 0;
-  for (int unit = blockIdx.x; unit < units; unit += gridDim.x - 1) {
+  for (int unit = blockIdx.x; unit < units; unit += blocks) {
     const int ai = __builtin_amdgcn_readfirstlane(unit / groups), tile0 = (unit - ai * groups) * CT;
     const Active ac = find_active(a, rt, ai);
     const int e = ac.e, count = __popcll(ac.mask), tile = tile0 + ct, n0 = tile * per;
@@ -536,7 +546,7 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(const MoeArgs a)
 #pragma unroll
       for (int m = 0; m < MF; ++m)
         mp.token(m, __builtin_amdgcn_ds_bpermute(4 * min(s0 + m * 16 + i, count - 1), tok), a.D * (FMT == FMT_F32 ? 4 : 2));
-      if (live) mp.run(k0, k1, acc);
+      if (live) mp.run(k0, k1, (blockIdx.x + ct) & 7, acc);
       float* to = part[turn][wave] + lane * LANE + g * 16;
 #pragma unroll
       for (int f = 0; f < 2; ++f)
@@ -581,9 +591,9 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(const MoeArgs a)
 // experts' hidden rows.  A hidden row's two parts lie in neighbouring columns of
 // a token fragment, which holds eight slots then, and their sums are added.
 template <int FMT, int MF>
-__global__ __launch_bounds__(kMoeThreads, 4) void moe_down_kernel(const MoeArgs a) {
+__global__ __launch_bounds__(kMoeThreads, 2) void moe_down_kernel(const MoeArgs a) {
   constexpr int PARTS = FMT == FMT_F32 ? 1 : 2, SLOTS = 16 / PARTS;      // of a hidden row; of a fragment
-  typedef MoeProduct<FMT, MF, true> MP;
+  typedef MoeProduct<FMT, MF, true, 160> MP;
   extern __shared__ __attribute__((aligned(16))) float yw[];      // [waves][T][32]
   __shared__ RouteOut rt;
   __shared__ int last;
@@ -629,7 +639,7 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_down_kernel(const MoeArgs 
 #pragma unroll
       for (int m = 0; m < MF; ++m)
         mp.token(m, (min(s0 + m * SLOTS + i / PARTS, hi - 1) - lo) * PARTS + i % PARTS, (uint32_t)a.ldh * (4 / PARTS));
-      mp.run(k0, k1, acc);
+      mp.run(k0, k1, (blockIdx.x + wave) & 7, acc);
       // into this wave's sums of the tokens (a token has one slot of an expert)
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
@@ -774,10 +784,12 @@ int launch_moe(MoeArgs& a, void* workspace, void* stream) {
   while (a.slices < kMoeWaves && a.slices < nk) a.slices *= 2;
   const int64_t units = experts * ceil_div(ceil_div(a.H, a.gated ? 16 : 32), kMoeWaves / a.slices);
   a.up_blocks = 1 + (int)(units < 2 * kCus ? units : 2 * kCus);
-  // as many token fragments as one expert can need, two at most (then in passes)
+  // As many token fragments as one expert can need, two at most (then in passes),
+  // four in the second kernel for bf16 (64 tokens over 4 experts of 4096 x 2048:
+  // 95 us, 102 with two; e4m3 spills with four)
   if (a.w_dt == DT_F32) return a.T > 16 ? launch<FMT_F32, 2, 2>(a, s) : launch<FMT_F32, 1, 1>(a, s);
   if (a.w_dt == DT_BF16)
-    return a.T > 16 ? launch<FMT_BF16, 2, 2>(a, s) : a.T > 8 ? launch<FMT_BF16, 1, 2>(a, s) : launch<FMT_BF16, 1, 1>(a, s);
+    return a.T > 16 ? launch<FMT_BF16, 2, 4>(a, s) : a.T > 8 ? launch<FMT_BF16, 1, 2>(a, s) : launch<FMT_BF16, 1, 1>(a, s);
   return a.T > 16 ? launch<FMT_FP8X, 2, 2>(a, s) : a.T > 8 ? launch<FMT_FP8X, 1, 2>(a, s) : launch<FMT_FP8X, 1, 1>(a, s);
 }
 
