@@ -1105,7 +1105,6 @@ ox_status expert_call(const char* fn, int dt, ox_dtype y_type, int64_t T, int64_
   // (tile offsets: up to 256 rows of K, or 64 rows of N)
   a.vec = aligned16(A) && aligned16(B) && rowb % 16 == 0 && rowb < (1 << 23) &&
           (transB || (colb % 16 == 0 && colb < (1 << 23)));
-  a.y_vec = aligned16(Y) && N * esize(y_type) % 16 == 0;
   const Force f = read_force();
   a.force = f.variant;
   a.chosen = "";

@@ -294,7 +294,6 @@ struct ExpertArgs {
   int act;
   int kn;                  // weights are [K, N]
   int vec;                 // A and B: every row starts on 16 bytes, and offsets inside a tile fit 32 bits
-  int y_vec;               // Y: rows start on 16 bytes and hold whole 16-byte pieces
   const char* force;       // a variant's name (OX_FORCE_KERNEL), or null
   const char* chosen;      // set by the launchers: the variant that runs
 };
