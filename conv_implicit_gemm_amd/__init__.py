@@ -612,8 +612,9 @@ def ox_rmsnorm(X, gamma=None, residual=None, eps=1e-6, out="same", Y=None, scale
     i8 = (_I8 or _small_types())[0]
     rows, K = X.shape
     dtype = X.dtype
+    t = _dtype_code(X)
     if out == "same":
-        code, shape, want = _dtype_code(X), None, dtype
+        code, shape, want = t, None, dtype
     elif out == "fp8":
         code, shape, want = OX_F8E4M3, ((K + 127) >> 7, rows), f8
     elif out == "i8":
@@ -624,7 +625,7 @@ def ox_rmsnorm(X, gamma=None, residual=None, eps=1e-6, out="same", Y=None, scale
         Y = _new_result((rows, K), want, X.device)
     elif Y.shape != (rows, K):
         raise _shape_error("Y", Y, (rows, K))
-    elif Y.dtype != want and not (want is f8 and Y.dtype == u8):
+    elif Y.dtype != want and not (out == "fp8" and Y.dtype == u8):
         raise TypeError("Y is %s, not %s" % (Y.dtype, want))
     if shape is None:
         if scales is not None:
@@ -640,18 +641,22 @@ def ox_rmsnorm(X, gamma=None, residual=None, eps=1e-6, out="same", Y=None, scale
     if residual is not None:
         if S is None:
             S = _new_result((rows, K), dtype, X.device)
-        for name, t in (("residual", residual), ("S", S)):
-            if t.shape != (rows, K):
-                raise _shape_error(name, t, (rows, K))
-            if t.dtype != dtype:
-                raise TypeError("%s is %s, X %s" % (name, t.dtype, dtype))
+        elif S.shape != (rows, K):
+            raise _shape_error("S", S, (rows, K))
+        if residual.shape != (rows, K):
+            raise _shape_error("residual", residual, (rows, K))
+        if residual.dtype != dtype or S.dtype != dtype:
+            raise TypeError("residual is %s, S %s, X %s" % (residual.dtype, S.dtype, dtype))
     elif S is not None:
         raise ValueError("S needs a residual")
     dev = X.get_device()
-    for t in (X, Y, scales, gamma, residual, S):
-        if t is not None and (dev < 0 or t.get_device() != dev or not t.is_contiguous()):
-            raise _refuse_memory(("X", "Y", "scales", "gamma", "residual", "S"), X, Y, scales, gamma, residual, S)
-    st = lib.ox_rmsnorm(_dtype_code(X), rows, K, X.data_ptr(), None if residual is None else residual.data_ptr(),
+    if not (dev >= 0 and Y.get_device() == dev and X.is_contiguous() and Y.is_contiguous()
+            and (scales is None or (scales.get_device() == dev and scales.is_contiguous()))
+            and (gamma is None or (gamma.get_device() == dev and gamma.is_contiguous()))
+            and (residual is None or (residual.get_device() == dev and residual.is_contiguous()
+                                      and S.get_device() == dev and S.is_contiguous()))):
+        raise _refuse_memory(("X", "Y", "scales", "gamma", "residual", "S"), X, Y, scales, gamma, residual, S)
+    st = lib.ox_rmsnorm(t, rows, K, X.data_ptr(), None if residual is None else residual.data_ptr(),
                         None if gamma is None else gamma.data_ptr(), eps, None if S is None else S.data_ptr(), code,
                         Y.data_ptr(), None if scales is None else scales.data_ptr(),
                         raw(dev) if stream is None else _stream(stream))

@@ -301,6 +301,7 @@ struct MoeProduct {
   uint32_t wo[2];
   Global x;                    // the first token
   uint32_t xo[MF];
+  bool on[MF];                 // this lane's column of the fragment holds a token
   int frags;                   // token fragments that hold tokens
   const float* sw[2];          // e4m3: the expert's scales, ONE: the fragment's (step 0)
   int sw_rows[2][4];           // ... where a lane's four rows have theirs
@@ -335,6 +336,7 @@ struct MoeProduct {
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
       if (m > 0 && m >= frags) break;
+      if (!on[m]) continue;      // (its column's sums are never looked at)
       const Global p = x + xk;
       const uint32_t o = opaque(xo[m]);
 #pragma unroll
@@ -367,12 +369,13 @@ struct MoeProduct {
   }
   __device__ __forceinline__ void multiply(const Step& st, f32x4_t (&acc)[2][MF]) const {
 #pragma unroll
-    for (int m = 0; m < MF; ++m) {
-      if (m > 0 && m >= frags) break;
+    for (int f = 0; f < 2; ++f) {
+      const Frag b = Mm::widen(st.w[f][0], st.w[f][1]);
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
+      for (int m = 0; m < MF; ++m) {
+        if (m > 0 && m >= frags) break;
         f32x4_t chain = {0.f, 0.f, 0.f, 0.f};
-        const Frag b = Mm::widen(st.w[f][0], st.w[f][1]), t = token_frag(st.x[m]);
+        const Frag t = token_frag(st.x[m]);
         chain = Mm::template half<0>(b, t, chain);
         chain = Mm::template half<1>(b, t, chain);
         if constexpr (F8) {
@@ -382,6 +385,9 @@ struct MoeProduct {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           acc[f][m][r] = F8 ? __builtin_fmaf(st.s[f][ONE ? 0 : r], chain[r], acc[f][m][r]) : acc[f][m][r] + chain[r];
+        // The addition stays here: moved behind the next branch, where it is taken,
+        // it came without the wait that the matrix instruction's result needs.
+        asm volatile("" : "+v"(acc[f][m]));
       }
     }
   }
@@ -441,8 +447,9 @@ struct MoeProduct {
       multiply(st, acc);
     }
   }
-  // token fragment m: this lane's row, `ld` bytes to a row
-  __device__ __forceinline__ void token(int m, uint32_t row, uint32_t ld) {
+  // token fragment m: this lane's row, `ld` bytes to a row, if it holds one
+  __device__ __forceinline__ void token(int m, bool holds, uint32_t row, uint32_t ld) {
+    on[m] = holds;
     xo[m] = row * ld + ((threadIdx.x & 63) >> 4) * (XB / 8);
   }
   // fragment f: rows n .. n + 15 of expert e's `rows` rows, of which those below
@@ -545,7 +552,7 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(const MoeArgs a)
       mp.frags = ceil_div(count - s0, 16);
 #pragma unroll
       for (int m = 0; m < MF; ++m)
-        mp.token(m, __builtin_amdgcn_ds_bpermute(4 * min(s0 + m * 16 + i, count - 1), tok), a.D * (FMT == FMT_F32 ? 4 : 2));
+        mp.token(m, s0 + m * 16 + i < count, __builtin_amdgcn_ds_bpermute(4 * min(s0 + m * 16 + i, count - 1), tok), a.D * (FMT == FMT_F32 ? 4 : 2));
       if (live) mp.run(k0, k1, (blockIdx.x + ct) & 7, acc);
       float* to = part[turn][wave] + lane * LANE + g * 16;
 #pragma unroll
@@ -638,7 +645,7 @@ __global__ __launch_bounds__(kMoeThreads, 2) void moe_down_kernel(const MoeArgs 
       mp.frags = ceil_div(hi - s0, SLOTS);
 #pragma unroll
       for (int m = 0; m < MF; ++m)
-        mp.token(m, (min(s0 + m * SLOTS + i / PARTS, hi - 1) - lo) * PARTS + i % PARTS, (uint32_t)a.ldh * (4 / PARTS));
+        mp.token(m, s0 + m * SLOTS + i / PARTS < hi, (min(s0 + m * SLOTS + i / PARTS, hi - 1) - lo) * PARTS + i % PARTS, (uint32_t)a.ldh * (4 / PARTS));
       mp.run(k0, k1, (blockIdx.x + wave) & 7, acc);
       // into this wave's sums of the tokens (a token has one slot of an expert)
 #pragma unroll
