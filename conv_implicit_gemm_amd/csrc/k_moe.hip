@@ -6,10 +6,10 @@
 //
 // With so few tokens the chosen experts' weights are what there is to move: they
 // are read once, straight into registers, as the matrix instructions take them
-// (16 rows of weights x 16 tokens).  A wave takes two fragments of 16 rows and a
-// range of K, so that a fragment of the tokens serves both, and the waves' sums
-// are added in their order: every sum's order depends on the sizes and on the
-// routing alone.
+// (16 rows of weights x 16 tokens).  A wave takes two or four fragments of 16 rows
+// and a range of K, so that a fragment of the tokens serves them all, and the
+// waves' sums are added in their order: every sum's order depends on the sizes and
+// on the routing alone.
 //
 // Every block of the first kernel routes all tokens for itself (a launch and a
 // trip to memory less than a kernel of its own); its last block does nothing else
@@ -20,8 +20,8 @@
 //
 // Precision.  bf16 weights (and e4m3 ones, widened: exact) meet bf16 tokens in
 // the bf16 instruction, whose sums are fp32; h is kept as two bf16 numbers (16
-// bits of significand, off by 2^-17 at most), each of which meets W2, so that the only
-// rounding that counts is Y's.  Every batch of K starts a chain of sums from zero.
+// bits of significand, off by 2^-17 at most), each of which meets W2, so that the
+// only rounding that counts is Y's.  Every batch of K starts a chain of sums from zero.
 #include "expert_gemm.hpp"
 
 namespace ox {
@@ -279,10 +279,10 @@ __device__ __forceinline__ u32x4_t part_of_piece(Global p, int n) {
   return u32x4_t{w[0], w[1], w[2], w[3]};
 }
 
-// Two fragments of 16 rows of weights times MF fragments of 16 tokens, over steps
+// NF fragments of 16 rows of weights times MF fragments of 16 tokens, over steps
 // [k0, k1) of K (128 bytes of a weight row each).
 // ONE: a fragment's sixteen rows of weights share a scale (e4m3).
-template <int FMT, int MF, bool ONE, int BUDGET>
+template <int FMT, int NF, int MF, bool ONE, int BUDGET>
 struct MoeProduct {
   typedef FmtOps<FMT> Mm;
   typedef typename Mm::Frag Frag;
@@ -291,28 +291,28 @@ struct MoeProduct {
   static constexpr int XP = F8 ? 4 : 2;            // pieces of a token's step
   static constexpr int XB = F8 ? 256 : 128;        // its bytes
   // Steps in flight, as many as BUDGET registers hold.
-  static constexpr int REGS = 16 + MF * XP * 4 + (F8 ? ONE ? 0 : 8 : 0);
+  static constexpr int REGS = NF * 8 + MF * XP * 4 + (F8 && !ONE ? NF * 4 : 0);
   static constexpr int U = BUDGET / REGS;
   static_assert(U >= 1, "a step fits");
 
   // Bases for all lanes, and this lane's offsets from them (its row, its first
   // piece): a load is a scalar base, a 32-bit offset and a constant.
-  Global w[2];                 // the fragments' first rows of weights
-  uint32_t wo[2];
+  Global w[NF];                // the fragments' first rows of weights
+  uint32_t wo[NF];
   Global x;                    // the first token
   uint32_t xo[MF];
   bool on[MF];                 // this lane's column of the fragment holds a token
   int frags;                   // token fragments that hold tokens
-  const float* sw[2];          // e4m3: the expert's scales, ONE: the fragment's (step 0)
-  int sw_rows[2][4];           // ... where a lane's four rows have theirs
+  const float* sw[NF];         // e4m3: the expert's scales, ONE: the fragment's (step 0)
+  int sw_rows[NF][4];          // ... where a lane's four rows have theirs
   int K;
 
   // piece i of a token's step, behind the lane's first
   static __device__ __forceinline__ constexpr int x_at(int i) { return F8 ? (i & 1) * 16 + (i >> 1) * 128 : i * 64; }
 
   struct Step {
-    u32x4_t w[2][2], x[MF][XP];
-    float s[2][ONE ? 1 : 4];
+    u32x4_t w[NF][2], x[MF][XP];
+    float s[NF][ONE ? 1 : 4];
   };
   // PART: K may end inside the step
   template <bool PART>
@@ -321,7 +321,7 @@ struct MoeProduct {
     const int left = (int)min((int64_t)XB, ((int64_t)K - (int64_t)k * KE) * Mm::ESZ);      // bytes of a weight row
     const int64_t wk = (int64_t)k * 128, xk = (int64_t)k * XB;
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
+    for (int f = 0; f < NF; ++f) {
       const Global p = w[f] + wk;
       const uint32_t o = opaque(wo[f]);
 #pragma unroll
@@ -350,7 +350,7 @@ struct MoeProduct {
     }
     if constexpr (F8) {
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
+      for (int f = 0; f < NF; ++f) {
         typedef const __attribute__((address_space(4))) float* Scalar;
         if constexpr (ONE) {
           st.s[f][0] = *(Scalar)(uintptr_t)(sw[f] + k);      // (by a scalar load)
@@ -367,9 +367,9 @@ struct MoeProduct {
     for (int i = 0; i < XP; ++i) f.v[i] = p[i];
     return f;
   }
-  __device__ __forceinline__ void multiply(const Step& st, f32x4_t (&acc)[2][MF]) const {
+  __device__ __forceinline__ void multiply(const Step& st, f32x4_t (&acc)[NF][MF]) const {
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
+    for (int f = 0; f < NF; ++f) {
       const Frag b = Mm::widen(st.w[f][0], st.w[f][1]);
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
@@ -394,7 +394,7 @@ struct MoeProduct {
   // All steps [first, end).  They are taken in turn from an eighth of the way that
   // `phase` gives: waves that all begin with a row's first bytes, and rows that
   // are a power of two apart, would keep asking the same few memory channels.
-  __device__ __forceinline__ void run(int first, int end, int phase, f32x4_t (&acc)[2][MF]) const {
+  __device__ __forceinline__ void run(int first, int end, int phase, f32x4_t (&acc)[NF][MF]) const {
     const int k0 = __builtin_amdgcn_readfirstlane(first), k1 = __builtin_amdgcn_readfirstlane(end);
     if (K == 0) return;
     const int whole = min(k1, K / KE);      // steps that K does not end inside
@@ -507,7 +507,7 @@ __device__ __forceinline__ float value_at(const void* p, int64_t at) {
 // gate rows and the 16 up rows beside them, or 32 rows.
 template <int FMT, int MF, bool ONE>
 __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(const MoeArgs a) {
-  typedef MoeProduct<FMT, MF, ONE, 80> MP;
+  typedef MoeProduct<FMT, 2, MF, ONE, 80> MP;
   constexpr int LANE = 4, SET = 64 * LANE + 48;      // floats: a lane's results, a fragment's (16 apart every 16 lanes: all banks)
   __shared__ Route rt;
   __shared__ __attribute__((aligned(16))) float part[2][kMoeWaves][2 * MF * SET];
@@ -594,14 +594,15 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(const MoeArgs a)
   }
 }
 
-// Block (tile, s): columns 32 tile .. + 31 of Y, range s of all the chosen
+// Block (tile, s): 16 NF columns of Y, range s of all the chosen
 // experts' hidden rows.  A hidden row's two parts lie in neighbouring columns of
 // a token fragment, which holds eight slots then, and their sums are added.
-template <int FMT, int MF>
+template <int FMT, int NF, int MF>
 __global__ __launch_bounds__(kMoeThreads, 2) void moe_down_kernel(const MoeArgs a) {
   constexpr int PARTS = FMT == FMT_F32 ? 1 : 2, SLOTS = 16 / PARTS;      // of a hidden row; of a fragment
-  typedef MoeProduct<FMT, MF, true, 160> MP;
-  extern __shared__ __attribute__((aligned(16))) float yw[];      // [waves][T][32]
+  typedef MoeProduct<FMT, NF, MF, true, 160> MP;
+  constexpr int TILE = 16 * NF, QUADS = TILE / 4;
+  extern __shared__ __attribute__((aligned(16))) float yw[];      // [waves][T][TILE]
   __shared__ RouteOut rt;
   __shared__ int last;
   const RouteOut* ro = (const RouteOut*)a.route;
@@ -618,11 +619,11 @@ __global__ __launch_bounds__(kMoeThreads, 2) void moe_down_kernel(const MoeArgs 
     rt.off[p] = ro->off[p];
   }
   if (threadIdx.x == 0) rt.nact = ro->nact;
-  float* mine = yw + wave * a.T * 32;
-  for (int p = lane; p < a.T * 8; p += 64) ((f32x4_t*)mine)[p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  float* mine = yw + wave * a.T * TILE;
+  for (int p = lane; p < a.T * QUADS; p += 64) ((f32x4_t*)mine)[p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   __syncthreads();
 
-  const int tile = blockIdx.x / a.S, s = blockIdx.x - tile * a.S, n0 = tile * 32;
+  const int tile = blockIdx.x / a.S, s = blockIdx.x - tile * a.S, n0 = tile * TILE;
   const int nk = max(1, ceil_div(a.H, MP::KE));
   const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(rt.nact) * nk, parts = (int64_t)a.S * kMoeWaves;
   int st = (int)(total * (s * kMoeWaves + wave) / parts);
@@ -633,13 +634,13 @@ __global__ __launch_bounds__(kMoeThreads, 2) void moe_down_kernel(const MoeArgs 
     const int ai = __builtin_amdgcn_readfirstlane(st / nk), k0 = st - ai * nk, k1 = min(nk, k0 + end - st);
     const int e = __builtin_amdgcn_readfirstlane(rt.act[ai]), lo = __builtin_amdgcn_readfirstlane(rt.off[ai]);
     const int hi = __builtin_amdgcn_readfirstlane(rt.off[ai + 1]);
-    mp.weights(0, a.W2, a.s2, e, a.D, n0, a.D);
-    mp.weights(1, a.W2, a.s2, e, a.D, min(n0 + 16, a.D - 1), a.D);
+#pragma unroll
+    for (int f = 0; f < NF; ++f) mp.weights(f, a.W2, a.s2, e, a.D, min(n0 + f * 16, a.D - 1), a.D);
     mp.x = uniform_global((const char*)a.hidden + (int64_t)lo * a.ldh * 4);
     for (int s0 = lo; s0 < hi; s0 += SLOTS * MF) {
-      f32x4_t acc[2][MF];
+      f32x4_t acc[NF][MF];
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
+      for (int f = 0; f < NF; ++f)
 #pragma unroll
         for (int m = 0; m < MF; ++m) acc[f][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       mp.frags = ceil_div(hi - s0, SLOTS);
@@ -653,16 +654,16 @@ __global__ __launch_bounds__(kMoeThreads, 2) void moe_down_kernel(const MoeArgs 
         const int slot = s0 + m * SLOTS + i / PARTS;
         if constexpr (PARTS == 2) {
 #pragma unroll
-          for (int f = 0; f < 2; ++f)
+          for (int f = 0; f < NF; ++f)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
               acc[f][m][r] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc[f][m][r]), 0xB1, 0xf, 0xf, true));   // lane ^ 1
         }
         if (slot >= hi || i % PARTS != 0) continue;
         const float wt = rt.weight[slot];
-        float* y = mine + rt.tok[slot] * 32 + g * 4;
+        float* y = mine + rt.tok[slot] * TILE + g * 4;
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
+        for (int f = 0; f < NF; ++f) {
           f32x4_t v = acc[f][m];
           if (a.b2 && k0 == 0) {
 #pragma unroll
@@ -682,9 +683,9 @@ __global__ __launch_bounds__(kMoeThreads, 2) void moe_down_kernel(const MoeArgs 
   }
   __syncthreads();
 
-  const int quads = a.T * 8;      // four columns of a token
+  const int quads = a.T * QUADS;      // four columns of a token
   auto store = [&](int q, f32x4_t v) {
-    const int t = q >> 3, n = n0 + (q & 7) * 4;
+    const int t = q / QUADS, n = n0 + q % QUADS * 4;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       if (n + r < a.D) {
@@ -725,9 +726,20 @@ __global__ __launch_bounds__(kMoeThreads, 2) void moe_down_kernel(const MoeArgs 
   }
 }
 
-// UF, DF: token fragments at a time in the first and the second kernel
-template <int FMT, int UF, int DF>
-int launch(const MoeArgs& a, hipStream_t s) {
+// Ranges of K that the second kernel's tiles are cut into: about one block for
+// every CU (two: one token 23.3 us, 21.7 with one; the others equal).
+int moe_ranges(int64_t tiles) { return (int)((kCus + tiles - 1) / tiles); }
+
+// UF, DF: token fragments at a time in the first and the second kernel; NF: weight
+// fragments of a wave in the second.
+template <int FMT, int UF, int NF, int DF>
+int launch_pair(MoeArgs& a, int64_t steps, hipStream_t s) {
+  a.tiles = ceil_div(a.D, 16 * NF);
+  // no more ranges than give every wave a step
+  int64_t S = moe_ranges(a.tiles);
+  while (S > 1 && S * kMoeWaves > steps) S = (S + 1) / 2;
+  a.S = (int)S;
+
   // (the up rows of a gated W1 start anywhere in a block of scales)
   if (FMT == FMT_FP8X && a.gated && a.H % 16 != 0)
     hipLaunchKernelGGL((moe_up_kernel<FMT, UF, FMT != FMT_FP8X>), dim3(a.up_blocks), dim3(kMoeThreads), 0, s, a);
@@ -735,21 +747,30 @@ int launch(const MoeArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((moe_up_kernel<FMT, UF, true>), dim3(a.up_blocks), dim3(kMoeThreads), 0, s, a);
   int rc = (int)hipGetLastError();
   if (rc) return rc;
-  hipLaunchKernelGGL((moe_down_kernel<FMT, DF>), dim3(a.tiles * a.S), dim3(kMoeThreads), kMoeWaves * a.T * 32 * 4, s, a);
+  hipLaunchKernelGGL((moe_down_kernel<FMT, NF, DF>), dim3(a.tiles * a.S), dim3(kMoeThreads),
+                     kMoeWaves * a.T * 16 * NF * 4, s, a);
   return (int)hipGetLastError();
+}
+
+// More than 16 tokens: four weight fragments a wave, 64 columns of Y, where that
+// still leaves every wave four steps: the tokens' pieces then serve twice as many
+// weights (64 tokens, 8 of 64 bf16 experts of 1024 x 2048: 174 us, 182 with two;
+// 4 of 32 e4m3 experts of 512 x 1024, one step a wave: 35.9 us, 30.5 with two).
+// Up to 16 tokens the weights alone bound it, and both widths take the same time.
+template <int FMT, int UF, int DF>
+int launch(MoeArgs& a, hipStream_t s) {
+  const int64_t experts = a.E < a.T * a.top ? a.E : a.T * a.top;
+  const int64_t steps = experts * (((int64_t)a.H * FmtOps<FMT>::ESZ + 127) / 128);
+  if constexpr (UF > 1) {
+    if (steps >= (int64_t)4 * kMoeWaves * moe_ranges(ceil_div(a.D, 64)))
+      return launch_pair<FMT, UF, 4, DF>(a, steps, s);
+  }
+  return launch_pair<FMT, UF, 2, DF>(a, steps, s);
 }
 
 constexpr int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
-
-// Ranges of K that the second kernel's tiles are cut into: about one block for
-// every CU (two: one token 23.3 us, 21.7 with one; the others equal).
-static int moe_ranges(int64_t D) {
-  const int64_t tiles = (D + 31) / 32;
-  const int64_t s = (kCus + tiles - 1) / tiles;
-  return (int)(s < 1 ? 1 : s);
-}
 
 // Workspace: routing, counters, hidden rows, partial sums.
 struct MoePlan {
@@ -761,7 +782,9 @@ static MoePlan moe_plan(int64_t T, int64_t D, int64_t H, int64_t top) {
   p.counters = up16(sizeof(RouteOut));
   p.hidden = p.counters + up16((D + 31) / 32 * 4);
   p.partials = p.hidden + up16(T * top * p.ldh * 4);
-  p.bytes = p.partials + (int64_t)moe_ranges(D) * T * ((D + 31) / 32 * 32) * 4;
+  const int64_t narrow = (D + 31) / 32, wide = (D + 63) / 64;
+  const int64_t a = moe_ranges(narrow) * narrow * 32, b = moe_ranges(wide) * wide * 64;
+  p.bytes = p.partials + (a > b ? a : b) * T * 4;
   return p;
 }
 size_t moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t top) {
@@ -778,14 +801,8 @@ int launch_moe(MoeArgs& a, void* workspace, void* stream) {
   a.hidden = ws + p.hidden;
   a.partials = (float*)(ws + p.partials);
   a.ldh = p.ldh;
-  a.tiles = ceil_div(a.D, 32);
   const int64_t experts = a.E < a.T * a.top ? a.E : a.T * a.top;
   const int esz = a.w_dt == DT_F32 ? 4 : a.w_dt == DT_BF16 ? 2 : 1;
-  // no more ranges than give every wave a step
-  const int64_t steps = experts * (((int64_t)a.H * esz + 127) / 128);
-  int64_t S = moe_ranges(a.D);
-  while (S > 1 && S * kMoeWaves > steps) S = (S + 1) / 2;
-  a.S = (int)S;
   const int nk = (int)(((int64_t)a.D * esz + 127) / 128);
   a.slices = 1;
   while (a.slices < kMoeWaves && a.slices < nk) a.slices *= 2;

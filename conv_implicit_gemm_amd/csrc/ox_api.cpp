@@ -1213,7 +1213,7 @@ ox_status ox_quantize_i8(ox_dtype t, int64_t rows, int64_t K, const void* X, int
 
 size_t ox_moe_few_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t top) {
   if (T < 1 || T > kMoeTokens || D < 1 || H < 0 || E < 1 || E > kMoeExperts || top < 1 || top > kMoeTop || top > E ||
-      D > kMoeWidth || H > kMoeWidth || too_big(T, D) || too_big(E, D, H))
+      D > kMoeWidth || H > kMoeWidth)
     return 0;
   return moe_workspace_bytes(T, D, H, E, top);
 }
@@ -1245,7 +1245,6 @@ ox_status ox_moe_few(ox_dtype t, ox_dtype w_type, int64_t T, int64_t D, int64_t 
   if (top > kMoeTop) return fail(OX_ERR_UNSUPPORTED, "%s: top=%lld, up to %d experts a token", fn, (long long)top, kMoeTop);
   if (D > kMoeWidth || H > kMoeWidth)
     return fail(OX_ERR_UNSUPPORTED, "%s: D=%lld or H=%lld is above %d", fn, (long long)D, (long long)H, kMoeWidth);
-  if (too_big(T, D) || too_big(E, gated ? 2 * H : H, D)) return fail(OX_ERR_UNSUPPORTED, "%s: a tensor holds 2^31 elements or more", fn);
   if (!X || !scores || !Y) return fail(OX_ERR_INVALID_ARG, "%s: X, scores or Y is NULL", fn);
   if (H > 0 && (!W1 || !W2)) return fail(OX_ERR_INVALID_ARG, "%s: W1 or W2 is NULL", fn);
   if (H > 0 && w_type == OX_F8E4M3 && (!w1_scales || !w2_scales))

@@ -356,3 +356,86 @@ def test_on_another_stream(ox):
     ox.ox_moe_few(X, scores, layer.W[0], layer.W[1], 2, Y=Y, workspace=ws, stream=s)
     s.synchronize()
     assert torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("t,H,shift", [("bf16", 512, 0), ("fp8", 1000, 3), ("f32", 250, 0)])
+def test_wide_rows_of_many_tokens(ox, t, H, shift):
+    """Many steps to every wave of the second product: its other tile, with a last
+    one of three columns, and an expert with more tokens than one pass takes."""
+    T, E, top, D = 40, 8, 2, 8195
+    say("moe_few wide", t, H, shift)
+    layer = Layer([8, H], t, E, D, H, False, True, shift)
+    scores = torch.from_numpy(layer.rng.standard_normal((T, E))).float()
+    scores[:36, 5] += 9.0
+    run_case(ox, layer, T, top, "relu", scores, shift=shift, what=("wide", t))
+
+
+def test_weights_behind_four_gigabytes(ox):
+    """The last of 130 experts, 4.5 GB behind the first, has the bits it has alone."""
+    E, D, H = 130, 4096, 4224
+    g = torch.Generator(device="cuda").manual_seed(9)
+    W1 = torch.empty((E, H, D), dtype=BF, device="cuda")
+    W2 = torch.empty((E, D, H), dtype=BF, device="cuda")
+    for w in (W1, W2):
+        w[0].zero_()
+        w[E - 1].normal_(0, 0.02, generator=g)
+    X = torch.randn((1, D), generator=g, device="cuda").bfloat16()
+    scores = torch.full((1, E), float("-inf"), device="cuda")
+    scores[0, E - 1] = 1.0
+    Y = ox.ox_moe_few(X, scores, W1, W2, 1, act="silu", gated=False)
+    alone = ox.ox_moe_few(X, torch.ones((1, 1), device="cuda"), W1[E - 1:], W2[E - 1:], 1, act="silu", gated=False)
+    assert torch.equal(Y, alone) and (Y != 0).any().item()
+
+
+def test_two_streams_at_once_with_a_workspace_each(ox):
+    layer = Layer(10, "bf16", 16, 1024, 512, True, False)
+    X = [torch.from_numpy(layer.rng.standard_normal((t, 1024))).bfloat16().cuda() for t in (30, 7)]
+    scores = [torch.from_numpy(layer.rng.standard_normal((len(x), 16))).float().cuda() for x in X]
+    want = [ox.ox_moe_few(x, s, layer.W[0], layer.W[1], 4) for x, s in zip(X, scores)]
+    streams = [torch.cuda.Stream() for _ in X]
+    ws = [torch.empty(ox.ox_moe_few_workspace_bytes(len(x), 1024, 512, 16, 4), dtype=torch.uint8, device="cuda") for x in X]
+    Y = [[torch.empty_like(x) for _ in range(20)] for x in X]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for x, s, w, y, st in zip(X, scores, ws, Y, streams):
+            ox.ox_moe_few(x, s, layer.W[0], layer.W[1], 4, Y=y[i], workspace=w, stream=st)
+    torch.cuda.synchronize()
+    for ys, y in zip(Y, want):
+        assert all(torch.equal(one, y) for one in ys)
+
+
+def test_the_result_in_place_of_the_tokens(ox):
+    layer = Layer(11, "fp8", 6, 200, 90, True, True)
+    X = torch.from_numpy(layer.rng.standard_normal((18, 200))).bfloat16().cuda()
+    scores = torch.from_numpy(layer.rng.standard_normal((18, 6))).float().cuda()
+
+    def call(x, y):
+        return ox.ox_moe_few(x, scores, layer.W[0], layer.W[1], 2, w1_scales=layer.scales[0], w2_scales=layer.scales[1],
+                             b1=layer.b[0], b2=layer.b[1], Y=y)
+    want = call(X, None)
+    assert torch.equal(call(X, X), want) and torch.equal(X, want)
+
+
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("T", [2, 64])
+def test_the_widest_layers(ox, T, t):
+    """D, then H, at their limit of 2^22, with values whose sums are exact in
+    fp32 in any order (multiples of 2^-20 below 2^3) and results exact in bf16."""
+    n, few = 1 << 22, 8
+    x = torch.ones((T, 1), dtype=t, device="cuda")
+    x[1::2] = 2.0
+    route = torch.zeros((T, 1), device="cuda")
+    say("moe_few widest", T, t)
+    W1 = torch.full((1, few, n), 2.0 ** -20, dtype=t, device="cuda")      # h = x
+    W1[..., 1::2] = 0
+    W1 *= 0.5
+    W2 = torch.zeros((1, n, few), dtype=t, device="cuda")
+    d = torch.arange(n, device="cuda") % 7
+    W2[0, :, 3] = d.to(t)
+    Y = ox.ox_moe_few(x.expand(T, n).contiguous(), route, W1, W2, 1, act="none", gated=False)
+    assert torch.equal(Y.float(), x.float() * d.float())
+    W1 = torch.zeros((1, n, few), dtype=t, device="cuda")
+    W1[0, :, 5] = (torch.arange(n, device="cuda") % 2).to(t)
+    W2 = torch.full((1, few, n), 2.0 ** -20, dtype=t, device="cuda")      # 2^21 of them are met
+    Y = ox.ox_moe_few(x.expand(T, few).contiguous(), route, W1, W2, 1, act="none", gated=False)
+    assert torch.equal(Y, (2 * x).expand(T, few))
