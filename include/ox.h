@@ -23,7 +23,7 @@
  *   - Any pointer alignment is accepted: kernels pick the widest vector
  *     access the pointers and strides permit.
  *   - Every tensor must hold fewer than 2^31 elements (OX_ERR_UNSUPPORTED
- *     otherwise).  Empty tensors (a zero dimension) are accepted and enqueue
+ *     otherwise; but for the weights of ox_moe_few, which may hold more).  Empty tensors (a zero dimension) are accepted and enqueue
  *     nothing (except a Gemm with K = 0, which still writes act(beta*bias)).
  *   - Errors: a non-zero ox_status; ox_last_error() then names the offending
  *     argument.  A failing HIP launch returns OX_ERR_HIP; device faults
@@ -524,8 +524,9 @@ ox_status ox_gemm_grouped_fp8(ox_dtype y_type, int64_t T, int64_t N, int64_t K, 
  * none), weights: DEVICE fp32 [T, top]; either may be NULL.
  * Sums are fp32, and Y is rounded once (h passes in 16 bits of significand for
  * bf16); their order depends on the sizes and on the routing alone.
- * T <= 64, E <= 512, top <= 16, D and H <= 2^22 (OX_ERR_UNSUPPORTED above; ox_gemm_grouped takes
- * any number of rows).  T = 0 or D = 0 enqueue nothing.
+ * Y may be X (in place); any other overlap of an output is undefined.
+ * T <= 64, E <= 512, top <= 16, D and H <= 2^22 (OX_ERR_UNSUPPORTED above;
+ * ox_gemm_grouped takes any number of rows).  T = 0 or D = 0 enqueue nothing.
  * workspace: DEVICE, 16-byte aligned, at least ox_moe_few_workspace_bytes(T, D,
  * H, E, top) bytes (0 for sizes that the call refuses); its contents on entry do
  * not matter.  Calls (and captured graphs) that share one must not overlap. */
