@@ -18,7 +18,7 @@
 // each read or written once: 8192 rows of 4096 bf16, residual, norm and e4m3
 // codes (236 MB) 45 us, 5.2 TB/s; int8 codes of 8192 rows of 8192 bf16 (201 MB)
 // 38.9 us, 5.2 TB/s, what a large copy reaches.  24 rows are one trip to HBM, a
-// barrier and a store: 3.2 and 2.7 us.  Blocks that stay and load the next row
+// barrier and a store: 3.4 and 2.8 us.  Blocks that stay and load the next row
 // ahead were no faster (47.7 us).
 #include "quant_codes.hpp"
 
