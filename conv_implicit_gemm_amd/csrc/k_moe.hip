@@ -291,7 +291,7 @@ struct MoeProduct {
   static constexpr int XP = F8 ? 4 : 2;            // pieces of a token's step
   static constexpr int XB = F8 ? 256 : 128;        // its bytes
   // Steps in flight, as many as BUDGET registers hold.
-  static constexpr int REGS = NF * 8 + MF * XP * 4 + (F8 && !ONE ? NF * 4 : 0);
+  static constexpr int REGS = NF * 8 + MF * XP * 4;
   static constexpr int U = BUDGET / REGS;
   static_assert(U >= 1, "a step fits");
 
@@ -303,8 +303,8 @@ struct MoeProduct {
   uint32_t xo[MF];
   bool on[MF];                 // this lane's column of the fragment holds a token
   int frags;                   // token fragments that hold tokens
-  const float* sw[NF];         // e4m3: the expert's scales, ONE: the fragment's (step 0)
-  int sw_rows[NF][4];          // ... where a lane's four rows have theirs
+  const float* sw[NF];         // e4m3: the scales of the fragment's first row (step 0)
+  int sw_next[NF], sw_rows[NF];      // ... those of its last row, from there; the rows in front of them
   int K;
 
   // piece i of a token's step, behind the lane's first
@@ -312,7 +312,7 @@ struct MoeProduct {
 
   struct Step {
     u32x4_t w[NF][2], x[MF][XP];
-    float s[NF][ONE ? 1 : 4];
+    float s[NF][ONE ? 1 : 2];
   };
   // PART: K may end inside the step
   template <bool PART>
@@ -352,12 +352,8 @@ struct MoeProduct {
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
         typedef const __attribute__((address_space(4))) float* Scalar;
-        if constexpr (ONE) {
-          st.s[f][0] = *(Scalar)(uintptr_t)(sw[f] + k);      // (by a scalar load)
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) st.s[f][r] = sw[f][sw_rows[f][r] + k];
-        }
+        st.s[f][0] = *(Scalar)(uintptr_t)(sw[f] + k);      // (by scalar loads)
+        if constexpr (!ONE) st.s[f][1] = *(Scalar)(uintptr_t)(sw[f] + sw_next[f] + k);
       }
     }
   }
@@ -383,8 +379,11 @@ struct MoeProduct {
           chain = Mm::template half<3>(b, t, chain);
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[f][m][r] = F8 ? __builtin_fmaf(st.s[f][ONE ? 0 : r], chain[r], acc[f][m][r]) : acc[f][m][r] + chain[r];
+        for (int r = 0; r < 4; ++r) {
+          const bool front = ONE || ((threadIdx.x & 63) >> 4) * 4 + r < sw_rows[f];
+          acc[f][m][r] = F8 ? __builtin_fmaf(front ? st.s[f][0] : st.s[f][ONE ? 0 : 1], chain[r], acc[f][m][r])
+                            : acc[f][m][r] + chain[r];
+        }
         // The addition stays here: moved behind the next branch, where it is taken,
         // it came without the wait that the matrix instruction's result needs.
         asm volatile("" : "+v"(acc[f][m]));
@@ -459,10 +458,10 @@ struct MoeProduct {
     w[f] = uniform_global((const char*)W + ((int64_t)e * rows + n) * K * Mm::ESZ);
     wo[f] = (uint32_t)min(i, end - 1 - n) * (uint32_t)K * Mm::ESZ + g * 16;
     if constexpr (F8) {
-      const int nb = ceil_div(rows, 128), kb = ceil_div(K, 128);
-      sw[f] = uniform_ptr(scales + (int64_t)e * nb * kb + (ONE ? min(n, end - 1) / 128 * kb : 0));
-#pragma unroll
-      for (int r = 0; r < 4; ++r) sw_rows[f][r] = min(n + g * 4 + r, end - 1) / 128 * kb;
+      const int nb = ceil_div(rows, 128), kb = ceil_div(K, 128), b = min(n, end - 1) / 128;
+      sw[f] = uniform_ptr(scales + ((int64_t)e * nb + b) * kb);
+      sw_next[f] = min(n + 15, end - 1) / 128 > b ? kb : 0;
+      sw_rows[f] = (b + 1) * 128 - n;
     }
   }
 };
