@@ -443,3 +443,19 @@ def test_a_feed_forward_layer_in_int8(ox):
         for a, b in zip(held, eager):
             assert torch.equal(a, b)
         check(held)
+
+
+@pytest.mark.parametrize("M,N", [(70, 66), (5, 300), (130, 130)])
+def test_every_end_of_a_row(ox, M, N):
+    """K that ends everywhere inside a piece of 16 bytes and a block of 128: int8
+    and bf16 products of small whole numbers, exact in fp32."""
+    g = torch.Generator().manual_seed(M)
+    for K in list(range(1, 35)) + list(range(111, 146)) + list(range(250, 275)):
+        say("row ends", M, N, K)
+        A, B = (torch.randint(-9, 10, (n, K), generator=g, dtype=torch.int8) for n in (M, N))
+        want = A.double() @ B.double().T
+        one = [torch.ones(n, device="cuda") for n in (M, N)]
+        assert torch.equal(ox.ox_gemm_i8(A.cuda(), one[0], B.cuda(), one[1], out_dtype=torch.float32).double().cpu(), want)
+        off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+        Y = ox.ox_gemm_grouped(A.bfloat16().cuda(), B.bfloat16().cuda()[None], off, transB=True)
+        assert torch.equal(Y.cpu(), want.bfloat16())
