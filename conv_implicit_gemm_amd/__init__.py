@@ -155,6 +155,27 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
+def _torch_stream(stream, device):
+    """A stream or its raw handle as torch's allocator takes it."""
+    cuda = _torch().cuda
+    if isinstance(stream, cuda.Stream):
+        return stream
+    handle = _stream(stream)
+    return cuda.ExternalStream(handle, device) if handle else cuda.default_stream(device)
+
+
+def _scratch(nbytes, device, stream):
+    """Memory that a call needs until its kernels are done, and drops before.  It
+    is the launch stream's: torch's allocator gives it on to that stream alone,
+    whose next kernels run behind these, and gives out none that another
+    stream's kernels may still be using."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _dense(t, name):
     if t is not None and not t.is_contiguous():
         raise ValueError("%s must be contiguous (dense row-major)" % name)
@@ -678,7 +699,8 @@ def ox_moe_few(X, scores, W1, W2, top, w1_scales=None, w2_scales=None, b1=None, 
     [E, H, D], W2 [E, D, H], of X's type, or float8_e4m3fn (uint8 codes) with
     scales per 128 x 128 beside bfloat16 X; b1, b2 of X's type.  experts (int32)
     and weights (float32) [T, top] are filled if given.  workspace: any dense
-    device tensor of ox_moe_few_workspace_bytes bytes (made if None)."""
+    device tensor of ox_moe_few_workspace_bytes bytes (made for the call, under its
+    stream, if None)."""
     f8, u8, f32, i32, raw = _F8 or _types()
     bf16 = (_I8 or _small_types())[1]
     T, D = X.shape
@@ -725,7 +747,7 @@ def ox_moe_few(X, scores, W1, W2, top, w1_scales=None, w2_scales=None, b1=None, 
     if weights is not None and (weights.shape != (T, top) or weights.dtype != f32):
         raise ValueError("weights must be float32 %s" % ((T, top),))
     if workspace is None:
-        workspace = _new_result((lib.ox_moe_few_workspace_bytes(T, D, H, E, top),), u8, X.device)
+        workspace = _scratch(lib.ox_moe_few_workspace_bytes(T, D, H, E, top), X.device, stream)
     dev = X.get_device()
     for t in (X, scores, W1, W2, Y, w1_scales, w2_scales, b1, b2, experts, weights, workspace):
         if t is not None and (dev < 0 or t.get_device() != dev or not t.is_contiguous()):

@@ -1,0 +1,131 @@
+"""Whose memory the binding hands to a launch on a stream that is not torch's
+current one (no GPU needed: torch's allocator and the library are stand-ins).
+
+torch's allocator keeps memory by the stream it was asked for under: what is
+given back serves the next tensor of that stream, whose work comes behind, and
+may still be in use by kernels of any other stream.  So what a call makes for a
+launch has to be of the launch's stream."""
+import contextlib
+import importlib.util
+import itertools
+import types
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+CURRENT = 5          # the current stream's handle
+
+
+class Tensor:
+    """A dense tensor on GPU 0 that remembers the stream it was made under."""
+    places = itertools.count(1 << 20, 1 << 20)
+
+    def __init__(self, shape, dtype, stream=CURRENT):
+        self.shape, self.dtype, self.stream = torch.Size(shape), dtype, stream
+        self.device, self.place, self.recorded = torch.device("cuda", 0), next(self.places), []
+
+    def data_ptr(self):
+        return self.place
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return torch.empty(0, dtype=self.dtype).element_size()
+
+    def record_stream(self, stream):
+        self.recorded.append(stream.cuda_stream)
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+class Torch:
+    """torch with an allocator of stand-ins and a current stream of its own."""
+
+    def __init__(self):
+        self.now, self.made = [CURRENT], []
+
+        def external(handle, device=None):
+            assert handle != 0, "torch takes a stream of its pool for handle 0"
+            return Stream(handle)
+
+        @contextlib.contextmanager
+        def under(stream):
+            self.now.append(stream.cuda_stream)
+            yield
+            self.now.pop()
+
+        self.cuda = types.SimpleNamespace(Stream=Stream, ExternalStream=external, stream=under,
+                                          default_stream=lambda device=None: Stream(0),
+                                          current_stream=lambda device=None: Stream(self.now[-1]))
+
+    def empty(self, *shape, dtype=None, device=None):
+        shape = shape[0] if len(shape) == 1 and not isinstance(shape[0], int) else shape
+        self.made.append(Tensor(shape, dtype or torch.float32, self.now[-1]))
+        return self.made[-1]
+
+    def __getattr__(self, name):
+        return getattr(torch, name)
+
+
+@pytest.fixture
+def ox():
+    """A copy of the binding over a library that only takes down its arguments."""
+    import conv_implicit_gemm_amd as real
+    spec = importlib.util.spec_from_file_location("conv_implicit_gemm_amd_streams", real.__file__)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    fake = Torch()
+    mod._types()
+    mod._F8 = mod._F8[:4] + (lambda device: fake.now[-1],)
+    mod._torch = lambda: fake
+    mod.fake, mod.calls, library = fake, [], mod.lib
+
+    class Library:
+        def __getattr__(self, name):
+            if name.endswith("_bytes"):
+                return getattr(library, name)
+
+            def call(*args):
+                mod.calls.append((name, args))
+                return 0
+            return call
+    mod.lib = Library()
+    return mod
+
+
+def made_of(ox, place):
+    """The stand-in at an address that the library was given."""
+    found = [t for t in ox.fake.made if t.place == place]
+    assert len(found) == 1
+    return found[0]
+
+
+STREAMS = [(None, CURRENT), (7, 7), (Stream(7), 7), (0, 0), (Stream(0), 0), (CURRENT, CURRENT), (Stream(CURRENT), CURRENT)]
+IDS = ["none", "handle", "object", "default-handle", "default-object", "current-handle", "current-object"]
+
+
+@pytest.mark.parametrize("stream,launched", STREAMS, ids=IDS)
+def test_scratch_of_the_routed_layer(ox, stream, launched):
+    T, D, H, E, top = 4, 64, 96, 8, 2
+    bf = torch.bfloat16
+    ox.ox_moe_few(Tensor((T, D), bf), Tensor((T, E), torch.float32), Tensor((E, 2 * H, D), bf), Tensor((E, D, H), bf), top,
+                  Y=Tensor((T, D), bf), stream=stream)
+    (name, args), = ox.calls
+    assert name == "ox_moe_few" and args[-1] == launched
+    scratch = made_of(ox, args[-3])
+    assert scratch.numel() == args[-2] == ox.ox_moe_few_workspace_bytes(T, D, H, E, top)
+    assert scratch.stream == launched

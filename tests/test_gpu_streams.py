@@ -1,0 +1,59 @@
+"""Calls on streams that are not torch's current one, with memory that the
+binding makes: nothing is handed on while the launch still uses it."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+WAIT = 5_000_000          # clock ticks of the kernel that holds a stream back: milliseconds
+
+
+@pytest.fixture(scope="module")
+def ox():
+    import conv_implicit_gemm_amd as ox
+    return ox
+
+
+def layer(T, E, D, H, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda")
+    return (normal(T, D).bfloat16(), normal(T, E), (normal(E, 2 * H, D) * D ** -0.5).bfloat16(),
+            (normal(E, D, H) * H ** -0.5).bfloat16(), 2)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_routed_layers_on_two_streams_make_a_workspace_each(ox, handle):
+    cases = [layer(48, 8, 512, 256, 1), layer(7, 16, 512, 256, 2)]
+    want = [ox.ox_moe_few(*c) for c in cases]
+    Y = [[torch.zeros_like(w) for _ in range(10)] for w in want]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for s in streams:
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(WAIT)
+    for i in range(10):
+        for c, y, s in zip(cases, Y, streams):
+            ox.ox_moe_few(*c, Y=y[i], stream=s.cuda_stream if handle else s)
+    # the current stream's next tensors, over anything that was given back
+    over = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(40)]
+    torch.cuda.synchronize()
+    for ys, w in zip(Y, want):
+        assert all(torch.equal(y, w) for y in ys)
+    assert all((o == 255).all().item() for o in over)
+
+
+def test_the_default_stream_by_its_handle(ox):
+    c = layer(5, 8, 256, 128, 3)
+    want = ox.ox_moe_few(*c)
+    side = torch.cuda.Stream()
+    Y = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        ox.ox_moe_few(*c, Y=Y, stream=torch.cuda.default_stream())
+        ox.ox_moe_few(*c, Y=Y, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want)
