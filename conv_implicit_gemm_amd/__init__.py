@@ -777,8 +777,7 @@ def ox_dynamic_quantize_linear(X, Y=None, y_scale=None, y_zp=None, workspace=Non
     if y_zp is None:
         y_zp = torch.empty(1, dtype=torch.uint8, device=X.device)
     if workspace is None:
-        workspace = torch.empty(int(lib.ox_dynamic_quantize_workspace_bytes()), dtype=torch.uint8,
-                                device=X.device)
+        workspace = _scratch(int(lib.ox_dynamic_quantize_workspace_bytes()), X.device, stream)
     _check(lib.ox_dynamic_quantize_linear(X.numel(), _ptr(X), _ptr(Y), _ptr(y_scale), _ptr(y_zp),
                                           _ptr(workspace), workspace.numel(), _stream(stream)))
     return Y, y_scale, y_zp

@@ -129,3 +129,14 @@ def test_scratch_of_the_routed_layer(ox, stream, launched):
     scratch = made_of(ox, args[-3])
     assert scratch.numel() == args[-2] == ox.ox_moe_few_workspace_bytes(T, D, H, E, top)
     assert scratch.stream == launched
+
+
+@pytest.mark.parametrize("stream,launched", STREAMS, ids=IDS)
+def test_scratch_of_the_dynamic_quantisation(ox, stream, launched):
+    u8, f32 = torch.uint8, torch.float32
+    ox.ox_dynamic_quantize_linear(Tensor((9, 100), f32), Tensor((9, 100), u8), Tensor((1,), f32), Tensor((1,), u8), stream=stream)
+    (name, args), = ox.calls
+    assert name == "ox_dynamic_quantize_linear" and args[-1] == launched
+    scratch = made_of(ox, args[-3])
+    assert scratch.numel() == args[-2] == ox.lib.ox_dynamic_quantize_workspace_bytes()
+    assert scratch.stream == launched

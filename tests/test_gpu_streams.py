@@ -57,3 +57,24 @@ def test_the_default_stream_by_its_handle(ox):
         ox.ox_moe_few(*c, Y=Y, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(Y, want)
+
+
+def test_dynamic_quantisation_on_two_streams(ox):
+    g = torch.Generator(device="cuda").manual_seed(4)
+    X = [torch.randn((1 << 20,), generator=g, device="cuda") * k for k in (1.0, 30.0)]
+    want = [ox.ox_dynamic_quantize_linear(x) for x in X]
+    out = [[[torch.zeros_like(w) for w in ws] for _ in range(10)] for ws in want]
+    streams = [torch.cuda.Stream() for _ in X]
+    torch.cuda.synchronize()
+    for s in streams:
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(WAIT)
+    for i in range(10):
+        for x, o, s in zip(X, out, streams):
+            ox.ox_dynamic_quantize_linear(x, *o[i], stream=s)
+    over = [torch.full((1 << 14,), 255, dtype=torch.uint8, device="cuda") for _ in range(40)]
+    torch.cuda.synchronize()
+    for os_, ws in zip(out, want):
+        for o in os_:
+            assert all(torch.equal(a, b) for a, b in zip(o, ws))
+    assert all((o == 255).all().item() for o in over)
