@@ -7,6 +7,11 @@ only (shapes from tensors, ``data_ptr()``, the current HIP stream).  Every
 step of the computation runs in the library's own HIP kernels; PyTorch only
 supplies device memory and the stream.  There is no CPU fallback: if libox.so
 cannot be loaded, importing this package fails.
+
+``stream`` is torch's current one, unless a call names another (a torch stream
+or a raw handle): what the call makes is then that stream's memory, and the
+caller orders the inputs with it and keeps them, as with any work on a stream
+of its own.
 """
 import ctypes as C
 import os
@@ -176,6 +181,19 @@ def _scratch(nbytes, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _new_result(shape, dtype, device, stream):
+    """Memory for a result.  Where the launch is on another stream than torch's
+    current one it is the launch stream's, as _scratch's is, and torch knows that
+    the current stream uses it too: dropped, it stays until both have passed."""
+    torch = _torch()
+    if stream is None or device.type != "cuda" or _stream(stream) == (_F8 or _types())[4](device.index):
+        return torch.empty(shape, dtype=dtype or torch.bfloat16, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        t = torch.empty(shape, dtype=dtype or torch.bfloat16, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _dense(t, name):
     if t is not None and not t.is_contiguous():
         raise ValueError("%s must be contiguous (dense row-major)" % name)
@@ -202,7 +220,6 @@ def conv_out_hw(H, W, kH, kW, stride=(1, 1), pads=(0, 0, 0, 0), dilation=(1, 1))
 
 def ox_matmul_batched(A, B, C_out=None, stream=None):
     """ONNX MatMul: A [batch,M,K] x B [batch,K,N] (or [K,N] broadcast) -> [batch,M,N]."""
-    torch = _torch()
     _dense(A, "A")
     _dense(B, "B")
     batch, M, K = A.shape
@@ -213,7 +230,7 @@ def ox_matmul_batched(A, B, C_out=None, stream=None):
         bb, K2, N = B.shape
         sB = 0 if (bb == 1 and batch != 1) else K2 * N
     if C_out is None:
-        C_out = torch.empty((batch, M, N), dtype=A.dtype, device=A.device)
+        C_out = _new_result((batch, M, N), A.dtype, A.device, stream)
     _dense(C_out, "C")
     _check(lib.ox_matmul_batched(_dtype_code(A), batch, M, N, K, _ptr(A), M * K, _ptr(B), sB,
                                  _ptr(C_out), _stream(stream)))
@@ -237,7 +254,7 @@ def ox_gemm_fused(A, B, bias=None, alpha=1.0, beta=1.0, transA=False, transB=Fal
     else:
         out_dtype = A.dtype
     if Y is None:
-        Y = torch.empty((M, N), dtype=out_dtype, device=A.device)
+        Y = _new_result((M, N), out_dtype, A.device, stream)
     _check(lib.ox_gemm_fused(code, M, N, K, int(transA), int(transB), float(alpha), _ptr(A), _ptr(B),
                              float(beta), _ptr(bias), ACT[act], _ptr(Y), _ptr(int8_params),
                              _stream(stream)))
@@ -252,14 +269,13 @@ def ox_gemm_workspace_bytes(dtype, M, N, K):
 def ox_gemm_fused_ws(A, B, workspace, bias=None, alpha=1.0, beta=1.0, transA=False, transB=False,
                      act="none", Y=None, stream=None):
     """Float Gemm + activation with a split-K workspace (see ox_gemm_workspace_bytes)."""
-    torch = _torch()
     for t, n in ((A, "A"), (B, "B"), (bias, "bias"), (Y, "Y"), (workspace, "workspace")):
         _dense(t, n)
     M = A.shape[1] if transA else A.shape[0]
     K = A.shape[0] if transA else A.shape[1]
     N = B.shape[0] if transB else B.shape[1]
     if Y is None:
-        Y = torch.empty((M, N), dtype=A.dtype, device=A.device)
+        Y = _new_result((M, N), A.dtype, A.device, stream)
     nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.ox_gemm_fused_ws(_dtype_code(A), M, N, K, int(transA), int(transB), float(alpha),
                                 _ptr(A), _ptr(B), float(beta), _ptr(bias), ACT[act], _ptr(Y),
@@ -272,7 +288,6 @@ def ox_conv2d_fused(X, W, bias=None, stride=(1, 1), pads=(0, 0, 0, 0), dilation=
     """ONNX Conv + bias + activation (NCHW).  W is [M, C/group, kH, kW].
     workspace: optional device tensor of >= ox_conv2d_workspace_bytes bytes
     (enables split-K; goes through ox_conv2d_fused_ws)."""
-    torch = _torch()
     for t, n in ((X, "X"), (W, "W"), (bias, "bias"), (Y, "Y")):
         _dense(t, n)
     N, Cin, H, Wd = X.shape
@@ -280,7 +295,7 @@ def ox_conv2d_fused(X, W, bias=None, stride=(1, 1), pads=(0, 0, 0, 0), dilation=
     d = conv_desc(N, Cin, H, Wd, M, kH, kW, stride, pads, dilation, group)
     if Y is None:
         ho, wo = conv_out_hw(H, Wd, kH, kW, stride, pads, dilation)
-        Y = torch.empty((N, M, max(ho, 0), max(wo, 0)), dtype=X.dtype, device=X.device)
+        Y = _new_result((N, M, max(ho, 0), max(wo, 0)), X.dtype, X.device, stream)
     if workspace is not None:
         _dense(workspace, "workspace")
         nbytes = workspace.numel() * workspace.element_size()
@@ -296,7 +311,6 @@ def ox_conv2d_fused_res(X, W, R, bias=None, stride=(1, 1), pads=(0, 0, 0, 0), di
                         group=1, act="none", Y=None, stream=None, workspace=None):
     """ONNX Conv + bias + residual R (the output's shape) + activation, fused:
     Y = act(conv(X, W) + bias + R).  Y may be R itself (in place)."""
-    torch = _torch()
     for t, n in ((X, "X"), (W, "W"), (R, "R"), (bias, "bias"), (Y, "Y")):
         _dense(t, n)
     N, Cin, H, Wd = X.shape
@@ -304,7 +318,7 @@ def ox_conv2d_fused_res(X, W, R, bias=None, stride=(1, 1), pads=(0, 0, 0, 0), di
     d = conv_desc(N, Cin, H, Wd, M, kH, kW, stride, pads, dilation, group)
     if Y is None:
         ho, wo = conv_out_hw(H, Wd, kH, kW, stride, pads, dilation)
-        Y = torch.empty((N, M, max(ho, 0), max(wo, 0)), dtype=X.dtype, device=X.device)
+        Y = _new_result((N, M, max(ho, 0), max(wo, 0)), X.dtype, X.device, stream)
     nbytes = 0
     if workspace is not None:
         _dense(workspace, "workspace")
@@ -325,7 +339,7 @@ def ox_matmul_nbits(A, B, scales, K, zero_points=None, bias=None, Y=None, stream
     M = A.shape[0]
     N = B.shape[0]
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        Y = _new_result((M, N), torch.bfloat16, A.device, stream)
     _check(lib.ox_matmul_nbits(OX_BF16, M, N, K, 4, 32, _ptr(A), _ptr(B), _ptr(scales),
                                _ptr(zero_points), _ptr(bias), _ptr(Y), _stream(stream)))
     return Y
@@ -376,11 +390,6 @@ def _refuse_f8(A, a_scales, B, b_scales, want_a, want_b):
     return _shape_error("b_scales", b_scales, want_b)
 
 
-def _new_result(shape, dtype, device):
-    torch = _torch()
-    return torch.empty(shape, dtype=dtype or torch.bfloat16, device=device)
-
-
 def _check_bias(bias, shape, Y):
     if bias.shape != shape:
         raise _shape_error("bias", bias, shape)
@@ -407,13 +416,13 @@ def ox_quantize_fp8(X, index=None, block_rows=1, Q=None, scales=None, stream=Non
         R, at = index.numel(), index.data_ptr()
     shape = (kb, R) if block_rows == 1 else ((R + 127) >> 7, kb)
     if Q is None:
-        Q = _new_result((R, K), f8, X.device)
+        Q = _new_result((R, K), f8, X.device, stream)
     elif Q.shape != (R, K):
         raise _shape_error("Q", Q, (R, K))
     elif Q.dtype != f8 and Q.dtype != u8:
         raise TypeError("Q must be float8_e4m3fn or uint8")
     if scales is None:
-        scales = _new_result(shape, f32, X.device)
+        scales = _new_result(shape, f32, X.device, stream)
     elif scales.shape != shape:
         raise _shape_error("scales", scales, shape)
     elif scales.dtype != f32:
@@ -445,7 +454,7 @@ def ox_gemm_fp8(A, a_scales, B, b_scales, bias=None, act="none", Y=None, out_dty
             and b_scales.dtype == f32 and a_scales.shape == (kb, M) and b_scales.shape == ((N + 127) >> 7, kb)):
         raise _refuse_f8(A, a_scales, B, b_scales, (kb, M), ((N + 127) >> 7, kb))
     if Y is None:
-        Y = _new_result((M, N), out_dtype, A.device)
+        Y = _new_result((M, N), out_dtype, A.device, stream)
     elif Y.shape != (M, N):
         raise _shape_error("Y", Y, (M, N))
     if bias is not None:
@@ -487,7 +496,7 @@ def ox_gemm_grouped(A, B, offsets, bias=None, transB=True, act="none", Y=None, s
     _check_offsets(offsets, E, i32)
     dtype = A.dtype
     if Y is None:
-        Y = _new_result((T, N), dtype, A.device)
+        Y = _new_result((T, N), dtype, A.device, stream)
     elif Y.shape != (T, N):
         raise _shape_error("Y", Y, (T, N))
     if B.dtype != dtype or Y.dtype != dtype:
@@ -523,7 +532,7 @@ def ox_gemm_grouped_fp8(A, a_scales, B, b_scales, offsets, bias=None, act="none"
             and b_scales.dtype == f32 and a_scales.shape == (kb, T) and b_scales.shape == (E, (N + 127) >> 7, kb)):
         raise _refuse_f8(A, a_scales, B, b_scales, (kb, T), (E, (N + 127) >> 7, kb))
     if Y is None:
-        Y = _new_result((T, N), out_dtype, A.device)
+        Y = _new_result((T, N), out_dtype, A.device, stream)
     elif Y.shape != (T, N):
         raise _shape_error("Y", Y, (T, N))
     if bias is not None:
@@ -560,13 +569,13 @@ def ox_quantize_i8(X, Q=None, scales=None, stream=None):
     i8 = (_I8 or _small_types())[0]
     rows, K = X.shape
     if Q is None:
-        Q = _new_result((rows, K), i8, X.device)
+        Q = _new_result((rows, K), i8, X.device, stream)
     elif Q.shape != (rows, K):
         raise _shape_error("Q", Q, (rows, K))
     elif Q.dtype != i8:
         raise TypeError("Q must be int8")
     if scales is None:
-        scales = _new_result((rows,), f32, X.device)
+        scales = _new_result((rows,), f32, X.device, stream)
     elif scales.shape != (rows,):
         raise _shape_error("scales", scales, (rows,))
     elif scales.dtype != f32:
@@ -602,7 +611,7 @@ def ox_gemm_i8(A, a_scales, B, b_scales, bias=None, act="none", Y=None, out_dtyp
     if b_scales.shape != (N,):
         raise _shape_error("b_scales", b_scales, (N,))
     if Y is None:
-        Y = _new_result((M, N), out_dtype, A.device)
+        Y = _new_result((M, N), out_dtype, A.device, stream)
     elif Y.shape != (M, N):
         raise _shape_error("Y", Y, (M, N))
     if bias is not None:
@@ -643,7 +652,7 @@ def ox_rmsnorm(X, gamma=None, residual=None, eps=1e-6, out="same", Y=None, scale
     else:
         raise ValueError("out must be 'same', 'fp8' or 'i8'")
     if Y is None:
-        Y = _new_result((rows, K), want, X.device)
+        Y = _new_result((rows, K), want, X.device, stream)
     elif Y.shape != (rows, K):
         raise _shape_error("Y", Y, (rows, K))
     elif Y.dtype != want and not (out == "fp8" and Y.dtype == u8):
@@ -652,7 +661,7 @@ def ox_rmsnorm(X, gamma=None, residual=None, eps=1e-6, out="same", Y=None, scale
         if scales is not None:
             raise ValueError("scales go with out='fp8' or 'i8'")
     elif scales is None:
-        scales = _new_result(shape, f32, X.device)
+        scales = _new_result(shape, f32, X.device, stream)
     elif scales.shape != shape:
         raise _shape_error("scales", scales, shape)
     elif scales.dtype != f32:
@@ -661,7 +670,7 @@ def ox_rmsnorm(X, gamma=None, residual=None, eps=1e-6, out="same", Y=None, scale
         raise _shape_error("gamma", gamma, (K,)) if gamma.shape != (K,) else TypeError("gamma is %s, X %s" % (gamma.dtype, dtype))
     if residual is not None:
         if S is None:
-            S = _new_result((rows, K), dtype, X.device)
+            S = _new_result((rows, K), dtype, X.device, stream)
         elif S.shape != (rows, K):
             raise _shape_error("S", S, (rows, K))
         if residual.shape != (rows, K):
@@ -733,7 +742,7 @@ def ox_moe_few(X, scores, W1, W2, top, w1_scales=None, w2_scales=None, b1=None, 
     else:
         raise TypeError("W1 and W2 are %s, X %s" % (W1.dtype, dtype))
     if Y is None:
-        Y = _new_result((T, D), dtype, X.device)
+        Y = _new_result((T, D), dtype, X.device, stream)
     elif Y.shape != (T, D):
         raise _shape_error("Y", Y, (T, D))
     elif Y.dtype != dtype:
@@ -771,11 +780,11 @@ def ox_dynamic_quantize_linear(X, Y=None, y_scale=None, y_zp=None, workspace=Non
     if X.dtype != torch.float32:
         raise TypeError("X must be float32")
     if Y is None:
-        Y = torch.empty(X.shape, dtype=torch.uint8, device=X.device)
+        Y = _new_result(X.shape, torch.uint8, X.device, stream)
     if y_scale is None:
-        y_scale = torch.empty(1, dtype=torch.float32, device=X.device)
+        y_scale = _new_result((1,), torch.float32, X.device, stream)
     if y_zp is None:
-        y_zp = torch.empty(1, dtype=torch.uint8, device=X.device)
+        y_zp = _new_result((1,), torch.uint8, X.device, stream)
     if workspace is None:
         workspace = _scratch(int(lib.ox_dynamic_quantize_workspace_bytes()), X.device, stream)
     _check(lib.ox_dynamic_quantize_linear(X.numel(), _ptr(X), _ptr(Y), _ptr(y_scale), _ptr(y_zp),
@@ -786,13 +795,12 @@ def ox_dynamic_quantize_linear(X, Y=None, y_scale=None, y_zp=None, workspace=Non
 def ox_batchnorm_act(X, gamma, beta, mean, var, eps=1e-5, act="none", Y=None, stream=None):
     """ONNX BatchNormalization (inference) + activation on NCHW X; the four
     parameters are fp32 device tensors [C].  Y may be X (in place)."""
-    torch = _torch()
     for t, n in ((X, "X"), (gamma, "gamma"), (beta, "beta"), (mean, "mean"), (var, "var"), (Y, "Y")):
         _dense(t, n)
     N, Cc = X.shape[:2]
     HW = X.numel() // max(1, N * Cc)
     if Y is None:
-        Y = torch.empty_like(X)
+        Y = _new_result(X.shape, X.dtype, X.device, stream)
     _check(lib.ox_batchnorm_act(_dtype_code(X), N, Cc, HW, _ptr(X), _ptr(gamma), _ptr(beta), _ptr(mean),
                                 _ptr(var), float(eps), ACT[act], _ptr(Y), _stream(stream)))
     return Y
@@ -800,27 +808,25 @@ def ox_batchnorm_act(X, gamma, beta, mean, var, eps=1e-5, act="none", Y=None, st
 
 def ox_maxpool2d(X, kernel, stride=(1, 1), pads=(0, 0, 0, 0), dilation=(1, 1), Y=None, stream=None):
     """ONNX MaxPool (NCHW, ceil_mode 0); pads (top, left, bottom, right)."""
-    torch = _torch()
     _dense(X, "X")
     _dense(Y, "Y")
     N, Cc, H, W = X.shape
     d = conv_desc(N, Cc, H, W, Cc, kernel[0], kernel[1], stride, pads, dilation, 1)
     if Y is None:
         ho, wo = conv_out_hw(H, W, kernel[0], kernel[1], stride, pads, dilation)
-        Y = torch.empty((N, Cc, max(ho, 0), max(wo, 0)), dtype=X.dtype, device=X.device)
+        Y = _new_result((N, Cc, max(ho, 0), max(wo, 0)), X.dtype, X.device, stream)
     _check(lib.ox_maxpool2d(_dtype_code(X), C.byref(d), _ptr(X), _ptr(Y), _stream(stream)))
     return Y
 
 
 def ox_global_avgpool(X, Y=None, stream=None):
     """ONNX GlobalAveragePool: [N, C, H, W] -> [N, C, 1, 1]."""
-    torch = _torch()
     _dense(X, "X")
     _dense(Y, "Y")
     N, Cc = X.shape[:2]
     HW = X.numel() // max(1, N * Cc)
     if Y is None:
-        Y = torch.empty((N, Cc, 1, 1), dtype=X.dtype, device=X.device)
+        Y = _new_result((N, Cc, 1, 1), X.dtype, X.device, stream)
     _check(lib.ox_global_avgpool(_dtype_code(X), N, Cc, HW, _ptr(X), _ptr(Y), _stream(stream)))
     return Y
 
@@ -830,7 +836,6 @@ def ox_conv2d_fused_packed(X, Wp, bias=None, stride=(1, 1), pads=(0, 0, 0, 0), d
                            workspace=None):
     """ox_conv2d_fused with weights packed by ox_conv2d_pack_weights (a device
     tensor of the packed bytes' dtype).  M: output channels; kernel: (kH, kW)."""
-    torch = _torch()
     for t, n in ((X, "X"), (Wp, "Wp"), (bias, "bias"), (Y, "Y")):
         _dense(t, n)
     N, Cin, H, Wd = X.shape
@@ -840,7 +845,7 @@ def ox_conv2d_fused_packed(X, Wp, bias=None, stride=(1, 1), pads=(0, 0, 0, 0), d
     d = conv_desc(N, Cin, H, Wd, M, kH, kW, stride, pads, dilation, group)
     if Y is None:
         ho, wo = conv_out_hw(H, Wd, kH, kW, stride, pads, dilation)
-        Y = torch.empty((N, M, max(ho, 0), max(wo, 0)), dtype=X.dtype, device=X.device)
+        Y = _new_result((N, M, max(ho, 0), max(wo, 0)), X.dtype, X.device, stream)
     if workspace is not None:
         _dense(workspace, "workspace")
         nbytes = workspace.numel() * workspace.element_size()
@@ -918,9 +923,8 @@ def ox_conv2d_int8(Xq, Wq, int8_params, y_type="i8", stride=(1, 1), pads=(0, 0, 
     yt = OX_I32 if y_type == "i32" else OX_I8
     if Y is None:
         ho, wo = conv_out_hw(H, Wd, kH, kW, stride, pads, dilation)
-        Y = torch.empty((N, M, max(ho, 0), max(wo, 0)),
-                        dtype=torch.int32 if yt == OX_I32 else
-                        (torch.uint8 if y_type == "u8" else torch.int8), device=Xq.device)
+        Y = _new_result((N, M, max(ho, 0), max(wo, 0)),
+                        torch.int32 if yt == OX_I32 else torch.uint8 if y_type == "u8" else torch.int8, Xq.device, stream)
     _check(lib.ox_conv2d_int8(C.byref(d), _ptr(Xq), _ptr(Wq), _ptr(int8_params), yt, _ptr(Y),
                               _stream(stream)))
     return Y

@@ -140,3 +140,55 @@ def test_scratch_of_the_dynamic_quantisation(ox, stream, launched):
     scratch = made_of(ox, args[-3])
     assert scratch.numel() == args[-2] == ox.lib.ox_dynamic_quantize_workspace_bytes()
     assert scratch.stream == launched
+
+
+def calls(ox, stream):
+    """One call of every entry point that makes its results."""
+    f32, bf, i8, u8, i32, f8 = torch.float32, torch.bfloat16, torch.int8, torch.uint8, torch.int32, torch.float8_e4m3fn
+    T, kw = Tensor, dict(stream=stream)
+    X4, W4 = T((2, 8, 6, 6), bf), T((16, 8, 3, 3), bf)
+    c = [T((8,), f32) for _ in range(4)]
+    A8, B8, kb = T((4, 256), f8), T((64, 256), f8), T((2, 4), f32)
+    Ai, Bi, si, sb = T((4, 256), i8), T((64, 256), i8), T((4,), f32), T((64,), f32)
+    return {
+        "matmul_batched": lambda: ox.ox_matmul_batched(T((2, 4, 8), f32), T((8, 6), f32), **kw),
+        "gemm_fused": lambda: ox.ox_gemm_fused(T((4, 8), f32), T((8, 6), f32), **kw),
+        "gemm_fused_i8": lambda: ox.ox_gemm_fused(T((4, 8), i8), T((6, 8), i8), transB=True, **kw),
+        "gemm_fused_ws": lambda: ox.ox_gemm_fused_ws(T((4, 8), f32), T((8, 6), f32), None, **kw),
+        "conv2d_fused": lambda: ox.ox_conv2d_fused(X4, W4, **kw),
+        "conv2d_fused_res": lambda: ox.ox_conv2d_fused_res(X4, W4, T((2, 16, 4, 4), bf), **kw),
+        "conv2d_fused_packed": lambda: ox.ox_conv2d_fused_packed(X4, T((16 * 8 * 9,), bf), **kw),
+        "conv2d_int8": lambda: ox.ox_conv2d_int8(T((2, 8, 6, 6), i8), T((16, 8, 3, 3), i8), T((64,), u8), **kw),
+        "matmul_nbits": lambda: ox.ox_matmul_nbits(T((4, 64), bf), T((6, 2, 16), u8), T((6, 2), f32), 64, **kw),
+        "dynamic_quantize_linear": lambda: ox.ox_dynamic_quantize_linear(T((9, 10), f32), workspace=T((8192,), u8), **kw),
+        "batchnorm_act": lambda: ox.ox_batchnorm_act(X4, *c, **kw),
+        "maxpool2d": lambda: ox.ox_maxpool2d(X4, (2, 2), **kw),
+        "global_avgpool": lambda: ox.ox_global_avgpool(X4, **kw),
+        "quantize_fp8": lambda: ox.ox_quantize_fp8(T((4, 256), bf), **kw),
+        "gemm_fp8": lambda: ox.ox_gemm_fp8(A8, kb, B8, T((1, 2), f32), **kw),
+        "gemm_grouped": lambda: ox.ox_gemm_grouped(T((4, 8), bf), T((3, 6, 8), bf), T((4,), i32), **kw),
+        "gemm_grouped_fp8": lambda: ox.ox_gemm_grouped_fp8(A8, kb, T((3, 64, 256), f8), T((3, 1, 2), f32), T((4,), i32), **kw),
+        "quantize_i8": lambda: ox.ox_quantize_i8(T((4, 256), bf), **kw),
+        "gemm_i8": lambda: ox.ox_gemm_i8(Ai, si, Bi, sb, **kw),
+        "rmsnorm": lambda: ox.ox_rmsnorm(T((4, 256), bf), residual=T((4, 256), bf), out="fp8", **kw),
+        "moe_few": lambda: ox.ox_moe_few(T((4, 64), bf), T((4, 8), f32), T((8, 192, 64), bf), T((8, 64, 96), bf), 2,
+                                         workspace=T((1 << 22,), u8), **kw),
+    }
+
+
+@pytest.mark.parametrize("stream,launched", STREAMS, ids=IDS)
+def test_results(ox, stream, launched):
+    """A result is of the launch's stream, so that nothing else still uses its
+    memory, and known to be used by the caller's stream too, so that nothing
+    gets it while that one still reads."""
+    makes = {"dynamic_quantize_linear": 3, "quantize_fp8": 2, "quantize_i8": 2, "rmsnorm": 3}
+    for name, call in calls(ox, stream).items():
+        ox.calls.clear()
+        ox.fake.made.clear()
+        call()
+        (entry, args), = ox.calls
+        assert entry.startswith("ox_" + name.replace("_i8", "")) and args[-1] == launched, name
+        assert len(ox.fake.made) == makes.get(name, 1), name
+        for t in ox.fake.made:
+            assert t.place in args and t.stream == launched, name
+            assert t.recorded == ([] if launched == CURRENT else [CURRENT]), name

@@ -78,3 +78,30 @@ def test_dynamic_quantisation_on_two_streams(ox):
         for o in os_:
             assert all(torch.equal(a, b) for a, b in zip(o, ws))
     assert all((o == 255).all().item() for o in over)
+
+
+def test_results_on_another_stream_are_of_memory_that_nothing_uses(ox):
+    """Memory that the current stream gave back and still reads is not the next
+    result's on another stream, and a result that is dropped at once is not the
+    current stream's next tensor while the launch still writes it."""
+    rows, K = 512, 2048
+    g = torch.Generator(device="cuda").manual_seed(5)
+    X, R = (torch.randn((rows, K), generator=g, device="cuda").bfloat16() for _ in range(2))
+    want = ox.ox_rmsnorm(X, residual=R, out="i8")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(WAIT)
+    given_back = [torch.full((rows, K), 3.0, device="cuda").bfloat16() for _ in range(8)]
+    doubled = [2 * t for t in given_back]
+    del given_back
+    early = [ox.ox_rmsnorm(X, residual=R, out="i8", stream=side) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all((d == 6.0).all().item() for d in doubled)
+    assert all(torch.equal(a, b) for e in early for a, b in zip(e, want))
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(WAIT)
+    for handle in (side, side.cuda_stream):
+        ox.ox_rmsnorm(X, residual=R, out="i8", stream=handle)
+    over = [torch.full((rows, K), 7.0, device="cuda").bfloat16() for _ in range(12)]
+    torch.cuda.synchronize()
+    assert all((o == 7.0).all().item() for o in over)
