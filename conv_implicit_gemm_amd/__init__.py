@@ -352,16 +352,27 @@ def ox_matmul_nbits(A, B, scales, K, zero_points=None, bias=None, Y=None, stream
 
 _F8 = None        # torch's types, looked up once: (float8_e4m3fn, uint8, float32, int32, raw stream function)
 _I8 = None        # int8 and bfloat16, likewise
+_current_device = None      # torch's lookup of the current GPU, set before _F8
 
 
 def _types():
-    global _F8
+    global _F8, _current_device
     if _F8 is None:
         torch = _torch()
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _F8 = (torch.float8_e4m3fn, torch.uint8, torch.float32, torch.int32,
                raw or (lambda device: _stream(None)))
     return _F8
+
+
+def _launch_on(device, call):
+    """The call with `device` as the current GPU: a launch on a default stream,
+    whose handle is 0 for every GPU, goes to the current one."""
+    def there(*args):
+        with _torch().cuda.device(device):
+            return call(*args)
+    return there
 
 
 def _shape_error(name, t, want):
@@ -433,8 +444,9 @@ def ox_quantize_fp8(X, index=None, block_rows=1, Q=None, scales=None, stream=Non
             and Q.is_contiguous() and scales.is_contiguous()
             and (index is None or (index.get_device() == dev and index.is_contiguous()))):
         raise _refuse_memory(("X", "Q", "scales", "index"), X, Q, scales, index)
-    st = lib.ox_quantize_fp8(code, rows, K, X.data_ptr(), R, at, block_rows, Q.data_ptr(), scales.data_ptr(),
-                             raw(dev) if stream is None else _stream(stream))
+    launch = lib.ox_quantize_fp8 if dev == _current_device() else _launch_on(dev, lib.ox_quantize_fp8)
+    st = launch(code, rows, K, X.data_ptr(), R, at, block_rows, Q.data_ptr(), scales.data_ptr(),
+                raw(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
     return Q, scales
@@ -466,9 +478,10 @@ def ox_gemm_fp8(A, a_scales, B, b_scales, bias=None, act="none", Y=None, out_dty
             and b_scales.is_contiguous() and Y.is_contiguous()
             and (bias is None or (bias.get_device() == dev and bias.is_contiguous()))):
         raise _refuse_memory(("A", "a_scales", "B", "b_scales", "Y", "bias"), A, a_scales, B, b_scales, Y, bias)
-    st = lib.ox_gemm_fp8(code, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(), b_scales.data_ptr(),
-                         None if bias is None else bias.data_ptr(), ACT[act], Y.data_ptr(),
-                         raw(dev) if stream is None else _stream(stream))
+    launch = lib.ox_gemm_fp8 if dev == _current_device() else _launch_on(dev, lib.ox_gemm_fp8)
+    st = launch(code, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(), b_scales.data_ptr(),
+                None if bias is None else bias.data_ptr(), ACT[act], Y.data_ptr(),
+                raw(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
     return Y
@@ -509,9 +522,10 @@ def ox_gemm_grouped(A, B, offsets, bias=None, transB=True, act="none", Y=None, s
             and A.is_contiguous() and B.is_contiguous() and offsets.is_contiguous() and Y.is_contiguous()
             and (bias is None or (bias.get_device() == dev and bias.is_contiguous()))):
         raise _refuse_memory(("A", "B", "offsets", "Y", "bias"), A, B, offsets, Y, bias)
-    st = lib.ox_gemm_grouped(code, T, N, K, E, 1 if transB else 0, A.data_ptr(), B.data_ptr(), offsets.data_ptr(),
-                             None if bias is None else bias.data_ptr(), ACT[act], Y.data_ptr(),
-                             raw(dev) if stream is None else _stream(stream))
+    launch = lib.ox_gemm_grouped if dev == _current_device() else _launch_on(dev, lib.ox_gemm_grouped)
+    st = launch(code, T, N, K, E, 1 if transB else 0, A.data_ptr(), B.data_ptr(), offsets.data_ptr(),
+                None if bias is None else bias.data_ptr(), ACT[act], Y.data_ptr(),
+                raw(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
     return Y
@@ -545,9 +559,10 @@ def ox_gemm_grouped_fp8(A, a_scales, B, b_scales, offsets, bias=None, act="none"
             and Y.is_contiguous() and (bias is None or (bias.get_device() == dev and bias.is_contiguous()))):
         raise _refuse_memory(("A", "a_scales", "B", "b_scales", "offsets", "Y", "bias"), A, a_scales, B, b_scales,
                              offsets, Y, bias)
-    st = lib.ox_gemm_grouped_fp8(code, T, N, K, E, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(),
-                                 b_scales.data_ptr(), offsets.data_ptr(), None if bias is None else bias.data_ptr(),
-                                 ACT[act], Y.data_ptr(), raw(dev) if stream is None else _stream(stream))
+    launch = lib.ox_gemm_grouped_fp8 if dev == _current_device() else _launch_on(dev, lib.ox_gemm_grouped_fp8)
+    st = launch(code, T, N, K, E, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(),
+                b_scales.data_ptr(), offsets.data_ptr(), None if bias is None else bias.data_ptr(),
+                ACT[act], Y.data_ptr(), raw(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
     return Y
@@ -585,8 +600,9 @@ def ox_quantize_i8(X, Q=None, scales=None, stream=None):
     if not (dev >= 0 and Q.get_device() == dev and scales.get_device() == dev and X.is_contiguous()
             and Q.is_contiguous() and scales.is_contiguous()):
         raise _refuse_memory(("X", "Q", "scales"), X, Q, scales)
-    st = lib.ox_quantize_i8(code, rows, K, X.data_ptr(), Q.data_ptr(), scales.data_ptr(),
-                            raw(dev) if stream is None else _stream(stream))
+    launch = lib.ox_quantize_i8 if dev == _current_device() else _launch_on(dev, lib.ox_quantize_i8)
+    st = launch(code, rows, K, X.data_ptr(), Q.data_ptr(), scales.data_ptr(),
+                raw(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
     return Q, scales
@@ -623,9 +639,10 @@ def ox_gemm_i8(A, a_scales, B, b_scales, bias=None, act="none", Y=None, out_dtyp
             and b_scales.is_contiguous() and Y.is_contiguous()
             and (bias is None or (bias.get_device() == dev and bias.is_contiguous()))):
         raise _refuse_memory(("A", "a_scales", "B", "b_scales", "Y", "bias"), A, a_scales, B, b_scales, Y, bias)
-    st = lib.ox_gemm_i8(code, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(), b_scales.data_ptr(),
-                        None if bias is None else bias.data_ptr(), ACT[act], Y.data_ptr(),
-                        raw(dev) if stream is None else _stream(stream))
+    launch = lib.ox_gemm_i8 if dev == _current_device() else _launch_on(dev, lib.ox_gemm_i8)
+    st = launch(code, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(), b_scales.data_ptr(),
+                None if bias is None else bias.data_ptr(), ACT[act], Y.data_ptr(),
+                raw(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
     return Y
@@ -686,10 +703,11 @@ def ox_rmsnorm(X, gamma=None, residual=None, eps=1e-6, out="same", Y=None, scale
             and (residual is None or (residual.get_device() == dev and residual.is_contiguous()
                                       and S.get_device() == dev and S.is_contiguous()))):
         raise _refuse_memory(("X", "Y", "scales", "gamma", "residual", "S"), X, Y, scales, gamma, residual, S)
-    st = lib.ox_rmsnorm(t, rows, K, X.data_ptr(), None if residual is None else residual.data_ptr(),
-                        None if gamma is None else gamma.data_ptr(), eps, None if S is None else S.data_ptr(), code,
-                        Y.data_ptr(), None if scales is None else scales.data_ptr(),
-                        raw(dev) if stream is None else _stream(stream))
+    launch = lib.ox_rmsnorm if dev == _current_device() else _launch_on(dev, lib.ox_rmsnorm)
+    st = launch(t, rows, K, X.data_ptr(), None if residual is None else residual.data_ptr(),
+                None if gamma is None else gamma.data_ptr(), eps, None if S is None else S.data_ptr(), code,
+                Y.data_ptr(), None if scales is None else scales.data_ptr(),
+                raw(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
     return Y, scales, S
@@ -762,11 +780,12 @@ def ox_moe_few(X, scores, W1, W2, top, w1_scales=None, w2_scales=None, b1=None, 
         if t is not None and (dev < 0 or t.get_device() != dev or not t.is_contiguous()):
             raise _refuse_memory(("X", "scores", "W1", "W2", "Y", "w1_scales", "w2_scales", "b1", "b2", "experts", "weights",
                                   "workspace"), X, scores, W1, W2, Y, w1_scales, w2_scales, b1, b2, experts, weights, workspace)
-    st = lib.ox_moe_few(code, w_code, T, D, H, E, top, X.data_ptr(), OX_F32 if scores.dtype == f32 else OX_BF16,
-                        scores.data_ptr(), 1 if renormalise else 0, W1.data_ptr(), _ptr(w1_scales), _ptr(b1), ACT[act],
-                        1 if gated else 0, W2.data_ptr(), _ptr(w2_scales), _ptr(b2), _ptr(experts), _ptr(weights),
-                        Y.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                        raw(dev) if stream is None else _stream(stream))
+    launch = lib.ox_moe_few if dev == _current_device() else _launch_on(dev, lib.ox_moe_few)
+    st = launch(code, w_code, T, D, H, E, top, X.data_ptr(), OX_F32 if scores.dtype == f32 else OX_BF16,
+                scores.data_ptr(), 1 if renormalise else 0, W1.data_ptr(), _ptr(w1_scales), _ptr(b1), ACT[act],
+                1 if gated else 0, W2.data_ptr(), _ptr(w2_scales), _ptr(b2), _ptr(experts), _ptr(weights),
+                Y.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                raw(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
     return Y

@@ -91,6 +91,7 @@ def ox():
     fake = Torch()
     mod._types()
     mod._F8 = mod._F8[:4] + (lambda device: fake.now[-1],)
+    mod._current_device = lambda: 0
     mod._torch = lambda: fake
     mod.fake, mod.calls, library = fake, [], mod.lib
 
@@ -192,3 +193,35 @@ def test_results(ox, stream, launched):
         for t in ox.fake.made:
             assert t.place in args and t.stream == launched, name
             assert t.recorded == ([] if launched == CURRENT else [CURRENT]), name
+
+
+FLAT = ["quantize_fp8", "gemm_fp8", "gemm_grouped", "gemm_grouped_fp8", "quantize_i8", "gemm_i8", "rmsnorm", "moe_few"]
+
+
+@pytest.mark.parametrize("current", [0, 1])
+@pytest.mark.parametrize("stream", [None, 9, 0])
+@pytest.mark.parametrize("name", FLAT)
+def test_tensors_on_another_gpu_than_the_current_one(ox, name, stream, current, monkeypatch):
+    """The calls that take tensors of any GPU launch with that GPU as the current
+    one: the default stream's handle, 0, names the current GPU's."""
+    at, of = [current], 1 - current
+
+    @contextlib.contextmanager
+    def device(index):
+        at.append(getattr(index, "index", index))
+        yield
+        at.pop()
+    monkeypatch.setattr(Tensor, "get_device", lambda t: of)
+    ox.fake.cuda.device = device
+    ox._current_device = lambda: at[-1]
+    seen = []
+
+    class Library:
+        def __getattr__(self, entry):
+            def call(*args):
+                seen.append((entry, at[-1]))
+                return 0
+            return call if not entry.endswith("_bytes") else lambda *args: 64
+    ox.lib = Library()
+    calls(ox, stream)[name]()
+    assert seen == [("ox_" + name, of)] and at == [current]
