@@ -655,8 +655,14 @@ __global__ __launch_bounds__(kMoeThreads, 2) void moe_down_kernel(const MoeArgs 
 #pragma unroll
           for (int f = 0; f < NF; ++f)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              acc[f][m][r] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc[f][m][r]), 0xB1, 0xf, 0xf, true));   // lane ^ 1
+            for (int r = 0; r < 4; ++r) {
+              // The low part's sum, of the next lane.  It is finite where the high
+              // part's is, or else met an infinite weight: that is the high part's to
+              // show, with h's sign (a low part of zero, or of the other sign, would
+              // make NaN of it).
+              const float low = __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc[f][m][r]), 0xB1, 0xf, 0xf, true));
+              acc[f][m][r] += __builtin_isfinite(low) ? low : 0.0f;
+            }
         }
         if (slot >= hi || i % PARTS != 0) continue;
         const float wt = rt.weight[slot];
