@@ -657,14 +657,15 @@ struct ExpertTileKernel {
         }
       }
   }
-  // int8: the columns' scales, as the biases
+  // int8: the columns' scales, as the biases; rows without columns (K = 0) have
+  // none to read
   __device__ __forceinline__ void load_scales(const Where& t, int wn, float (&sv)[NF][4]) const {
 #pragma unroll
     for (int j = 0; j < NF; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int n = col_of(wn, j, r);
-        sv[j][r] = Mm::INT && n < t.cols ? a.sb[(int64_t)t.e * a.N + t.n0 + n] : 0.0f;
+        sv[j][r] = Mm::INT && nk > 0 && n < t.cols ? a.sb[(int64_t)t.e * a.N + t.n0 + n] : 0.0f;
       }
   }
   template <int ACT>
@@ -886,7 +887,7 @@ struct ExpertTileKernel {
     load_scales(t, wn, sv);
 #pragma unroll
     for (int f = 0; f < MF; ++f)
-      sm[f] = Mm::INT ? a.sa[t.row0 + min(wm * TM + f * 16 + (int)(threadIdx.x & 15), t.rows - 1)] : 0.0f;
+      sm[f] = Mm::INT && nk > 0 ? a.sa[t.row0 + min(wm * TM + f * 16 + (int)(threadIdx.x & 15), t.rows - 1)] : 0.0f;
     wait_vmem();
     with_act(a.act, [&](auto act) { store<decltype(act)::value>(t, wm, wn, acc, bv, sv, sm); });
   }
@@ -1009,11 +1010,11 @@ __global__ __launch_bounds__(kStreamWaves * 64) void expert_stream_kernel(const 
     const int n = n0 + g * 4;
     if (!live || m >= hi || n >= a.N) continue;
     float v[4];
-    const float sm = Mm::INT ? a.sa[m] : 0.0f;
+    const float sm = Mm::INT && nk > 0 ? a.sa[m] : 0.0f;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float bv = 0.0f;
-      const float sv = Mm::INT && n + r < a.N ? a.sb[(int64_t)e * a.N + n + r] : 0.0f;
+      const float sv = Mm::INT && nk > 0 && n + r < a.N ? a.sb[(int64_t)e * a.N + n + r] : 0.0f;
       if (a.bias && n + r < a.N) {
         const int64_t at = (int64_t)e * a.N + n + r;
         bv = a.out_dt == DT_F32 ? ((const float*)a.bias)[at] : bf16_to_f32(((const uint16_t*)a.bias)[at]);

@@ -437,7 +437,8 @@ ox_status ox_gemm_fp8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const ui
  * t: the type of X, OX_F32 or OX_BF16; X: DEVICE [rows, K], K <= 65536 (a row
  * lies in registers; OX_ERR_UNSUPPORTED above); Q: DEVICE int8 [rows, K];
  * scales: DEVICE fp32 [rows].  2^26 rows or more, if short, can be too many
- * blocks for one launch (OX_ERR_UNSUPPORTED). */
+ * blocks for one launch (OX_ERR_UNSUPPORTED).  K = 0 enqueues nothing: such rows
+ * get no scale, and ox_gemm_i8 reads none. */
 ox_status ox_quantize_i8(ox_dtype t, int64_t rows, int64_t K, const void* X, int8_t* Q, float* scales,
                          void* stream);
 
@@ -448,7 +449,8 @@ ox_status ox_quantize_i8(ox_dtype t, int64_t rows, int64_t K, const void* X, int
  * b_scales DEVICE fp32 [N] (both as ox_quantize_i8 writes them).  The sums are
  * int32 and exact: K <= 131071 (OX_ERR_UNSUPPORTED above).  They are turned to
  * fp32, scaled and biased there and rounded once to y_type (OX_F32 or OX_BF16),
- * the type of Y DEVICE [M, N] and of bias DEVICE [N] or NULL. */
+ * the type of Y DEVICE [M, N] and of bias DEVICE [N] or NULL.  K = 0 writes
+ * act(bias), whatever the scales hold. */
 ox_status ox_gemm_i8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const int8_t* A, const float* a_scales,
                      const int8_t* B, const float* b_scales, const void* bias, ox_act act, void* Y, void* stream);
 
