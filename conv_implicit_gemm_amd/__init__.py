@@ -11,7 +11,8 @@ cannot be loaded, importing this package fails.
 ``stream`` is torch's current one, unless a call names another (a torch stream
 or a raw handle): what the call makes is then that stream's memory, and the
 caller orders the inputs with it and keeps them, as with any work on a stream
-of its own.
+of its own.  Tensors are on the current GPU; the e4m3, int8, norm and expert calls
+take another's too.
 """
 import ctypes as C
 import os
@@ -160,12 +161,18 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
+def _handle(stream):
+    """A stream's handle as a number, also of a pointer object."""
+    handle = _stream(stream)
+    return getattr(handle, "value", handle) or 0
+
+
 def _torch_stream(stream, device):
     """A stream or its raw handle as torch's allocator takes it."""
     cuda = _torch().cuda
     if isinstance(stream, cuda.Stream):
         return stream
-    handle = _stream(stream)
+    handle = _handle(stream)
     return cuda.ExternalStream(handle, device) if handle else cuda.default_stream(device)
 
 
@@ -186,7 +193,7 @@ def _new_result(shape, dtype, device, stream):
     current one it is the launch stream's, as _scratch's is, and torch knows that
     the current stream uses it too: dropped, it stays until both have passed."""
     torch = _torch()
-    if stream is None or device.type != "cuda" or _stream(stream) == (_F8 or _types())[4](device.index):
+    if stream is None or device.type != "cuda" or _handle(stream) == (_F8 or _types())[4](device.index):
         return torch.empty(shape, dtype=dtype or torch.bfloat16, device=device)
     with torch.cuda.stream(_torch_stream(stream, device)):
         t = torch.empty(shape, dtype=dtype or torch.bfloat16, device=device)

@@ -6,6 +6,7 @@ given back serves the next tensor of that stream, whose work comes behind, and
 may still be in use by kernels of any other stream.  So what a call makes for a
 launch has to be of the launch's stream."""
 import contextlib
+import ctypes
 import importlib.util
 import itertools
 import types
@@ -115,8 +116,15 @@ def made_of(ox, place):
     return found[0]
 
 
-STREAMS = [(None, CURRENT), (7, 7), (Stream(7), 7), (0, 0), (Stream(0), 0), (CURRENT, CURRENT), (Stream(CURRENT), CURRENT)]
-IDS = ["none", "handle", "object", "default-handle", "default-object", "current-handle", "current-object"]
+STREAMS = [(None, CURRENT), (7, 7), (Stream(7), 7), (0, 0), (Stream(0), 0), (CURRENT, CURRENT), (Stream(CURRENT), CURRENT),
+           (ctypes.c_void_p(7), 7), (ctypes.c_void_p(0), 0), (ctypes.c_void_p(CURRENT), CURRENT)]
+IDS = ["none", "handle", "object", "default-handle", "default-object", "current-handle", "current-object", "pointer",
+       "default-pointer", "current-pointer"]
+
+
+def handle_of(at):
+    """The handle that the library was given, as a number."""
+    return (at.value or 0) if isinstance(at, ctypes.c_void_p) else at
 
 
 @pytest.mark.parametrize("stream,launched", STREAMS, ids=IDS)
@@ -126,7 +134,7 @@ def test_scratch_of_the_routed_layer(ox, stream, launched):
     ox.ox_moe_few(Tensor((T, D), bf), Tensor((T, E), torch.float32), Tensor((E, 2 * H, D), bf), Tensor((E, D, H), bf), top,
                   Y=Tensor((T, D), bf), stream=stream)
     (name, args), = ox.calls
-    assert name == "ox_moe_few" and args[-1] == launched
+    assert name == "ox_moe_few" and handle_of(args[-1]) == launched
     scratch = made_of(ox, args[-3])
     assert scratch.numel() == args[-2] == ox.ox_moe_few_workspace_bytes(T, D, H, E, top)
     assert scratch.stream == launched
@@ -137,7 +145,7 @@ def test_scratch_of_the_dynamic_quantisation(ox, stream, launched):
     u8, f32 = torch.uint8, torch.float32
     ox.ox_dynamic_quantize_linear(Tensor((9, 100), f32), Tensor((9, 100), u8), Tensor((1,), f32), Tensor((1,), u8), stream=stream)
     (name, args), = ox.calls
-    assert name == "ox_dynamic_quantize_linear" and args[-1] == launched
+    assert name == "ox_dynamic_quantize_linear" and handle_of(args[-1]) == launched
     scratch = made_of(ox, args[-3])
     assert scratch.numel() == args[-2] == ox.lib.ox_dynamic_quantize_workspace_bytes()
     assert scratch.stream == launched
@@ -188,7 +196,7 @@ def test_results(ox, stream, launched):
         ox.fake.made.clear()
         call()
         (entry, args), = ox.calls
-        assert entry.startswith("ox_" + name.replace("_i8", "")) and args[-1] == launched, name
+        assert entry.startswith("ox_" + name.replace("_i8", "")) and handle_of(args[-1]) == launched, name
         assert len(ox.fake.made) == makes.get(name, 1), name
         for t in ox.fake.made:
             assert t.place in args and t.stream == launched, name
