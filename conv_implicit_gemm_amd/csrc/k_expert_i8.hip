@@ -6,7 +6,11 @@ namespace ox {
 
 namespace {
 
-// (xN: K divided over N groups of waves)
+// (xN: K divided over N groups of waves)  The estimates are for the choice, which
+// is within 4% of the fastest variant in 16 shapes from 1 x 4096 x 4096 to 8192^3.
+// A call takes up to 40% more: operands that come from memory, sizes that end
+// inside tiles and fp32 results are not in them (64x64x2: 1024 x 1024 x 2048 7.6
+// us, 6.7 by the table; 1000 x 1000 x 2000 8.8 to bf16, 9.8 to fp32 with biases).
 constexpr TileCost kTiles[] = {{"32x64", 32, 64, 4, 2.5, 0.31, 0.53},
                                {"64x64", 64, 64, 3, 2.5, 0.39, 0.59},
                                {"128x128", 128, 128, 2, 5.3, 0.71, 0.98},

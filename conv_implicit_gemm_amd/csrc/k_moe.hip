@@ -761,7 +761,7 @@ int launch_pair(MoeArgs& a, int64_t steps, hipStream_t s) {
 // still leaves every wave four steps: the tokens' pieces then serve twice as many
 // weights (64 tokens, 8 of 64 bf16 experts of 1024 x 2048: 174 us, 182 with two;
 // 4 of 32 e4m3 experts of 512 x 1024, one step a wave: 35.9 us, 30.5 with two).
-// Up to 16 tokens the weights alone bound it, and both widths take the same time.
+// Up to 16 tokens both widths take the same time.
 template <int FMT, int UF, int DF>
 int launch(MoeArgs& a, hipStream_t s) {
   const int64_t experts = a.E < a.T * a.top ? a.E : a.T * a.top;

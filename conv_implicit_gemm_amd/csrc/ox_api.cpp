@@ -1046,7 +1046,7 @@ ox_status ox_quantize_fp8(ox_dtype t, int64_t rows, int64_t K, const void* X, in
 
 namespace {
 
-// The sizes of the calls that hold a row in registers.
+// The sizes of the calls whose blocks hold whole rows.
 ox_status check_rows(const char* fn, int64_t rows, int64_t K) {
   if (rows < 0 || K < 0)
     return fail(OX_ERR_SHAPE, "%s: rows=%lld or K=%lld is negative", fn, (long long)rows, (long long)K);

@@ -322,7 +322,7 @@ int launch_quantize_fp8(const QuantF8Args& a, void* stream);
 // RMS norm of X (+ residual) with results of X's type, e4m3 codes (a scale per
 // 1 x 128 block) or int8 codes (a scale per row), and the int8 quantisation of
 // X's rows (X, Y and scales alone).
-constexpr int kMaxNormRow = 65536;   // a row lies in the registers of 1024 threads
+constexpr int kMaxNormRow = 65536;   // a row is held by 1024 threads at most, 64 elements each
 struct NormArgs {
   int rows, K;
   int dt;                  // X, residual, gamma, sum_out: DT_F32 or DT_BF16
@@ -360,7 +360,7 @@ struct MoeArgs {
   void* route;
   int* counters;           // [tiles]
   void* hidden;            // [T * top][ldh], bf16: twice (high and low parts)
-  float* partials;         // [tiles][S][T][32]
+  float* partials;         // [tiles][S][T][columns of a tile: 32 or 64]
   int64_t ldh;
   int tiles, S, slices, up_blocks;
 };

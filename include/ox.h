@@ -434,8 +434,8 @@ ox_status ox_gemm_fp8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const ui
  * per output channel.  An infinity gives +-127 and does not move the scale; a
  * row that holds a NaN gets a scale of NaN (no int8 code can say it, so what is
  * multiplied by the scale does) and the code 0 in its place.
- * t: the type of X, OX_F32 or OX_BF16; X: DEVICE [rows, K], K <= 65536 (a row
- * lies in registers; OX_ERR_UNSUPPORTED above); Q: DEVICE int8 [rows, K];
+ * t: the type of X, OX_F32 or OX_BF16; X: DEVICE [rows, K], K <= 65536 (a block
+ * of threads holds a row; OX_ERR_UNSUPPORTED above); Q: DEVICE int8 [rows, K];
  * scales: DEVICE fp32 [rows].  2^26 rows or more, if short, can be too many
  * blocks for one launch (OX_ERR_UNSUPPORTED).  K = 0 enqueues nothing: such rows
  * get no scale, and ox_gemm_i8 reads none. */
@@ -457,7 +457,8 @@ ox_status ox_gemm_i8(ox_dtype y_type, int64_t M, int64_t N, int64_t K, const int
 /* RMS norm of rows, with the residual's addition in front and 8-bit results
  * with scales behind, for the products above:
  *   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * gamma
- * in fp32; the norm is that of the fp32 sum.
+ * in fp32; the norm is that of the fp32 sum, and s * gamma, which is formed
+ * first, has to stay inside fp32's normal range where y does.
  * t: OX_F32 or OX_BF16, the type of X, residual, sum_out DEVICE [rows, K] and
  * gamma DEVICE [K].  residual NULL: s = x; gamma NULL: ones.  sum_out: s,
  * rounded once, for the next residual (NULL: not written; needs a residual).
