@@ -182,7 +182,7 @@ def _scratch(nbytes, device, stream):
     whose next kernels run behind these, and gives out none that another
     stream's kernels may still be using."""
     torch = _torch()
-    if stream is None:
+    if stream is None or device.type != "cuda":
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     with torch.cuda.stream(_torch_stream(stream, device)):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)

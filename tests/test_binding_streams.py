@@ -233,3 +233,13 @@ def test_tensors_on_another_gpu_than_the_current_one(ox, name, stream, current, 
     ox.lib = Library()
     calls(ox, stream)[name]()
     assert seen == [("ox_" + name, of)] and at == [current]
+
+
+def test_host_tensors_are_refused_whatever_the_stream():
+    import conv_implicit_gemm_amd as real
+    X, s, W1, W2 = torch.zeros(4, 64), torch.zeros(4, 8), torch.zeros(8, 192, 64), torch.zeros(8, 64, 96)
+    for stream in (None, 0, 7):
+        for call in (lambda: real.ox_moe_few(X, s, W1, W2, 2, stream=stream), lambda: real.ox_rmsnorm(X, out="i8", stream=stream),
+                     lambda: real.ox_quantize_i8(X, stream=stream)):
+            with pytest.raises(ValueError, match="GPU"):
+                call()
